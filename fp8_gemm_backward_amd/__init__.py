@@ -8,7 +8,10 @@ fallback, and importing this package fails if the library is not built
 (`python fp8_gemm_backward_amd/build.py`).
 
 Formats (see include/lp.h): "bf16", "mxfp4", "nvfp4", "fp8_b128", "mxfp8",
-and the per-tensor scaled "fp8t_e4m3", "fp8t_e5m2".
+the per-tensor scaled "fp8t_e4m3", "fp8t_e5m2", and "fp8_r128" (E4M3 with an
+fp32 scale per run of 128, the counterpart of an "fp8_b128" weight in FP8
+products).  include/lp_train.h declares the quantizers of the last two, the
+forwards that quantize their own input, and the AdamW step.
 """
 from __future__ import annotations
 
@@ -24,7 +27,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "liblp.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "lp.h")
 
-FMT = {"bf16": 0, "mxfp4": 1, "nvfp4": 2, "fp8_b128": 3, "mxfp8": 4, "fp8t_e4m3": 5, "fp8t_e5m2": 6}
+FMT = {"bf16": 0, "mxfp4": 1, "nvfp4": 2, "fp8_b128": 3, "mxfp8": 4, "fp8t_e4m3": 5, "fp8t_e5m2": 6, "fp8_r128": 8}
 STATUS = {0: "LP_OK", 1: "LP_ERR_NULL", 2: "LP_ERR_SHAPE", 3: "LP_ERR_FORMAT", 4: "LP_ERR_ALIGN",
           5: "LP_ERR_HIP"}
 
@@ -63,11 +66,20 @@ def _load() -> ctypes.CDLL:
     lib.lp_tensor_quant_delayed.argtypes = [v, i64, i32, v, i32, i32, i32, v, v, v]
     lib.lp_linear_fwd.argtypes = [P, P, v, v]
     lib.lp_grouped_fwd.argtypes = [P, P, v, i64, v, v]
+    lib.lp_r128_quant.argtypes = [v, i64, i64, i64, i32, v, i64, v, v, v]
+    lib.lp_r128_quant_dual.argtypes = [v, i64, i64, i64, v, i64, v, v, v, v, v]
+    lib.lp_b128_quant.argtypes = [v, i64, i64, i64, v, v, v]
+    lib.lp_linear_fwd_dyn.argtypes = [v, i64, P, v, v, v, v]
+    lib.lp_grouped_fwd_dyn.argtypes = [v, i64, P, v, i64, v, v, v, v]
+    f64 = ctypes.c_double
+    lib.lp_adamw.argtypes = [v, i64, i32, i32, i32, f64, f64, f64, f64, i64, v, v]
     lib.lp_status_string.argtypes = [i32]
     lib.lp_status_string.restype = ctypes.c_char_p
     for f in ("lp_dequant", "lp_mx_quant", "lp_mx_quant_dual", "lp_linear_bwd", "lp_grouped_bwd",
               "lp_linear_bwd_workspace", "lp_linear_bwd_ws", "lp_linear_bwd_noalloc", "lp_grouped_dx_deferred", "lp_tensor_amax", "lp_tensor_quant",
-              "lp_scale_from_history", "lp_linear_fwd", "lp_grouped_fwd", "lp_tensor_quant_delayed"):
+              "lp_scale_from_history", "lp_linear_fwd", "lp_grouped_fwd", "lp_tensor_quant_delayed",
+              "lp_r128_quant", "lp_r128_quant_dual", "lp_b128_quant", "lp_linear_fwd_dyn", "lp_grouped_fwd_dyn",
+              "lp_adamw"):
         getattr(lib, f).restype = ctypes.c_int32
     return lib
 
@@ -75,7 +87,8 @@ def _load() -> ctypes.CDLL:
 lib = _load()
 
 
-_CODE_BITS = {"bf16": 16, "mxfp4": 4, "nvfp4": 4, "fp8_b128": 8, "mxfp8": 8, "fp8t_e4m3": 8, "fp8t_e5m2": 8}
+_CODE_BITS = {"bf16": 16, "mxfp4": 4, "nvfp4": 4, "fp8_b128": 8, "mxfp8": 8, "fp8t_e4m3": 8, "fp8t_e5m2": 8,
+              "fp8_r128": 8}
 
 
 def _scale_bytes(fmt: str, axis: int, b: int, r: int, c: int) -> int:
@@ -88,6 +101,8 @@ def _scale_bytes(fmt: str, axis: int, b: int, r: int, c: int) -> int:
         return b * r * (c // 16)
     if fmt == "fp8_b128":
         return b * (-(-r // 128)) * (-(-c // 128)) * 4
+    if fmt == "fp8_r128":
+        return 4 * (b * (-(-c // 128)) * r if axis == -1 else b * (-(-r // 128)) * c)
     return 0
 
 
@@ -444,3 +459,192 @@ def lp_grouped_fwd(x: QTensor, w: QTensor, offsets: torch.Tensor, y: Optional[to
 
 def lp_status_string(status: int) -> str:
     return lib.lp_status_string(status).decode()
+
+
+# ---------------------------------------------------------------- include/lp_train.h
+
+def _shape3(src: torch.Tensor) -> tuple:
+    return tuple(src.shape) if src.dim() == 3 else (1,) + tuple(src.shape)
+
+
+def _runs(rows: int, offsets: Optional[torch.Tensor]) -> int:
+    """Token runs of `rows` rows: per group when there are offsets."""
+    if offsets is None:
+        return -(-rows // 128)
+    _device(offsets, "offsets", 4 * offsets.numel(), torch.int32)
+    return rows // 128 + offsets.numel()
+
+
+def _offsets(offsets: Optional[torch.Tensor]) -> tuple:
+    return (None, 0) if offsets is None else (offsets.data_ptr(), offsets.numel())
+
+
+def lp_r128_quant(src: torch.Tensor, axis: int = -1, offsets: Optional[torch.Tensor] = None, stream=None) -> QTensor:
+    """Quantize a bf16 tensor [batch, rows, cols] (or [rows, cols]) to
+    "fp8_r128" along `axis` (-1 or -2).  offsets (axis -2): int32 cumulative
+    group ends; runs restart at every group's first row."""
+    b, r, c = shape = _shape3(src)
+    dev = src.device
+    codes = torch.empty(shape, dtype=torch.uint8, device=dev)
+    scales = torch.empty((b, -(-c // 128), r) if axis == -1 else (b, _runs(r, offsets), c), dtype=torch.float32,
+                         device=dev)
+    _device(src, "src", 2 * b * r * c, torch.bfloat16)
+    _check(lib.lp_r128_quant(src.data_ptr(), b, r, c, axis, *_offsets(offsets), codes.data_ptr(), scales.data_ptr(),
+                             _stream(stream)), "lp_r128_quant")
+    return QTensor("fp8_r128", codes, scales, None, shape, axis)
+
+
+def lp_r128_quant_dual(src: torch.Tensor, offsets: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """Both "fp8_r128" copies of a bf16 tensor from one read: (along -1, along
+    -2); the second one's runs restart at each group of `offsets`.  Rows past
+    the last offset are left unwritten in both."""
+    b, r, c = shape = _shape3(src)
+    dev = src.device
+    codes_c = torch.empty(shape, dtype=torch.uint8, device=dev)
+    codes_r = torch.empty(shape, dtype=torch.uint8, device=dev)
+    scales_c = torch.empty((b, -(-c // 128), r), dtype=torch.float32, device=dev)
+    scales_r = torch.empty((b, _runs(r, offsets), c), dtype=torch.float32, device=dev)
+    _device(src, "src", 2 * b * r * c, torch.bfloat16)
+    _check(lib.lp_r128_quant_dual(src.data_ptr(), b, r, c, *_offsets(offsets), codes_c.data_ptr(), scales_c.data_ptr(),
+                                  codes_r.data_ptr(), scales_r.data_ptr(), _stream(stream)), "lp_r128_quant_dual")
+    return QTensor("fp8_r128", codes_c, scales_c, None, shape, -1), QTensor("fp8_r128", codes_r, scales_r, None, shape, -2)
+
+
+def lp_b128_quant(src: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                  stream=None) -> QTensor:
+    """Quantize a bf16 tensor [batch, rows, cols] (or [rows, cols]) to
+    "fp8_b128" (into `codes` and `scales` when given)."""
+    b, r, c = shape = _shape3(src)
+    if codes is None:
+        codes = torch.empty(shape, dtype=torch.uint8, device=src.device)
+    if scales is None:
+        scales = torch.empty((b, -(-r // 128), -(-c // 128)), dtype=torch.float32, device=src.device)
+    _device(src, "src", 2 * b * r * c, torch.bfloat16)
+    _device(codes, "codes", b * r * c)
+    _device(scales, "scales", _scale_bytes("fp8_b128", -1, b, r, c), torch.float32)
+    _check(lib.lp_b128_quant(src.data_ptr(), b, r, c, codes.data_ptr(), scales.data_ptr(), _stream(stream)),
+           "lp_b128_quant")
+    return QTensor("fp8_b128", codes, scales, None, shape)
+
+
+def _fwd_dyn(x: torch.Tensor, w: QTensor, offsets: Optional[torch.Tensor], y: Optional[torch.Tensor], stream):
+    M, K = x.shape
+    if K != w.cols:
+        raise ValueError(f"x has {K} columns, the weight {w.cols}")
+    _device(x, "x", 2 * M * K, torch.bfloat16)
+    if y is None:
+        y = torch.empty((M, w.rows), dtype=torch.bfloat16, device=x.device)
+    _device(y, "y", 2 * M * w.rows)
+    nb = -(-K // 128)
+    scales = 4 * nb * M                                      # scratch: scales, then (16-byte aligned) codes
+    scratch = torch.empty(-(-scales // 16) * 16 + M * K, dtype=torch.uint8, device=x.device)
+    at = scratch.data_ptr()
+    args = (at + -(-scales // 16) * 16, at, y.data_ptr(), _stream(stream))
+    wc = w.c()
+    if offsets is None:
+        _check(lib.lp_linear_fwd_dyn(x.data_ptr(), M, ctypes.byref(wc), *args), "lp_linear_fwd_dyn")
+    else:
+        _device(offsets, "offsets", 4 * offsets.numel(), torch.int32)
+        _check(lib.lp_grouped_fwd_dyn(x.data_ptr(), M, ctypes.byref(wc), offsets.data_ptr(), offsets.numel(), *args),
+               "lp_grouped_fwd_dyn")
+    return y
+
+
+def lp_linear_fwd_dyn(x: torch.Tensor, w: QTensor, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y [M, N] = x @ w^T: a bf16 x [M, K], quantized to "fp8_r128" in the
+    call, times an "fp8_b128" weight."""
+    return _fwd_dyn(x, w, None, y, stream)
+
+
+def lp_grouped_fwd_dyn(x: torch.Tensor, w: QTensor, offsets: torch.Tensor, y: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """y [M, N]: rows of group g are x[rows] @ w[g]^T, x quantized in the
+    call; rows at or past offsets[-1] are left as they were in `y`."""
+    return _fwd_dyn(x, w, offsets, y, stream)
+
+
+class _AdamWTensorC(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scales", ctypes.c_void_p),
+                ("exp_avg_sq_scales", ctypes.c_void_p), ("param_copy", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("lr_scale", ctypes.c_float), ("weight_decay", ctypes.c_float)]
+
+
+class AdamWPlan:
+    """The tensors of an AdamW step, checked once: lists of equal length with
+    each tensor's parameter (float32 or bfloat16), gradient (float32 or
+    bfloat16) and moments.  Moments are float32 of the parameter's size, or
+    uint8 E4M3 codes with float32 scales per 128 elements
+    (exp_avg_sq_scales: of sqrt(v)).  copies: bfloat16 tensors that receive
+    the new float32 parameters.  weight_decay, lr_scale: one number or one
+    per tensor.  The plan keeps the tensors alive; gradients may be replaced
+    with set_grads."""
+
+    def __init__(self, params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales=None, exp_avg_sq_scales=None, copies=None,
+                 weight_decay=0.0, lr_scale=1.0):
+        k = len(params)
+        lists = {"grads": grads, "exp_avgs": exp_avgs, "exp_avg_sqs": exp_avg_sqs, "exp_avg_scales": exp_avg_scales,
+                 "exp_avg_sq_scales": exp_avg_sq_scales, "copies": copies}
+        for name, v in lists.items():
+            if v is not None and len(v) != k:
+                raise ValueError(f"{name}: {len(v)} tensors for {k} parameters")
+        if (exp_avg_scales is None) != (exp_avg_sq_scales is None):
+            raise ValueError("8-bit moments need exp_avg_scales and exp_avg_sq_scales")
+        self.bits8 = exp_avg_scales is not None
+        self.param_dtype = params[0].dtype if k else torch.float32
+        self._n = [p.numel() for p in params]
+        self._c = (_AdamWTensorC * max(k, 1))()
+        self._kept = [list(params), list(exp_avgs), list(exp_avg_sqs)] + [list(v) for v in (exp_avg_scales, exp_avg_sq_scales, copies) if v is not None]
+        if self.param_dtype not in _ADAMW_DTYPE:
+            raise ValueError(f"parameters must be float32 or bfloat16, not {self.param_dtype}")
+        wd = weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * k
+        ls = lr_scale if isinstance(lr_scale, (list, tuple)) else [lr_scale] * k
+        if len(wd) != k or len(ls) != k:
+            raise ValueError("weight_decay and lr_scale: one number, or one per parameter")
+        state = torch.uint8 if self.bits8 else torch.float32
+        for i, (p, n) in enumerate(zip(params, self._n)):
+            c = self._c[i]
+            runs = -(-n // 128)
+
+            def ptr(t, name, count, dtype):
+                size = torch.empty((), dtype=dtype).element_size()
+                _device(t, f"{name}[{i}]", count * size, dtype)
+                return t.data_ptr()
+            c.param = ptr(p, "params", n, self.param_dtype)
+            c.exp_avg = ptr(exp_avgs[i], "exp_avgs", n, state)
+            c.exp_avg_sq = ptr(exp_avg_sqs[i], "exp_avg_sqs", n, state)
+            if self.bits8:
+                c.exp_avg_scales = ptr(exp_avg_scales[i], "exp_avg_scales", runs, torch.float32)
+                c.exp_avg_sq_scales = ptr(exp_avg_sq_scales[i], "exp_avg_sq_scales", runs, torch.float32)
+            if copies is not None:
+                c.param_copy = ptr(copies[i], "copies", n, torch.bfloat16)
+            c.n, c.weight_decay, c.lr_scale = n, wd[i], ls[i]
+        self.set_grads(grads)
+
+    def set_grads(self, grads) -> None:
+        """Use these gradients from now on (all of one dtype)."""
+        if len(grads) != len(self._n):
+            raise ValueError(f"grads: {len(grads)} tensors for {len(self._n)} parameters")
+        dtype = grads[0].dtype if grads else torch.float32
+        if dtype not in _ADAMW_DTYPE:
+            raise ValueError(f"gradients must be float32 or bfloat16, not {dtype}")
+        size = 4 if dtype == torch.float32 else 2
+        for i, (g, n) in enumerate(zip(grads, self._n)):
+            _device(g, f"grads[{i}]", n * size, dtype)
+        for c, g in zip(self._c, grads):
+            c.grad = g.data_ptr()
+        self.grad_dtype, self._grads = dtype, list(grads)
+
+
+_ADAMW_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def lp_adamw(plan: AdamWPlan, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, step: int = 1,
+             grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One AdamW step over the plan's tensors, in place.  step: 1 for the
+    first; grad_scale: a float32 device scalar that multiplies every gradient."""
+    if grad_scale is not None:
+        _device(grad_scale, "grad_scale", 4, torch.float32)
+    _check(lib.lp_adamw(plan._c, len(plan._n), _ADAMW_DTYPE[plan.param_dtype], _ADAMW_DTYPE[plan.grad_dtype],
+                        int(plan.bits8), lr, beta1, beta2, eps, step,
+                        None if grad_scale is None else grad_scale.data_ptr(), _stream(stream)), "lp_adamw")

@@ -44,12 +44,12 @@ bool has_block_scales(int f) { return f != LP_BF16 && !is_fp8t(f); }
 // Shape, pointer and alignment checks of one operand tensor.
 lp_status check_tensor(const lp_qtensor* t) {
   if (t == nullptr) return LP_ERR_NULL;
-  if (t->fmt < LP_BF16 || t->fmt > LP_FP8T_E5M2) return LP_ERR_FORMAT;
+  if ((t->fmt < LP_BF16 || t->fmt > LP_FP8T_E5M2) && t->fmt != LP_FP8_R128) return LP_ERR_FORMAT;
   if (t->batch < 0 || t->rows < 0 || t->cols < 0) return LP_ERR_SHAPE;
   if (t->rows > kMaxDim || t->cols > kMaxDim || t->batch > kMaxDim) return LP_ERR_SHAPE;
   const int axis = has_block_scales(t->fmt) ? t->scale_axis : -1;
   if (axis != -1 && axis != -2) return LP_ERR_FORMAT;
-  if (axis == -2 && t->fmt != LP_MXFP8) return LP_ERR_FORMAT;
+  if (axis == -2 && t->fmt != LP_MXFP8 && t->fmt != LP_FP8_R128) return LP_ERR_FORMAT;
   if (t->cols % 16) return LP_ERR_SHAPE;
   if ((t->fmt == LP_MXFP4 || (t->fmt == LP_MXFP8 && axis == -1)) && t->cols % 32) return LP_ERR_SHAPE;
   if (t->fmt == LP_MXFP8 && axis == -2 && t->rows % 32) return LP_ERR_SHAPE;
@@ -74,20 +74,25 @@ lp_status check_bwd(const lp_qtensor* grad, const lp_qtensor* x, const lp_qtenso
   lp_status st = check_tensor(grad);
   if (st != LP_OK) return st;
   if (grad->batch != 1) return LP_ERR_SHAPE;
-  // grad_out: bf16 for every product; MXFP8 along its columns (the dX
+  // grad_out: LP_FP8_R128 along its columns with a block-FP8 weight (dX only)
+  // or along its rows with an input scaled along its rows (dW only);
+  // otherwise bf16 for every product; MXFP8 along its columns (the dX
   // contraction) for dX only; MXFP8 along its rows (the dW contraction) for a
   // dense dW of an MXFP8 input scaled along its rows, only; per-tensor FP8
   // for both products, with per-tensor FP8 operands only.
   const bool g_mx_cols = grad->fmt == LP_MXFP8 && grad->scale_axis == -1;
   const bool g_mx_rows = grad->fmt == LP_MXFP8 && grad->scale_axis == -2;
   const bool g_t = is_fp8t(grad->fmt);
-  if (grad->fmt != LP_BF16 && !g_mx_cols && !g_mx_rows && !g_t) return LP_ERR_FORMAT;
+  const bool g_r = grad->fmt == LP_FP8_R128;
+  if (grad->fmt != LP_BF16 && !g_mx_cols && !g_mx_rows && !g_t && !g_r) return LP_ERR_FORMAT;
+  if (g_r && (grad->scale_axis == -1 ? grad_w : grad_x) != nullptr) return LP_ERR_FORMAT;
   if (g_mx_rows && (grad_x != nullptr || groups != 0)) return LP_ERR_FORMAT;
   const int64_t M = grad->rows, N = grad->cols;
   int64_t K = -1;
   if (grad_x != nullptr) {
     if ((st = check_tensor(w)) != LP_OK) return st;
-    if (is_fp8t(w->fmt) != g_t) return LP_ERR_FORMAT;
+    if (is_fp8t(w->fmt) != g_t || w->fmt == LP_FP8_R128) return LP_ERR_FORMAT;
+    if (g_r && w->fmt != LP_FP8_B128) return LP_ERR_FORMAT;
     if (w->batch != (groups ? groups : 1) || w->rows != N) return LP_ERR_SHAPE;
     K = w->cols;
   }
@@ -95,6 +100,7 @@ lp_status check_bwd(const lp_qtensor* grad, const lp_qtensor* x, const lp_qtenso
     if (g_mx_cols) return LP_ERR_FORMAT;              // its scales do not run along the dW contraction
     if ((st = check_tensor(x)) != LP_OK) return st;
     if (is_fp8t(x->fmt) != g_t) return LP_ERR_FORMAT;
+    if ((x->fmt == LP_FP8_R128) != g_r || (g_r && x->scale_axis != -2)) return LP_ERR_FORMAT;
     if (g_mx_rows && !(x->fmt == LP_MXFP8 && x->scale_axis == -2)) return LP_ERR_FORMAT;
     if (x->batch != 1 || x->rows != M) return LP_ERR_SHAPE;
     if (K >= 0 && x->cols != K) return LP_ERR_SHAPE;
@@ -343,7 +349,8 @@ extern "C" {
 
 // Checks of the forward: x [M][K] and w [G][N][K], both MXFP4 or both MXFP8
 // scaled along k (K % 128 for MXFP4, K % 64 for MXFP8), both NVFP4 (K % 32),
-// or a bf16 x with a bf16 or block-FP8 weight (K % 16); N % 16.
+// a bf16 x with a bf16 or block-FP8 weight, or an LP_FP8_R128 x (along k) with
+// a block-FP8 weight (K % 16); N % 16.
 static lp_status check_fwd(const lp_qtensor* x, const lp_qtensor* w, void* y, int64_t groups) {
   lp_status st = check_tensor(x);
   if (st != LP_OK) return st;
@@ -351,7 +358,8 @@ static lp_status check_fwd(const lp_qtensor* x, const lp_qtensor* w, void* y, in
   const bool mx = (x->fmt == LP_MXFP4 || x->fmt == LP_MXFP8) && w->fmt == x->fmt;
   const bool nv = x->fmt == LP_NVFP4 && w->fmt == LP_NVFP4;
   const bool b16 = x->fmt == LP_BF16 && (w->fmt == LP_BF16 || w->fmt == LP_FP8_B128 || w->fmt == LP_NVFP4);
-  if (!mx && !nv && !b16) return LP_ERR_FORMAT;
+  const bool r128 = x->fmt == LP_FP8_R128 && x->scale_axis == -1 && w->fmt == LP_FP8_B128;
+  if (!mx && !nv && !b16 && !r128) return LP_ERR_FORMAT;
   if ((mx || nv) && (x->scale_axis != -1 || w->scale_axis != -1)) return LP_ERR_FORMAT;
   if (w->fmt == LP_NVFP4 && w->scale_axis != -1) return LP_ERR_FORMAT;
   if (x->batch != 1 || w->batch != (groups ? groups : 1) || w->cols != x->cols) return LP_ERR_SHAPE;
@@ -363,6 +371,14 @@ static lp_status check_fwd(const lp_qtensor* x, const lp_qtensor* w, void* y, in
   if (!aligned(y, 16)) return LP_ERR_ALIGN;
   return LP_OK;
 }
+
+}  // extern "C"
+
+lp_status lp::check_forward(const lp_qtensor* x, const lp_qtensor* w, void* y, int64_t groups) {
+  return check_fwd(x, w, y, groups);
+}
+
+extern "C" {
 
 lp_status lp_linear_fwd(const lp_qtensor* x, const lp_qtensor* w, void* y, void* stream) {
   lp_status st = check_fwd(x, w, y, 0);

@@ -185,6 +185,42 @@ __global__ __launch_bounds__(kThreads) void dequant_fp8_b128(const u32x2* __rest
   }
 }
 
+// E4M3 with an fp32 scale per run of 128: along the columns
+// (scales[batch][run][row], one for the unit) or along the rows
+// (scales[batch][row / 128][col], one for each of the unit's eight columns).
+template <bool kAlongCols>
+__global__ __launch_bounds__(kThreads) void dequant_r128(const u32x2* __restrict__ codes,
+                                                         const float* __restrict__ scales, u32x4* __restrict__ out,
+                                                         uint32_t nunits, FastDiv units_per_row,
+                                                         FastDiv rows_per_batch, uint32_t nruns, uint32_t cols) {
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    const uint32_t u = unit_of(j);
+    if (u >= nunits) break;
+    const uint32_t grow = fdiv(u, units_per_row);        // row over batch*rows
+    const uint32_t col = (u - grow * units_per_row.d) * 8u;
+    const uint32_t b = fdiv(grow, rows_per_batch);
+    const uint32_t r = grow - b * rows_per_batch.d;
+    const u32x2 c = __builtin_nontemporal_load(codes + u);
+    uint32_t o[4];
+    if constexpr (kAlongCols) {
+      const float S = scales[((size_t)b * nruns + (col >> 7)) * rows_per_batch.d + r];
+      fp8x4_to_bf16_mul(c[0], S, o);
+      fp8x4_to_bf16_mul(c[1], S, o + 2);
+    } else {
+      const float* S = scales + ((size_t)b * nruns + (r >> 7)) * cols + col;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[h], 1.0f, false);
+        const f32x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[h], 1.0f, true);
+        o[2 * h] = pack_bf16x2(lo[0] * S[4 * h], lo[1] * S[4 * h + 1]);
+        o[2 * h + 1] = pack_bf16x2(hi[0] * S[4 * h + 2], hi[1] * S[4 * h + 3]);
+      }
+    }
+    __builtin_nontemporal_store(fix_fp8(o, c), out + u);
+  }
+}
+
 }  // namespace
 
 hipError_t launch_dequant(const lp_qtensor& t, void* dst, hipStream_t stream) {
@@ -215,6 +251,16 @@ hipError_t launch_dequant(const lp_qtensor& t, void* dst, hipStream_t stream) {
           c64, static_cast<const float*>(t.scales), out, nunits, make_fastdiv((uint32_t)(t.cols / 8)),
           make_fastdiv((uint32_t)t.rows), (uint32_t)((t.rows + 127) / 128), (uint32_t)((t.cols + 127) / 128));
       break;
+    case LP_FP8_R128: {
+      const FastDiv upr = make_fastdiv((uint32_t)(t.cols / 8)), rpb = make_fastdiv((uint32_t)t.rows);
+      const float* s = static_cast<const float*>(t.scales);
+      const uint32_t runs = (uint32_t)(((t.scale_axis == -1 ? t.cols : t.rows) + 127) / 128), cols = (uint32_t)t.cols;
+      if (t.scale_axis == -1)
+        dequant_r128<true><<<grid, block, 0, stream>>>(c64, s, out, nunits, upr, rpb, runs, cols);
+      else
+        dequant_r128<false><<<grid, block, 0, stream>>>(c64, s, out, nunits, upr, rpb, runs, cols);
+      break;
+    }
     case LP_FP8T_E4M3:
     case LP_FP8T_E5M2:
       return launch_tensor_dequant(t, dst, stream);

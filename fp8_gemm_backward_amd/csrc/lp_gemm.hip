@@ -36,6 +36,11 @@ Op make_op(const lp_qtensor& t) {
     case LP_FP8T_E5M2:
       o.code_ld = (int32_t)Cc;
       break;
+    case LP_FP8_R128:                                            // scale rows: one per run
+      o.code_ld = (int32_t)Cc;
+      o.scale_ld = (int32_t)((t.scale_axis == -1 ? R : Cc) * 4);
+      o.scale_bytes = (((t.scale_axis == -1 ? Cc : R) + 127) / 128) * o.scale_ld;
+      break;
     case LP_MXFP8:
       o.code_ld = (int32_t)Cc;
       if (t.scale_axis == -1) {
@@ -175,9 +180,12 @@ bool is_fp8t(int f) { return f == LP_FP8T_E4M3 || f == LP_FP8T_E5M2; }
 // Per-tensor scaled FP8 on both sides of the product.
 bool native_pt(const GemmCall& call) { return is_fp8t(call.grad->fmt) && is_fp8t(call.other->fmt); }
 
+// E4M3 with fp32 scales per 128 on both sides.
+bool native_b128(const GemmCall& call) { return call.grad->fmt == LP_FP8_R128; }
+
 SplitPlan split_plan(const GemmCall& call) {
   SplitPlan sp{1, 0, big_tiles(call), 0};
-  if (call.offsets != nullptr || native_mx(call) || native_pt(call) || narrow_tiles(call) >= kCUs / 2 || sp.tiles == 0) return sp;
+  if (call.offsets != nullptr || native_mx(call) || native_pt(call) || native_b128(call) || narrow_tiles(call) >= kCUs / 2 || sp.tiles == 0) return sp;
   const int64_t ktot = call.dw ? call.M : call.N;
   const int64_t nk = (ktot + BK - 1) / BK;
   int64_t s = kCUs / sp.tiles;
@@ -245,9 +253,33 @@ Params native_params(const GemmCall& call) {
   return prm;
 }
 
+// Tile counts and order of a product with fp32 scales per 128 on b x b tiles.
+// rows: output rows; groups split them (grad_X, forward) unless dw, where
+// every group has all of them.
+void b128_tiles(Params& prm, int b, bool dw) {
+  const int64_t np = (prm.Ptot + b - 1) / b;
+  prm.nq = (prm.Qtot + b - 1) / b;
+  if (prm.offsets == nullptr || !dw) prm.gm = tile_group(b, b, prm.offsets == nullptr ? np : kCUsPerXcd);
+  const int64_t pt = dw ? np * prm.groups : prm.offsets ? prm.Ptot / b + prm.groups : np;
+  prm.ntiles = (int32_t)(pt * prm.nq);
+}
+
+// Whether 256 x 256 tiles make enough workgroups for the GPU.
+bool b128_big(const Params& prm, bool dw) {
+  Params t = prm;
+  b128_tiles(t, 256, dw);
+  return t.ntiles >= kCUs;
+}
+
 }  // namespace
 
 hipError_t launch_gemm(const GemmCall& call, hipStream_t stream) {
+  if (native_b128(call)) {
+    Params prm = base_params(call);
+    const bool big = b128_big(prm, call.dw);
+    b128_tiles(prm, big ? 256 : 128, call.dw);
+    return call.dw ? b128_dw(prm, big, stream) : b128_dx(prm, big, stream);
+  }
   if (native_mx(call) || native_pt(call)) {
     const Params prm = native_params(call);
     const int fp = call.grad->fmt, fq = call.other->fmt;
@@ -284,6 +316,11 @@ hipError_t launch_fwd(const lp_qtensor& x, const lp_qtensor& w, const int32_t* o
   prm.offsets = offsets;
   prm.groups = groups;
   prm.splits = 1;
+  if (x.fmt == LP_FP8_R128) {
+    const bool big = b128_big(prm, false);
+    b128_tiles(prm, big ? 256 : 128, false);
+    return b128_fwd(prm, big, stream);
+  }
   // MX operands run on the block-scaled MFMA (256 x 256 tiles); the others
   // through bf16 tiles, 256 x 256 unless both are bf16 (256 x 128: three
   // stages of both tiles fit in LDS only at that width).
@@ -299,6 +336,15 @@ hipError_t launch_fwd(const lp_qtensor& x, const lp_qtensor& w, const int32_t* o
   const hipError_t e = fwd_dec(prm, x.fmt, w.fmt, false, stream);
   if (e != hipSuccess || !split) return e;
   return fwd_dec(tail_params(prm), x.fmt, w.fmt, true, stream);
+}
+
+hipError_t launch_fwd_dyn(const void* x, const lp_qtensor& xq, const lp_qtensor& w, const int32_t* offsets,
+                          int32_t groups, void* x_codes, void* x_scales, void* y, hipStream_t stream) {
+  if (xq.cols > 0) {
+    const hipError_t e = launch_r128_cols(x, 1, xq.rows, xq.cols, x_codes, x_scales, stream);
+    if (e != hipSuccess) return e;
+  }
+  return launch_fwd(xq, w, offsets, groups, y, stream);
 }
 
 hipError_t launch_grouped_dx_deferred(const lp_qtensor& grad, const void* w, int64_t K, const int32_t* offsets,

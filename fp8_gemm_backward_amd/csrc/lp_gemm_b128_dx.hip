@@ -1,0 +1,12 @@
+// grad_X = grad_out @ W of FP8 operands with fp32 scales per 128, dense and grouped.
+#include "lp_gemm_b128_kernel.hpp"
+
+namespace lp {
+namespace gk {
+
+hipError_t b128_dx(const Params& prm, bool big, hipStream_t s) {
+  return big ? run_b128<B256, kB128Dx>(prm, s) : run_b128<B128, kB128Dx>(prm, s);
+}
+
+}  // namespace gk
+}  // namespace lp

@@ -1004,6 +1004,11 @@ hipError_t pt_pair(const Params& dx, const Params& dw, int fmt_p, int fmt_q, hip
 // in one launch, grad_X's tiles first; W and X both LP_MXFP4 or both
 // LP_NVFP4 (fmt_q), scaled along their last axis.
 hipError_t dec_pair(const Params& dx, const Params& dw, int fmt_q, hipStream_t s);
+// Products of E4M3 operands with fp32 scales per 128, on 256 x 256 (big) or
+// 128 x 128 tiles.
+hipError_t b128_fwd(const Params& prm, bool big, hipStream_t s);
+hipError_t b128_dx(const Params& prm, bool big, hipStream_t s);
+hipError_t b128_dw(const Params& prm, bool big, hipStream_t s);
 
 }  // namespace gk
 }  // namespace lp

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "lp.h"
+#include "lp_train.h"
 
 namespace lp {
 
@@ -97,5 +98,35 @@ hipError_t launch_grouped_dx_deferred(const lp_qtensor& grad, const void* w, int
 hipError_t launch_mx_quant_rows_groups(const void* src, int64_t groups, int64_t rows, int64_t cols,
                                        const int32_t* offsets, int64_t M, int64_t min_rows, void* codes, void* scales,
                                        hipStream_t stream);
+
+// E4M3 with fp32 scales per 128 (lp_r128.hip).  Runs along the columns:
+// codes and scales [batch][ceil(cols/128)][rows].
+hipError_t launch_r128_cols(const void* src, int64_t batch, int64_t rows, int64_t cols, void* codes, void* scales,
+                            hipStream_t stream);
+// By 128 x 128 tiles: runs along the rows into codes_r / scales_r and, when
+// given, runs along the columns into codes_c / scales_c; with codes_r null,
+// one scale per tile into codes_c / scales_c.  offsets: token runs restart at
+// each group's first row.
+hipError_t launch_r128_tiles(const void* src, int64_t batch, int64_t rows, int64_t cols, const int32_t* offsets,
+                             int64_t groups, void* codes_c, void* scales_c, void* codes_r, void* scales_r,
+                             hipStream_t stream);
+// The forward of a bf16 x [M][K] by an LP_FP8_B128 weight; xq describes the
+// scratch that a quantized copy of x goes to.
+hipError_t launch_fwd_dyn(const void* x, const lp_qtensor& xq, const lp_qtensor& w, const int32_t* offsets,
+                          int32_t groups, void* x_codes, void* x_scales, void* y, hipStream_t stream);
+
+// One AdamW step (lp_adamw.hip); arguments checked by the caller.
+struct AdamwCall {
+  const lp_adamw_tensor* tensors;
+  int64_t count;
+  bool bf16_param, bf16_grad, bits8;
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  const float* grad_scale;
+};
+hipError_t launch_adamw(const AdamwCall& c, hipStream_t stream);
+
+// The checks of lp_linear_fwd (groups 0) and lp_grouped_fwd (lp_api.hip).
+lp_status check_forward(const lp_qtensor* x, const lp_qtensor* w, void* y, int64_t groups);
 
 }  // namespace lp

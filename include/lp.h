@@ -71,6 +71,14 @@
  *   LP_FP8T_E5M2 E5M2 codes, one byte each, one fp32 tensor scale likewise.
  *                ("AstrAI fp8.py": per-tensor scaled FP8, E4M3 for the
  *                forward operands and E5M2 for gradients.)
+ *   LP_FP8_R128  E4M3 codes, one byte each; one fp32 scale (decode multiplier)
+ *                per run of 128 elements along `scale_axis`, the last run cut
+ *                at the tensor edge.  Scales are stored run by run:
+ *                -1 -> scales[batch][ceil(cols/128)][rows],
+ *                -2 -> scales[batch][ceil(rows/128)][cols]
+ *                (the product reads one run's scales of many rows at a time).
+ *                The activations and gradients that go with an LP_FP8_B128
+ *                weight in FP8 products (lp_train.h has the quantizers).
  *
  * Element values: E2M1 (1 sign, 2 exponent bits with bias 1, 1 mantissa bit:
  * 0, 0.5, 1, 1.5, 2, 3, 4, 6), E4M3 (bias 7, max 448, no infinities,
@@ -110,14 +118,15 @@ typedef enum {
   LP_FP8_B128 = 3,
   LP_MXFP8 = 4,
   LP_FP8T_E4M3 = 5,
-  LP_FP8T_E5M2 = 6
+  LP_FP8T_E5M2 = 6,
+  LP_FP8_R128 = 8          /* 7 is unassigned */
 } lp_fmt;
 
 /* A (possibly block-scaled) tensor of logical shape [batch][rows][cols]. */
 typedef struct {
   int32_t fmt;               /* lp_fmt                                          */
   int32_t scale_axis;        /* -1: scale blocks run along cols; -2: along rows
-                                (LP_MXFP8 only; ignored for LP_BF16)            */
+                                (LP_MXFP8, LP_FP8_R128 only; ignored for LP_BF16) */
   int64_t batch;             /* groups for a grouped weight, else 1             */
   int64_t rows;
   int64_t cols;              /* logical elements (not packed bytes)             */
@@ -138,8 +147,8 @@ typedef struct {
  * src       any format except LP_BF16.  Divisibility: cols % 32 == 0 for
  *           LP_MXFP4 and for LP_MXFP8 with scale_axis -1; rows % 32 == 0 and
  *           cols % 16 == 0 for LP_MXFP8 with scale_axis -2; cols % 16 == 0 for
- *           LP_NVFP4, LP_FP8_B128 and LP_FP8T_* (rows arbitrary; partial
- *           128-blocks are cut at the edge).
+ *           LP_NVFP4, LP_FP8_B128, LP_FP8_R128 and LP_FP8T_* (rows arbitrary;
+ *           partial 128-blocks are cut at the edge).
  * dst_bf16  device bf16 output [batch][rows][cols].
  * Result is bit-exact: the rule in the header comment above.
  */
@@ -283,6 +292,12 @@ lp_status lp_tensor_quant_delayed(const void* src_bf16, int64_t n, int32_t dst_f
  *           Or LP_FP8T_E4M3 / LP_FP8T_E5M2, one copy for both products, with
  *           x and w LP_FP8T_* too ("AstrAI fp8.py", _LinearFp8.backward):
  *           per-tensor scaled operands pair only with each other.
+ *           Or LP_FP8_R128 with scale_axis -1 (needs grad_w == NULL and w
+ *           LP_FP8_B128) or -2 (needs grad_x == NULL and x LP_FP8_R128 with
+ *           scale_axis -2), as produced by lp_r128_quant_dual: the product
+ *           runs on the FP8 MFMA, in fp32 within each 128 of the contraction;
+ *           each such sum is multiplied by the two scales' fp32 product and
+ *           added in fp32.  LP_FP8_R128 pairs with nothing else.
  * x         [M][K] saved input, or NULL when grad_w == NULL.
  * w         [N][K] saved weight, or NULL when grad_x == NULL.
  *           x and w: LP_BF16, LP_MXFP4, LP_NVFP4 (scale_axis -1), LP_FP8_B128,
@@ -398,9 +413,11 @@ lp_status lp_linear_bwd_noalloc(const lp_qtensor* grad_out, const lp_qtensor* x,
  *           written.
  * grad_w    device bf16 [groups][N][K] or NULL.  An empty group's slice is
  *           written with zeros (the empty sum).
- * Size and format rules as for lp_linear_bwd, except that grad_out scaled
- * along its rows (-2) is not accepted (its 32-row blocks would straddle
- * groups); 1 <= groups <= 1024.
+ * Size and format rules as for lp_linear_bwd, except that an LP_MXFP8
+ * grad_out scaled along its rows (-2) is not accepted (its 32-row blocks would
+ * straddle groups); 1 <= groups <= 1024.  LP_FP8_R128 operands scaled along
+ * their rows have runs that restart at every group's first row, with scales
+ * [M / 128 + groups][cols], as lp_r128_quant with these offsets writes them.
  */
 lp_status lp_grouped_bwd(const lp_qtensor* grad_out, const lp_qtensor* x, const lp_qtensor* w,
                          const int32_t* offsets, int64_t groups, void* grad_x, void* grad_w,
@@ -466,7 +483,10 @@ lp_status lp_grouped_dx_deferred(const lp_qtensor* grad_out, const void* w, int6
  *      scale); K % 32 == 0;
  *    - x LP_BF16 and w LP_BF16 or LP_FP8_B128 (K % 16 == 0) or LP_NVFP4
  *      (scale_axis -1, K % 32 == 0): an NVFP4 x decoded first with
- *      lp_dequant, which saves the per-tile decode of x.
+ *      lp_dequant, which saves the per-tile decode of x;
+ *    - x LP_FP8_R128 (scale_axis -1) and w LP_FP8_B128 (K % 16 == 0), on the
+ *      FP8 MFMA: fp32 sums within each 128 of K, times the two scales'
+ *      fp32 product, added in fp32.
  *    N % 16 == 0; M >= 0 arbitrary.
  * y  device bf16 [M][N].
  * MX operands: y[m][n] = sum_k dec(x)[m][k] * dec(w)[n][k] on the

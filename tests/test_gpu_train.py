@@ -1,0 +1,476 @@
+"""FP8 with fp32 scales per 128 elements (lp_train.h) against the fp64 oracle
+(GPU): quantizers and decode bit for bit, products within a bound derived from
+the arithmetic."""
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+from gpu_util import assert_bits_equal, assert_close, bf16_dev, bits_host, dev
+from oracle import train as O
+from oracle.formats import E4M3_TABLE, bf16_bits_to_f64, f32_to_bf16_bits, round_f32
+
+pytestmark = pytest.mark.gpu
+
+
+def bits(rng, shape, sigma=1.0):
+    """bf16 bits of N(0, sigma) with a few large and a few tiny values."""
+    v = rng.standard_normal(shape, dtype=np.float32) * np.float32(sigma)
+    v = np.where(rng.random(shape) < 0.01, v * 50, v)
+    v = np.where(rng.random(shape) < 0.01, v * 1e-4, v)
+    return W.bf16_bits(v.astype(np.float32))
+
+
+def special_bits(rng, shape):
+    """Random bits with zero runs, subnormals, values around the scale floor, the largest finite values, NaN and
+    infinities of both signs."""
+    b = bits(rng, shape)
+    flat = b.reshape(-1)
+    R, C = shape
+    pick = [0x7FC0, 0xFFC1, 0x7F80, 0xFF80, 0x0001, 0x8001, 0x7F7F, 0xFF7F, 0x1F80, 0x1F7F, 0x0000, 0x8000]
+    for i, p in enumerate(pick):
+        flat[(i * 977 + 13) % flat.size] = p
+    b[R // 2, :] = 0
+    b[:, C // 2] = 0x8000
+    if R > 2:
+        b[1, :] = (b[1, :] & 0x807F) | 0x1F00           # magnitudes near 2^-65
+        b[R - 1, :] &= 0x807F                            # subnormals
+    return b
+
+
+SHAPES = [(1, 16), (1, 128), (3, 144), (128, 256), (130, 272), (257, 400), (64, 1040)]
+
+
+def ends_of(sizes):
+    return np.cumsum(sizes).astype(np.int32)
+
+
+def scales_array(scales: dict, n: int, cols: int):
+    out = np.zeros((n, cols), np.float32)
+    for k, v in scales.items():
+        out[k] = v
+    return out
+
+
+def f32_bits(t):
+    a = t.cpu().numpy() if isinstance(t, torch.Tensor) else np.asarray(t, np.float32)
+    a = a.copy()
+    a[np.isnan(a)] = np.nan                              # one NaN pattern
+    return a.view(np.uint32)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("make", [bits, special_bits])
+def test_quantizers_bit_exact(lp, shape, make):
+    b = make(np.random.default_rng(shape[0] * 1000 + shape[1]), shape)
+    x = bf16_dev(b)
+    qc, qr, qb = lp.lp_r128_quant(x, -1), lp.lp_r128_quant(x, -2), lp.lp_b128_quant(x)
+    dc, dr = lp.lp_r128_quant_dual(x)
+    codes, scales = O.quant_cols(b)
+    for q in (qc, dc):
+        assert_bits_equal(q.codes.cpu().numpy()[0], codes, "codes along the columns")
+        assert_bits_equal(f32_bits(q.scales)[0], f32_bits(scales), "scales along the columns")
+    codes, scales = O.quant_rows(b)
+    for q in (qr, dr):
+        assert_bits_equal(q.codes.cpu().numpy()[0], codes, "codes along the rows")
+        assert_bits_equal(f32_bits(q.scales)[0], f32_bits(scales_array(scales, -(-shape[0] // 128), shape[1])), "scales")
+    codes, scales = O.quant_blocks(b)
+    assert_bits_equal(qb.codes.cpu().numpy()[0], codes, "codes of blocks")
+    assert_bits_equal(f32_bits(qb.scales)[0], f32_bits(scales), "scales of blocks")
+
+
+def test_quantizers_of_a_batch_equal_those_of_its_entries(lp):
+    x = bf16_dev(bits(np.random.default_rng(5), (3, 150, 272)))
+    for quant in (lambda t: [lp.lp_r128_quant(t, -1)], lambda t: [lp.lp_r128_quant(t, -2)],
+                  lambda t: [lp.lp_b128_quant(t)], lp.lp_r128_quant_dual):
+        whole, parts = quant(x), [quant(x[i]) for i in range(3)]
+        for k, q in enumerate(whole):
+            assert torch.equal(q.codes, torch.cat([p[k].codes for p in parts]))
+            assert torch.equal(q.scales, torch.cat([p[k].scales for p in parts]))
+
+
+GROUPS = [[0, 0], [1], [130], [0, 1, 127, 128, 129, 0, 300, 5], [64] * 7, [3] * 70, [256, 0, 128]]
+
+
+@pytest.mark.parametrize("sizes", GROUPS)
+@pytest.mark.parametrize("tail", [0, 37])
+def test_grouped_quantizer_bit_exact_and_leaves_the_rest(lp, sizes, tail):
+    M, C = sum(sizes) + tail, 144
+    if M == 0:
+        M = 5
+    b = bits(np.random.default_rng(M), (M, C))
+    ends = ends_of(sizes)
+    runs = M // 128 + len(sizes)
+    out = [torch.full((M, C), 0xA5, dtype=torch.uint8, device="cuda"),
+           torch.full((2, M), -7.0, device="cuda"),
+           torch.full((M, C), 0xA5, dtype=torch.uint8, device="cuda"),
+           torch.full((runs, C), -7.0, device="cuda")]
+    x, off = bf16_dev(b), dev(ends)
+    st = lp.lib.lp_r128_quant_dual(x.data_ptr(), 1, M, C, off.data_ptr(), len(sizes), *[t.data_ptr() for t in out],
+                                   lp._stream(None))
+    assert st == 0
+    cc, sc, cr, sr = [t.cpu().numpy() for t in out]
+    live = int(ends[-1])
+    want_c, want_sc = O.quant_cols(b)
+    assert_bits_equal(cc[:live], want_c[:live], "columns copy")
+    assert_bits_equal(f32_bits(sc[:, :live]), f32_bits(want_sc[:, :live]), "its scales")
+    assert (cc[live:] == 0xA5).all() and (cr[live:] == 0xA5).all() and (sc[:, live:] == -7).all()
+    want_r, want_sr = O.quant_rows(b, ends)
+    assert_bits_equal(cr[:live], want_r[:live], "rows copy")
+    for run in range(runs):
+        want = want_sr.get(run, np.full(C, -7.0, np.float32))
+        assert_bits_equal(f32_bits(sr[run]), f32_bits(want), f"scales of run {run}")
+    alone = lp.lp_r128_quant(x, -2, off)
+    assert torch.equal(alone.codes[0, :live], out[2][:live])
+
+
+@pytest.mark.parametrize("axis", [-1, -2])
+def test_decode_bit_exact(lp, axis):
+    """Every code under scales of many magnitudes, zero, infinite and NaN ones among them."""
+    R, C = 300, 272
+    codes = np.arange(R * C, dtype=np.int64).reshape(R, C).astype(np.uint8)
+    pool = np.array([1.0, 0.0, -1.5, 1e-40, 1e-30, 3.7, 6e4, 1e30, 3e38, np.inf, np.nan, 0.00173], np.float32)
+    n = (3, R) if axis == -1 else (3, C)
+    scales = pool[np.arange(n[0] * n[1]).reshape(n) % len(pool)]
+    S = np.repeat(scales.T, 128, 1)[:, :C] if axis == -1 else np.repeat(scales, 128, 0)[:R]
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = f32_to_bf16_bits(round_f32(E4M3_TABLE[codes] * S.astype(np.float64)), nan_sign=codes >> 7)
+    got = lp.lp_dequant(lp.QTensor("fp8_r128", dev(codes), dev(scales), axis=axis))
+    assert_bits_equal(bits_host(got)[0], want, f"axis {axis}")
+
+
+# ---------------------------------------------------------------- products
+
+def assert_product(got, a, b, what=""):
+    """got (bf16) against a @ b in fp64, element by element: rounding to bf16 (half a unit of 8 significant bits, 2^-8)
+    plus the sum.  Inside one instruction the FP8 matrix core aligns the products to the largest of them and drops low
+    bits: at most 2^-10 of each product's magnitude in all (measured on random codes: 2^-12.6).  And the library's
+    criterion for every product (gpu_util)."""
+    g = got.float().cpu().numpy().astype(np.float64)
+    ref, mag = a @ b, np.abs(a) @ np.abs(b)
+    bound = 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * mag + 1e-37
+    bad = ~(np.abs(g - ref) <= bound)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} beyond the bound, worst {np.nanmax(np.abs(g - ref) / bound)}"
+    assert_close(got, ref, what)
+
+
+def weight(lp, rng, G, N, K):
+    """G block-scaled weights: descriptor and decoded fp64 values."""
+    b = bits(rng, (G, N, K), 0.02)
+    q = lp.lp_b128_quant(bf16_dev(b))
+    c, s = q.codes.cpu().numpy(), q.scales.cpu().numpy()
+    return q, [O.values_blocks(c[g], s[g]) for g in range(G)]
+
+
+def decoded(q):
+    return O.values_cols(q.codes.cpu().numpy()[0], q.scales.cpu().numpy()[0])
+
+
+def decoded_rows(q, ends=None):
+    return O.values_rows(q.codes.cpu().numpy()[0], q.scales.cpu().numpy()[0], ends)
+
+
+# one row to several tiles, sizes off every tile, one long contraction, 256 tiles of 256 x 256
+DENSE = [(1, 16, 16), (1, 512, 2048), (2, 144, 128), (5, 272, 1040), (16, 4096, 512), (17, 400, 400), (33, 128, 144),
+         (64, 272, 272), (65, 528, 656), (128, 128, 128), (129, 272, 400), (300, 1040, 144), (700, 512, 4112),
+         (4096, 4096, 144)]
+
+
+@pytest.mark.parametrize("M,N,K", DENSE)
+def test_dense_products(lp, M, N, K):
+    rng = np.random.default_rng(M + N + K)
+    w, wv = weight(lp, rng, 1, N, K)
+    x, g = bf16_dev(bits(rng, (M, K))), bf16_dev(bits(rng, (M, N), 1e-3))
+    xc, xr = lp.lp_r128_quant_dual(x)
+    gc, gr = lp.lp_r128_quant_dual(g)
+    assert_product(lp.lp_linear_fwd(xc, w), decoded(xc), wv[0].T, "y")
+    assert_product(lp.lp_linear_fwd_dyn(x, w), decoded(xc), wv[0].T, "y from bf16")
+    dx, _ = lp.lp_linear_bwd(gc, None, w, need_dw=False)
+    assert_product(dx, decoded(gc), wv[0], "dX")
+    _, dw = lp.lp_linear_bwd(gr, xr, None, need_dx=False)
+    assert_product(dw, decoded_rows(gr).T, decoded_rows(xr), "dW")
+
+
+GROUPED = [([5], 16, 16), ([0, 0, 3], 144, 128), ([1] * 9, 272, 272), ([0, 1, 127, 128, 129, 0, 300, 5], 272, 400),
+           ([2, 0, 1, 4] * 80, 128, 144), ([900, 30, 0, 600, 257], 1040, 272), ([2500, 1500, 0, 97], 4096, 144)]
+
+
+@pytest.mark.parametrize("sizes,N,K", GROUPED)
+@pytest.mark.parametrize("tail", [0, 19])
+def test_grouped_products(lp, sizes, N, K, tail):
+    """Against the oracle per group; rows past the last offset are neither read (they hold NaN codes) nor written,
+    an empty group's grad_W is zero."""
+    rng = np.random.default_rng(sum(sizes) + N)
+    M, G, ends = sum(sizes) + tail, len(sizes), ends_of(sizes)
+    live = int(ends[-1])
+    w, wv = weight(lp, rng, G, N, K)
+    off = dev(ends)
+    xb, gb = bits(rng, (M, K)), bits(rng, (M, N), 1e-3)
+    xb[live:], gb[live:] = 0x7FC0, 0x7FC0
+    x, g = bf16_dev(xb), bf16_dev(gb)
+    xq = lp.lp_r128_quant(x, -1)
+    (gc, gr), (_, xr) = lp.lp_r128_quant_dual(g, off), lp.lp_r128_quant_dual(x, off)
+    for q in (gc, gr, xr):
+        q.codes[0, live:] = 0x7F
+    y, y2, dx = (torch.full((M, n), 3.0, dtype=torch.bfloat16, device="cuda") for n in (N, N, K))
+    dw = torch.full((G, N, K), 3.0, dtype=torch.bfloat16, device="cuda")
+    lp.lp_grouped_fwd(xq, w, off, y=y)
+    lp.lp_grouped_fwd_dyn(x, w, off, y=y2)
+    lp.lp_grouped_bwd(gc, None, w, off, need_dw=False, grad_x=dx)
+    lp.lp_grouped_bwd(gr, xr, None, off, need_dx=False, grad_w=dw)
+    for t in (y, y2, dx):
+        assert (t[live:] == 3).all()
+    xv, gv = decoded(xq), decoded(gc)
+    xrv, grv = decoded_rows(xr, ends), decoded_rows(gr, ends)
+    for k, (a, b) in enumerate(O.groups(M, ends)):
+        if a == b:
+            assert not dw[k].any()
+            continue
+        assert_product(y[a:b], xv[a:b], wv[k].T, f"y of group {k}")
+        assert_product(y2[a:b], xv[a:b], wv[k].T, f"y of group {k} from bf16")
+        assert_product(dx[a:b], gv[a:b], wv[k], f"dX of group {k}")
+        assert_product(dw[k], grv[a:b].T, xrv[a:b], f"dW of group {k}")
+
+
+@pytest.mark.parametrize("M", [1, 40, 200])
+def test_nan_stays_in_its_row_and_column(lp, M):
+    """A NaN in x gives a NaN row, an infinity in the gradient a NaN row of dX and a NaN row of dW, a NaN weight code
+    a NaN column: nothing else."""
+    rng = np.random.default_rng(M)
+    N, K = 272, 400
+    w, _ = weight(lp, rng, 1, N, K)
+    w.codes[0, 7, 3] = 0x7F
+    xb = bits(rng, (M, K))
+    xb[M // 2, 9] = 0x7FC0
+    y = torch.isnan(lp.lp_linear_fwd_dyn(bf16_dev(xb), w).float()).cpu().numpy()
+    want = np.zeros((M, N), bool)
+    want[M // 2], want[:, 7] = True, True
+    assert (y == want).all()
+    w.codes[0, 7, 3] = 0
+    gb = bits(rng, (M, N))
+    gb[M // 2, 5] = 0xFF80
+    gc, gr = lp.lp_r128_quant_dual(bf16_dev(gb))
+    xr = lp.lp_r128_quant(bf16_dev(bits(rng, (M, K))), -2)
+    dx = torch.isnan(lp.lp_linear_bwd(gc, None, w, need_dw=False)[0].float()).cpu().numpy()
+    want = np.zeros((M, K), bool)
+    want[M // 2] = True
+    assert (dx == want).all()
+    dw = torch.isnan(lp.lp_linear_bwd(gr, xr, None, need_dx=False)[1].float()).cpu().numpy()
+    want = np.zeros((N, K), bool)
+    want[5] = True
+    assert (dw == want).all()
+
+
+def test_large_and_small_scales(lp):
+    """Scales near both ends of fp32 meet in one product."""
+    rng = np.random.default_rng(3)
+    w, wv = weight(lp, rng, 1, 144, 272)
+    x = bf16_dev(bits(rng, (40, 272), 1e30))
+    w.scales.mul_(1e-28)
+    xq = lp.lp_r128_quant(x, -1)
+    assert_product(lp.lp_linear_fwd(xq, w), decoded(xq), O.values_blocks(w.codes.cpu().numpy()[0], w.scales.cpu().numpy()[0]).T)
+
+
+def test_gradients_against_differences(lp):
+    """L = sum(c * y): dX and dW with grad_out = c (made of E4M3 values, so its quantization is exact) against central
+    differences of L in fp64 in the decoded operands; L is linear in each, so the differences carry no truncation."""
+    rng = np.random.default_rng(11)
+    M, N, K = 37, 144, 272
+    w, wv = weight(lp, rng, 1, N, K)
+    c = E4M3_TABLE[rng.integers(0, 0x7E, (M, N))] * rng.choice([-1.0, 1.0], (M, N))
+    c[:, ::128] = c[0, :] = 448.0                        # every run's and column's largest: scale 1 along both axes
+    g = bf16_dev(W.bf16_bits(c.astype(np.float32)))
+    gc, gr = lp.lp_r128_quant_dual(g)
+    assert np.array_equal(decoded(gc), c) and np.array_equal(decoded_rows(gr), c)
+    x = bf16_dev(bits(rng, (M, K)))
+    xr = lp.lp_r128_quant(x, -2)
+    xv, h = decoded_rows(xr), 2.0 ** -10
+    dx = lp.lp_linear_bwd(gc, None, w, need_dw=False)[0].float().cpu().numpy()
+    dw = lp.lp_linear_bwd(gr, xr, None, need_dx=False)[1].float().cpu().numpy()
+
+    def loss(xx, ww):
+        return float((c * (xx @ ww.T)).sum())
+    for _ in range(25):
+        m, n, k = rng.integers(M), rng.integers(N), rng.integers(K)
+        for got, at, a, mag in ((dx[m, k], (m, k), 0, np.abs(c[m]) @ np.abs(wv[0][:, k])),
+                                (dw[n, k], (n, k), 1, np.abs(c[:, n]) @ np.abs(xv[:, k]))):
+            ops = [[xv.copy(), wv[0].copy()] for _ in range(2)]
+            ops[0][a][at] += h
+            ops[1][a][at] -= h
+            diff = (loss(*ops[0]) - loss(*ops[1])) / (2 * h)
+            noise = 2.0 ** -50 * np.abs(c).sum() * np.abs(wv[0]).max() * K * np.abs(xv).max() / h
+            assert abs(got - diff) <= 2.0 ** -8 * abs(diff) + 2.0 ** -10 * mag + noise
+
+
+def test_other_stream_and_repeated_calls_agree(lp):
+    rng = np.random.default_rng(2)
+    w, _ = weight(lp, rng, 4, 272, 400)
+    x, off = bf16_dev(bits(rng, (260, 400))), dev(ends_of([100, 0, 31, 129]))
+    want = lp.lp_grouped_fwd_dyn(x, w, off)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = [lp.lp_grouped_fwd_dyn(x, w, off) for _ in range(5)]
+    s.synchronize()
+    assert all(torch.equal(want, t) for t in got)
+
+
+# ---------------------------------------------------------------- AdamW
+
+def f32(x):
+    return np.asarray(x, np.float32)
+
+
+def adamw_f32(p, g, m, v, lr, b1, b2, eps, step, wd):
+    """The stated fp32 operations one by one (numpy rounds each)."""
+    m = f32(m * f32(b1)) + f32(g * f32(1 - b1))
+    v = f32(v * f32(b2)) + f32(f32(g * g) * f32(1 - b2))
+    r = np.sqrt(v)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        u = m / f32(f32(r * f32(1 / np.sqrt(1 - b2 ** step))) + f32(eps))
+    return f32(p * f32(1 - lr * wd)) - f32(u * f32(lr / (1 - b1 ** step))), m, v, r
+
+
+HYPER = dict(lr=3e-3, beta1=0.9, beta2=0.99, eps=1e-8)
+SIZES = [1, 5, 127, 128, 129, 1000, 4096, 4097, 20000]
+
+
+def adam_inputs(rng, n, first=False):
+    mag = np.exp(rng.standard_normal(n) * 2)
+    p, g = f32(rng.standard_normal(n)), W.bf16_bits(f32(rng.standard_normal(n) * 1e-3 * mag))
+    m = f32(np.zeros(n) if first else rng.standard_normal(n) * 1e-3 * mag)
+    r = f32(np.zeros(n) if first else np.abs(rng.standard_normal(n)) * 1e-3 * mag)
+    if n > 4:
+        p[2], g[3], m[3], r[3] = 0, 0, 0, 0
+    return p, g, m, r
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+@pytest.mark.parametrize("grad_bf16", [True, False])
+@pytest.mark.parametrize("param_bf16", [False, True])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_adamw_bit_exact(lp, bits8, grad_bf16, param_bf16, shift):
+    """Many tensors of odd sizes at once (more than one launch takes), aligned or one element off; against the fp32
+    operations one by one, and their distance from the fp64 formula."""
+    rng = np.random.default_rng(7 + shift)
+    step, wd = 3, 0.1
+    tensors, want = {k: [] for k in ("p", "g", "m", "v", "ms", "vs", "copy")}, []
+    for n in SIZES * 7:
+        p, gb, m, r = adam_inputs(rng, n)
+        if param_bf16:
+            p = f32(bf16_bits_to_f64(W.bf16_bits(p)))
+        g = f32(bf16_bits_to_f64(gb))
+
+        def put(a, dtype):
+            buf = torch.zeros(n + shift, dtype=dtype, device="cuda")
+            buf[shift:] = a.to(dtype)
+            return buf[shift:]
+        tensors["p"].append(put(torch.from_numpy(p), torch.bfloat16 if param_bf16 else torch.float32))
+        tensors["g"].append(put(torch.from_numpy(g), torch.bfloat16 if grad_bf16 else torch.float32))
+        tensors["copy"].append(torch.zeros(n, dtype=torch.bfloat16, device="cuda"))
+        if bits8:
+            mc, ms = O.quant_state(m.astype(np.float64))
+            rc, rs = O.quant_state(r.astype(np.float64), keep=True)
+            m, r = f32(O.state_values(mc, ms)), f32(O.state_values(rc, rs))
+            tensors["m"].append(put(torch.from_numpy(mc), torch.uint8))
+            tensors["v"].append(put(torch.from_numpy(rc), torch.uint8))
+            tensors["ms"].append(dev(ms))
+            tensors["vs"].append(dev(rs))
+        else:
+            tensors["m"].append(put(torch.from_numpy(m), torch.float32))
+            tensors["v"].append(put(torch.from_numpy(r * r), torch.float32))
+        new = adamw_f32(p, g, m, r * r, step=step, wd=wd, lr=HYPER["lr"], b1=0.9, b2=0.99, eps=1e-8)
+        want.append((p, g, m, r, new))
+    plan = lp.AdamWPlan(tensors["p"], tensors["g"], tensors["m"], tensors["v"],
+                        exp_avg_scales=tensors["ms"] if bits8 else None,
+                        exp_avg_sq_scales=tensors["vs"] if bits8 else None,
+                        copies=None if param_bf16 else tensors["copy"], weight_decay=wd)
+    lp.lp_adamw(plan, step=step, **HYPER)
+    for i, (p, g, m, r, (np_, nm, nv, nr)) in enumerate(want):
+        n = p.size
+        got = tensors["p"][i].float().cpu().numpy()
+        if param_bf16:
+            assert_bits_equal(bits_host(tensors["p"][i]), f32_to_bf16_bits(np_), f"p {i} of {n}")
+        else:
+            assert_bits_equal(got.view(np.uint32), np_.view(np.uint32), f"p {i} of {n}")
+            assert_bits_equal(bits_host(tensors["copy"][i]), f32_to_bf16_bits(np_), "copy")
+            ref = O.adamw(p.astype(np.float64), g, m.astype(np.float64), r.astype(np.float64) ** 2, step=step,
+                          weight_decay=wd, **HYPER)[0]
+            # the step has magnitude lr m-hat / sqrt(v-hat) and about ten fp32 roundings; p itself two
+            assert (np.abs(got - ref) <= 2.0 ** -22 * np.abs(ref) + 16 * 2.0 ** -24 * (np.abs(ref - p) + np.abs(p) * 1e-3)).all()
+        if bits8:
+            mc, ms = O.quant_state(nm.astype(np.float64))
+            rc, rs = O.quant_state(nr.astype(np.float64), keep=True)
+            assert_bits_equal(tensors["m"][i].cpu().numpy(), mc, f"m codes {i}")
+            assert_bits_equal(tensors["v"][i].cpu().numpy(), rc, f"sqrt(v) codes {i}")
+            assert_bits_equal(f32_bits(tensors["ms"][i]), f32_bits(ms), "m scales")
+            assert_bits_equal(f32_bits(tensors["vs"][i]), f32_bits(rs), "sqrt(v) scales")
+        else:
+            assert_bits_equal(tensors["m"][i].cpu().numpy().view(np.uint32), nm.view(np.uint32), "m")
+            assert_bits_equal(tensors["v"][i].cpu().numpy().view(np.uint32), nv.view(np.uint32), "v")
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+def test_adamw_first_step_from_zero_state_and_grad_scale(lp, bits8):
+    """From all-zero moments the first step moves every parameter with a gradient by lr, whatever the gradient's size;
+    elements without one only decay.  grad_scale multiplies the gradient."""
+    n = 1000
+    rng = np.random.default_rng(1)
+    p, gb, _, _ = adam_inputs(rng, n, first=True)
+    g = f32(bf16_bits_to_f64(gb))
+    t = [torch.zeros(n, dtype=torch.uint8 if bits8 else torch.float32, device="cuda") for _ in range(2)]
+    s = [[torch.zeros(8, device="cuda")] for _ in range(2)] if bits8 else [None, None]
+    pt, scale = dev(p), torch.tensor([1024.0], device="cuda")
+    plan = lp.AdamWPlan([pt], [bf16_dev(gb)], [t[0]], [t[1]], exp_avg_scales=s[0], exp_avg_sq_scales=s[1], weight_decay=0.1)
+    lp.lp_adamw(plan, lr=0.01, eps=0.0, step=1, grad_scale=scale)
+    got = pt.cpu().numpy()
+    want = np.where(g == 0, np.nan, p * (1 - 0.001) - 0.01 * np.sign(g))     # eps = 0: 0 / 0 where there is no gradient
+    ok = g != 0
+    assert np.allclose(got[ok], want[ok], rtol=0, atol=1e-6)
+    assert np.isnan(got[~ok]).all()
+    if not bits8:
+        assert np.allclose(t[0].cpu().numpy(), 102.4 * g, rtol=1e-5)
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+def test_adamw_nan_gradient_and_long_run(lp, bits8):
+    """A NaN gradient reaches its own element (fp32 moments) or its own run of 128 (8-bit moments) and no other; many
+    steps on a quadratic bowl reach its bottom."""
+    n = 512
+    p = torch.ones(n, device="cuda")
+    g = torch.full((n,), 0.5, device="cuda")
+    g[200] = float("nan")
+    m, v = (torch.zeros(n, dtype=torch.uint8 if bits8 else torch.float32, device="cuda") for _ in range(2))
+    s = [[torch.zeros(4, device="cuda")] for _ in range(2)] if bits8 else [None, None]
+    plan = lp.AdamWPlan([p], [g], [m], [v], exp_avg_scales=s[0], exp_avg_sq_scales=s[1])
+    lp.lp_adamw(plan, lr=0.01, step=1)
+    lp.lp_adamw(plan, lr=0.01, step=2)
+    bad = torch.isnan(p).cpu().numpy()
+    want = np.zeros(n, bool)
+    want[128:256 if bits8 else 128] = True
+    want[200] = True
+    assert (bad == want).all()
+    target = torch.randn(n, device="cuda")
+    p, m, v = torch.zeros(n, device="cuda"), torch.zeros_like(m), torch.zeros_like(v)
+    s = [[torch.zeros(4, device="cuda")] for _ in range(2)] if bits8 else [None, None]
+    g = torch.zeros(n, device="cuda")
+    plan = lp.AdamWPlan([p], [g], [m], [v], exp_avg_scales=s[0], exp_avg_sq_scales=s[1])
+    for k in range(1, 401):
+        torch.sub(p, target, out=g)
+        lp.lp_adamw(plan, lr=0.05 * (1 - k / 401), beta2=0.95, step=k)
+    assert (p - target).abs().max().item() < 0.05
+
+
+def test_adamw_set_grads_and_empty(lp):
+    p = torch.ones(10, device="cuda")
+    z = lambda: torch.zeros(10, device="cuda")  # noqa: E731
+    plan = lp.AdamWPlan([p], [z()], [z()], [z()])
+    lp.lp_adamw(plan, lr=0.1, step=1)
+    assert (p == 1).all()
+    plan.set_grads([torch.ones(10, dtype=torch.bfloat16, device="cuda")])
+    lp.lp_adamw(plan, lr=0.1, step=1)
+    assert torch.allclose(p, torch.full_like(p, 0.9), atol=1e-6)
+    e = torch.zeros(0, device="cuda")
+    lp.lp_adamw(lp.AdamWPlan([e], [e], [e], [e]), lr=0.1)
+    lp.lp_adamw(lp.AdamWPlan([], [], [], []), lr=0.1)
+    torch.cuda.synchronize()
