@@ -26,17 +26,19 @@
 // A 128-deep stage of both operands and its scales goes from global memory
 // straight into LDS, two stages deep; one barrier per stage.  LDS layouts:
 // * contraction contiguous in memory (x and W in fwd, the gradient in dX):
-//   [row][128 B], 16-byte chunk c of row r at c ^ ((r >> 1) & 7), so that
-//   the 16 rows a read serves together fall in distinct 16-byte slots of
-//   256 bytes;
+//   [row][128 B], 16-byte chunk c of row r at c ^ ((r >> 1) & 7);
 // * contraction along the rows (W in dX, both operands in dW): [k][columns],
 //   read with the transposing ds_read_b64_tr_b8, whose 32 lanes read rows
-//   n0 .. n0+7 and n0+32 .. n0+39 of one chunk; chunk c of row n is at
-//   c ^ swz_cols(n), which makes those 16 slots distinct.
-// Lane l of the MFMA holds row (column) l % 16 of its operand and the 32
-// contraction bytes 32 (l / 16) .. + 31; both operands use the same order,
-// so any order inside the instruction gives the same sum.  The result is
-// D[q][p]: lane l holds column p = l % 16 and rows q = 4 (l / 16) .. + 3.
+//   n0 .. n0+7 and n0+16 .. n0+23 of one chunk; chunk c of row n is at
+//   c ^ swz_cols(n), which puts them in distinct 16-byte slots of 256 bytes.
+// Lane l of the MFMA holds row (column) l % 16 of its operand and, h = l / 16,
+// the contraction bytes 16 h .. + 15 and 64 + 16 h .. + 15.  Any order inside
+// the instruction gives the same sum as long as both operands use it; this one
+// reads neighbouring 16-byte chunks in neighbouring lane rows, because the
+// 16 lanes that a 16-byte LDS read serves together are 0-3, 12-15, 20-27 (and
+// so on): with chunks 2 h and 2 h + 1 instead, 45% of the LDS cycles of the
+// forward were bank conflicts.  The result is D[q][p]: lane l holds column
+// p = l % 16 and rows q = 4 (l / 16) .. + 3.
 #pragma once
 
 #include "lp_gemm_kernel.hpp"
@@ -69,7 +71,7 @@ using B128 = BCfg<128, 128, 64, 64>;
 // Chunk swizzle of a [k][kCols bytes] tile (see above).
 template <int kCols>
 __device__ __forceinline__ int swz_cols(int n) {
-  return (kCols == 256 ? 2 * (n & 7) : 2 * ((n >> 1) & 3)) ^ ((n >> 5) & 1);
+  return (kCols == 256 ? 2 * (n & 7) : 2 * ((n >> 1) & 3)) ^ ((n >> 4) & 1);
 }
 
 // Direct loads of one operand.  kKMajor: kMN rows of 128 bytes; otherwise
@@ -79,8 +81,9 @@ struct B128Loader {
   const uint8_t* base;      // first byte of the tile's rows (k-major) or of the tensor's group
   int64_t bytes;            // k-major: bytes from base to the end of the tile's rows
   int32_t ld;
-  int32_t off[2];           // lane offset of even and odd blocks
+  int32_t off[2];           // lane offset of blocks of either parity (128 columns: of blocks 0, 1 and 2, 3)
   int32_t kcol[2];          // k-major: the lane's first column in the stage
+  static constexpr int kStep = !kKMajor && kMN == 128 ? 2 : 1;   // blocks between the two offsets
   int32_t lds;
 
   __device__ __forceinline__ void init(const Op& op, int g, int mn0, int mnend, int wave, int lane) {
@@ -101,9 +104,9 @@ struct B128Loader {
       constexpr int LPR = kMN / 16, RPB = 64 / LPR;               // lanes per row, rows per block
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
-        const int n = RPB * (4 * wave + o) + lane / LPR;
+        const int n = RPB * (4 * wave + kStep * o) + lane / LPR;
         kcol[o] = 0;
-        off[o] = (n - RPB * o) * ld + mn0 + 16 * ((lane % LPR) ^ swz_cols<kMN>(n));
+        off[o] = (n - RPB * kStep * o) * ld + mn0 + 16 * ((lane % LPR) ^ swz_cols<kMN>(n));
       }
     }
   }
@@ -115,7 +118,7 @@ struct B128Loader {
       dma<16>(r, (lds_void*)(dst + lds + 1024 * u), k0 + kcol[u & 1] >= kend ? kOOB : off[u & 1], 8 * u * ld);
     } else {
       const Rsrc r = make_rsrc(base + (int64_t)k0 * ld, (int64_t)(kend - k0) * ld);
-      dma<16>(r, (lds_void*)(dst + lds + 1024 * u), off[u & 1], (1024 / kMN) * u * ld);
+      dma<16>(r, (lds_void*)(dst + lds + 1024 * u), off[u / kStep & 1], (1024 / kMN) * u * ld);
     }
   }
 };
@@ -127,9 +130,9 @@ struct B128Frag {
   __device__ __forceinline__ void init(int mn, int lane) {       // mn: the wave's first row (column), a multiple of 64
     const int r = lane & 15, h = lane >> 4;
     if constexpr (kKMajor) {
-      a = (mn + r) * kRun + 16 * ((2 * h) ^ ((r >> 1) & 7));
+      a = (mn + r) * kRun + 16 * (h ^ ((r >> 1) & 7));
     } else {
-      const int n = 32 * h + r / 2;
+      const int n = 16 * h + r / 2;
       a = n * kMN + 16 * ((mn / 16) ^ swz_cols<kMN>(n)) + 8 * (r & 1);
     }
   }
@@ -139,14 +142,14 @@ struct B128Frag {
     if constexpr (kKMajor) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(tile + (a ^ (16 * e)) + f * 16 * kRun);
+        const u32x4 x = *reinterpret_cast<const u32x4*>(tile + (a ^ (64 * e)) + f * 16 * kRun);
 #pragma unroll
         for (int d = 0; d < 4; ++d) v[4 * e + d] = (int)x[d];
       }
     } else {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const i32x2b x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2b*)(tile + (a ^ (16 * f)) + 8 * t * kMN));
+        const i32x2b x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2b*)(tile + (a ^ (16 * f)) + (64 * (t / 2) + 8 * (t % 2)) * kMN));
         v[2 * t] = x[0];
         v[2 * t + 1] = x[1];
       }
@@ -203,11 +206,16 @@ __global__ __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2
     slen = kQK ? (qb * kRun < p.Qtot ? 4 : 0) : p.Q.scale_ld;
   }
 
-  auto issue = [&](uint8_t* sb, int kb) {
+  const int nk = (kend - kbeg + kRun - 1) / kRun;
+  // Load u of stage kb: blocks of P, blocks of Q, scales.  Stages at or past
+  // the end of the contraction read nothing (zeros).
+  constexpr int kLoads = C::PB + C::QB + 1;
+  auto issue = [&](auto ui, uint8_t* sb, int kb) {
+    constexpr int u = decltype(ui)::value;
     const int k0 = kbeg + kb * kRun;
-    static_for<C::PB>([&](auto u) { lp.template load<decltype(u)::value>(sb + C::kP, k0, kend); });
-    static_for<C::QB>([&](auto u) { lq.template load<decltype(u)::value>(sb + C::kQ, k0, kend); });
-    dma<4>(make_rsrc(sbase + kb * sstep, slen), (lds_void*)(sb + C::kPS + 256 * wave), soff, 0);
+    if constexpr (u < C::PB) lp.template load<u>(sb + C::kP, k0, kend);
+    else if constexpr (u < C::PB + C::QB) lq.template load<u - C::PB>(sb + C::kQ, k0, kend);
+    else dma<4>(make_rsrc(sbase + kb * sstep, kb < nk ? slen : 0), (lds_void*)(sb + C::kPS + 256 * wave), soff, 0);
   };
 
   B128Frag<kPK, C::BP> fp;
@@ -223,56 +231,75 @@ __global__ __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2
 #pragma unroll
     for (int j = 0; j < C::FQ; ++j) acc[i][j] = f32x4{};
 
-  // One stage: FP x FQ MFMAs, the products of MFMA m added to the sums
-  // after MFMA m + kLag has been issued.
+  // One stage: FP x FQ MFMAs (rows of FQ), the products of MFMA m added to
+  // the sums after MFMA m + kLag has been issued.  P fragments are read kAhead
+  // rows early; once the stage's last one is in registers, in row kSync, one
+  // barrier says both that every wave is done with this buffer and that the
+  // next stage has landed.  The rows that remain cover the next stage's first
+  // reads: P's first fragments and each Q fragment after its last MFMA.  The
+  // loads of the stage after that go into this buffer, one per MFMA from the
+  // barrier on: a wave that issues them in one go waits for the memory
+  // pipeline to take them, with its MFMAs behind them.
   constexpr int kLag = 2, kRing = kLag + 1, NM = C::FP * C::FQ;
-  auto compute = [&](const uint8_t* sb) {
-    i32x8b q[C::FQ], pf[2];
-    float sp[C::FP];
+  constexpr int kAhead = 1, kSlots = 2 * kAhead, kSync = C::FP - kAhead;
+  constexpr int kEarly = NM - kSync * C::FQ < kLoads ? NM - kSync * C::FQ : kLoads;   // loads before the stage's end
+  static_assert(C::FP % kSlots == 0, "a row's slot is the same in every stage");
+  i32x8b q[C::FQ], pf[kSlots];
+  if (nk > 0) {
+    static_for<kLoads>([&](auto u) { issue(u, smem, 0); });
+    static_for<kEarly>([&](auto u) { issue(u, smem + C::STAGE, 1); });
+    barrier_vm<kEarly>();
+    static_for<kAhead>([&](auto i) { pf[decltype(i)::value] = fp.template read<decltype(i)::value>(smem + C::kP); });
+    static_for<C::FQ>([&](auto j) { q[decltype(j)::value] = fq.template read<decltype(j)::value>(smem + C::kQ); });
+  }
+  int cur = 0;
+  for (int kb = 0; kb < nk; ++kb) {
+    uint8_t* const sb = smem + cur;
+    uint8_t* const nx = smem + (C::STAGE - cur);
+    float sp[C::FP], w;
     f32x4 sq[kDW ? C::FQ : 1];
-    f32x4 part[kRing];
-    pf[0] = fp.template read<0>(sb + C::kP);
-    static_for<C::FQ>([&](auto j) { q[decltype(j)::value] = fq.template read<decltype(j)::value>(sb + C::kQ); });
 #pragma unroll
     for (int i = 0; i < C::FP; ++i) sp[i] = *reinterpret_cast<const float*>(sb + psa + 64 * i);
     if constexpr (kDW) {
 #pragma unroll
       for (int j = 0; j < C::FQ; ++j) sq[j] = *reinterpret_cast<const f32x4*>(sb + qsa + 64 * j);
     } else {
-      const float w = *reinterpret_cast<const float*>(sb + qsa);
-#pragma unroll
-      for (int i = 0; i < C::FP; ++i) sp[i] *= w;
+      w = *reinterpret_cast<const float*>(sb + qsa);
     }
+    f32x4 part[kRing];
     static_for<NM + kLag>([&](auto mi) {
       constexpr int m = decltype(mi)::value;
+      constexpr int i = m / C::FQ, j = m % C::FQ;
+      if constexpr (m == kSync * C::FQ) barrier_vm<0>();
       if constexpr (m < NM) {
-        constexpr int i = m / C::FQ, j = m % C::FQ;
-        if constexpr (j == 0 && i + 1 < C::FP) pf[(i + 1) & 1] = fp.template read<i + 1>(sb + C::kP);
-        part[m % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q[j], pf[i & 1], f32x4{}, 0, 0, 0, 127, 0, 127);
+        if constexpr (j == 0) {
+          constexpr int n = i + kAhead;
+          if constexpr (n < C::FP) pf[n % kSlots] = fp.template read<n>(sb + C::kP);
+          else pf[n % kSlots] = fp.template read<n - C::FP>(nx + C::kP);
+        }
+        part[m % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q[j], pf[i % kSlots], f32x4{}, 0, 0, 0, 0, 0, 0);
+        if constexpr (i == C::FP - 1) q[j] = fq.template read<j>(nx + C::kQ);
+        if constexpr (m >= kSync * C::FQ && m - kSync * C::FQ < kEarly) {
+          issue(IC<m - kSync * C::FQ>{}, sb, kb + 2);
+        }
+        if constexpr (m < kLoads - kEarly) {
+          issue(IC<m + kEarly>{}, nx, kb + 1);
+        }
       }
       if constexpr (m >= kLag) {
-        constexpr int d = m - kLag, i = d / C::FQ, j = d % C::FQ;
+        constexpr int d = m - kLag, di = d / C::FQ, dj = d % C::FQ;
+        if constexpr (!kDW && dj == 0) sp[di] *= w;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float s = kDW ? sp[i] * sq[kDW ? j : 0][r] : sp[i];
-          acc[i][j][r] = __builtin_fmaf(part[d % kRing][r], s, acc[i][j][r]);
+          const float f = kDW ? sp[di] * sq[kDW ? dj : 0][r] : sp[di];
+          acc[di][dj][r] = __builtin_fmaf(part[d % kRing][r], f, acc[di][dj][r]);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     });
-  };
-
-  const int nk = (kend - kbeg + kRun - 1) / kRun;
-  if (nk > 0) issue(smem, 0);
-  int cur = 0;
-  for (int kb = 0; kb < nk; ++kb) {
-    // Stage kb landed everywhere, and every wave is done with the other buffer.
-    barrier_vm<0>();
-    if (kb + 1 < nk) issue(smem + (C::STAGE - cur), kb + 1);
-    compute(smem + cur);
     cur = C::STAGE - cur;
   }
-  __syncthreads();
+  barrier_vm<0>();                                               // the last loads (zeros) have landed
 
   // bf16 results through LDS, so that each row of the wave tile is stored as
   // one 128-byte line: 8-byte slot s of row r at s ^ (r & 15).
