@@ -303,8 +303,10 @@ hipError_t launch_gemm(const GemmCall& call, hipStream_t stream) {
   return launch_cfg<Narrow>(call, prm, stream);
 }
 
-hipError_t launch_fwd(const lp_qtensor& x, const lp_qtensor& w, const int32_t* offsets, int32_t groups, void* y,
-                      hipStream_t stream) {
+namespace {
+
+// Shapes and operands of a forward.
+Params fwd_params(const lp_qtensor& x, const lp_qtensor& w, const int32_t* offsets, int32_t groups, void* y) {
   Params prm{};
   prm.P = make_op(x);
   prm.Q = make_op(w);
@@ -316,7 +318,23 @@ hipError_t launch_fwd(const lp_qtensor& x, const lp_qtensor& w, const int32_t* o
   prm.offsets = offsets;
   prm.groups = groups;
   prm.splits = 1;
+  return prm;
+}
+
+// Row tiles of 16 for the forward that streams the weight (1, 2 or 4), 0 when
+// the tile kernels are the better choice.
+int skinny_tiles(const Params& prm) {
+  const int64_t rows = prm.offsets ? (prm.Ptot + prm.groups - 1) / prm.groups : prm.Ptot;   // mean rows of a group
+  return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 0;
+}
+
+}  // namespace
+
+hipError_t launch_fwd(const lp_qtensor& x, const lp_qtensor& w, const int32_t* offsets, int32_t groups, void* y,
+                      hipStream_t stream) {
+  Params prm = fwd_params(x, w, offsets, groups, y);
   if (x.fmt == LP_FP8_R128) {
+    if (const int t = skinny_tiles(prm)) return b128_fwd_skinny(prm, t, stream);
     const bool big = b128_big(prm, false);
     b128_tiles(prm, big ? 256 : 128, false);
     return b128_fwd(prm, big, stream);
@@ -340,6 +358,8 @@ hipError_t launch_fwd(const lp_qtensor& x, const lp_qtensor& w, const int32_t* o
 
 hipError_t launch_fwd_dyn(const void* x, const lp_qtensor& xq, const lp_qtensor& w, const int32_t* offsets,
                           int32_t groups, void* x_codes, void* x_scales, void* y, hipStream_t stream) {
+  const Params prm = fwd_params(xq, w, offsets, groups, y);
+  if (b128_can_fuse(prm)) return b128_fwd_fused(prm, x, stream);
   if (xq.cols > 0) {
     const hipError_t e = launch_r128_cols(x, 1, xq.rows, xq.cols, x_codes, x_scales, stream);
     if (e != hipSuccess) return e;

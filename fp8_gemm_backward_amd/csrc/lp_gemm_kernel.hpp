@@ -1007,6 +1007,13 @@ hipError_t dec_pair(const Params& dx, const Params& dw, int fmt_q, hipStream_t s
 // Products of E4M3 operands with fp32 scales per 128, on 256 x 256 (big) or
 // 128 x 128 tiles.
 hipError_t b128_fwd(const Params& prm, bool big, hipStream_t s);
+// The forward of few rows: row tiles of 16 `tiles` (1, 2 or 4) rows; and from
+// a bf16 x of at most kFuseRows rows that the kernel quantizes itself, when
+// b128_can_fuse says so.
+constexpr int kFuseRows = 4;
+hipError_t b128_fwd_skinny(const Params& prm, int tiles, hipStream_t s);
+bool b128_can_fuse(const Params& prm);
+hipError_t b128_fwd_fused(const Params& prm, const void* x, hipStream_t s);
 hipError_t b128_dx(const Params& prm, bool big, hipStream_t s);
 hipError_t b128_dw(const Params& prm, bool big, hipStream_t s);
 
