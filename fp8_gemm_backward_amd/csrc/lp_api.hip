@@ -53,6 +53,7 @@ lp_status check_tensor(const lp_qtensor* t) {
   if (t->cols % 16) return LP_ERR_SHAPE;
   if ((t->fmt == LP_MXFP4 || (t->fmt == LP_MXFP8 && axis == -1)) && t->cols % 32) return LP_ERR_SHAPE;
   if (t->fmt == LP_MXFP8 && axis == -2 && t->rows % 32) return LP_ERR_SHAPE;
+  if (t->fmt == LP_FP8_R128 && t->rows >= (int64_t)1 << 29) return LP_ERR_SHAPE;   // a run's scales span < 2^31 bytes
   int64_t n = 0;
   if (!count_ok(t->batch, t->rows, t->cols, &n)) return LP_ERR_SHAPE;
   if (n == 0) return LP_OK;

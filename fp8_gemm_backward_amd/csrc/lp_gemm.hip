@@ -1,6 +1,7 @@
 // Host side of the fused backward GEMMs: operand descriptors, tile-size
 // choice and dispatch to the per-format kernel instantiations.
 #include "lp_gemm_kernel.hpp"
+#include <cstdlib>
 
 namespace lp {
 namespace gk {
@@ -264,11 +265,37 @@ void b128_tiles(Params& prm, int b, bool dw) {
   prm.ntiles = (int32_t)(pt * prm.nq);
 }
 
-// Whether 256 x 256 tiles make enough workgroups for the GPU.
-bool b128_big(const Params& prm, bool dw) {
-  Params t = prm;
-  b128_tiles(t, 256, dw);
-  return t.ntiles >= kCUs;
+// Grouped grad_X and forward split by dispatch round, as tile_split does.
+// (Measured with the split / without: 16384 rows over 8 experts, forward 2048 x
+// 4096 TODO.)
+bool b128_split(Params& prm) {
+  if (prm.offsets == nullptr || prm.ntiles < kCUs || getenv("NOTAIL")) return false;
+  prm.tail = 1;
+  return true;
+}
+
+// The tile size of a product with fp32 scales per 128: the least estimated
+// time of one contraction stage over all dispatch rounds, in units of 10 ns
+// (measured per stage and round: 256 x 256 tiles 1.35 us, 128 x 128 0.50 us for
+// up to 128 tiles and 0.62 us above, 64 x 64 0.20 and 0.28 us; a second round
+// of 64 x 64 tiles lost to 128 x 128 in every case).  Grouped grad_X and
+// grad_W keep 256 x 256 unless 128 x 128 fits one round: their narrow tiles
+// read or write 128-byte pieces of long rows (64 experts of 2048 x 7168, 1024
+// tokens: grad_X 293 us on 256 x 256 tiles, 377 us on 128 x 128).
+enum class B128Op { kFwd, kDx, kDw };
+int b128_tile(const Params& prm, B128Op op) {
+  if (const char* e = getenv("LPT")) return atoi(e);
+  auto count = [&](int b) {
+    Params t = prm;
+    b128_tiles(t, b, op == B128Op::kDw);
+    return (int64_t)t.ntiles;
+  };
+  const int64_t t256 = count(256), t128 = count(128), t64 = count(64);
+  const bool one_round = prm.offsets != nullptr && op != B128Op::kFwd;
+  const int64_t c256 = 135 * ((t256 + kCUs - 1) / kCUs);
+  const int64_t c128 = t128 <= kCUs / 2 ? 50 : one_round && t128 > kCUs ? INT64_MAX : 62 * ((t128 + kCUs - 1) / kCUs);
+  const int64_t c64 = t64 <= kCUs / 2 ? 20 : t64 <= kCUs ? 28 : INT64_MAX;
+  return c64 <= c128 && c64 <= c256 ? 64 : c128 <= c256 ? 128 : 256;
 }
 
 }  // namespace
@@ -276,9 +303,12 @@ bool b128_big(const Params& prm, bool dw) {
 hipError_t launch_gemm(const GemmCall& call, hipStream_t stream) {
   if (native_b128(call)) {
     Params prm = base_params(call);
-    const bool big = b128_big(prm, call.dw);
-    b128_tiles(prm, big ? 256 : 128, call.dw);
-    return call.dw ? b128_dw(prm, big, stream) : b128_dx(prm, big, stream);
+    const int tile = b128_tile(prm, call.dw ? B128Op::kDw : B128Op::kDx);
+    b128_tiles(prm, tile, call.dw);
+    if (call.dw) return b128_dw(prm, tile, stream);
+    const bool split = tile == 256 && b128_split(prm);
+    const hipError_t e = b128_dx(prm, tile, stream);
+    return e != hipSuccess || !split ? e : b128_dx_tail(tail_params(prm), stream);
   }
   if (native_mx(call) || native_pt(call)) {
     const Params prm = native_params(call);
@@ -321,11 +351,12 @@ Params fwd_params(const lp_qtensor& x, const lp_qtensor& w, const int32_t* offse
   return prm;
 }
 
-// Row tiles of 16 for the forward that streams the weight (1, 2 or 4), 0 when
-// the tile kernels are the better choice.
-int skinny_tiles(const Params& prm) {
-  const int64_t rows = prm.offsets ? (prm.Ptot + prm.groups - 1) / prm.groups : prm.Ptot;   // mean rows of a group
-  return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 0;
+// Whether the forward streams the weight past a few rows: up to 16 rows, or
+// 8 in a group's mean.  (16 x 4096 x 4096: 7.5 us against 8.8 us on 64 x 64
+// tiles, 32 rows 10.2 against 8.7; 64 experts of 2048 x 7168: 512 tokens 196 to
+// 235 us against 249 to 259 on 128 x 128 tiles, 1024 tokens 330 against 262.)
+bool skinny(const Params& prm) {
+  return prm.offsets ? prm.Ptot <= 8 * (int64_t)prm.groups : prm.Ptot <= 16;
 }
 
 }  // namespace
@@ -334,10 +365,12 @@ hipError_t launch_fwd(const lp_qtensor& x, const lp_qtensor& w, const int32_t* o
                       hipStream_t stream) {
   Params prm = fwd_params(x, w, offsets, groups, y);
   if (x.fmt == LP_FP8_R128) {
-    if (const int t = skinny_tiles(prm)) return b128_fwd_skinny(prm, t, stream);
-    const bool big = b128_big(prm, false);
-    b128_tiles(prm, big ? 256 : 128, false);
-    return b128_fwd(prm, big, stream);
+    if (skinny(prm)) return b128_fwd_skinny(prm, stream);
+    const int tile = b128_tile(prm, B128Op::kFwd);
+    b128_tiles(prm, tile, false);
+    const bool split = tile == 256 && b128_split(prm);
+    const hipError_t e = b128_fwd(prm, tile, stream);
+    return e != hipSuccess || !split ? e : b128_fwd_tail(tail_params(prm), stream);
   }
   // MX operands run on the block-scaled MFMA (256 x 256 tiles); the others
   // through bf16 tiles, 256 x 256 unless both are bf16 (256 x 128: three

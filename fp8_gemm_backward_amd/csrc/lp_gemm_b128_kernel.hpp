@@ -54,72 +54,97 @@ enum : int { kB128Fwd = 0, kB128Dx = 1, kB128Dw = 2 };
 
 constexpr int kRun = 128;                       // contraction elements per scale
 
-template <int kBP, int kBQ, int kWP, int kWQ>
+template <int kBP, int kBQ, int kWP, int kWQ, int kStages, int kSplit = 1>
 struct BCfg {
+  static constexpr int NS = kStages;                             // LDS stages
+  static constexpr int KW = kSplit;                              // groups of waves that share the contraction
   static constexpr int BP = kBP, BQ = kBQ, WP = kWP, WQ = kWQ;
   static constexpr int NWQ = BQ / WQ, NW = (BP / WP) * NWQ;
   static constexpr int FP = WP / 16, FQ = WQ / 16;
   static constexpr int PB = BP * kRun / 1024 / NW, QB = BQ * kRun / 1024 / NW;   // 1 KiB loads per wave and stage
   static constexpr int kP = 0, kQ = BP * kRun, kPS = kQ + BQ * kRun, kQS = kPS + BP * 4;
   static constexpr int STAGE = kQS + BQ * 4;
-  static_assert(NW == BP / 64 + BQ / 64, "one scale load per wave");
-  static_assert(PB == 4 && QB == 4, "load offsets are written for four blocks per wave and operand");
+  static_assert(NW >= BP / 64 + BQ / 64, "one scale load per wave");
 };
-using B256 = BCfg<256, 256, 128, 64>;
-using B128 = BCfg<128, 128, 64, 64>;
+using B256 = BCfg<256, 256, 128, 64, 2>;
+using B256N = BCfg<256, 128, 64, 64, 3>;
+using B128 = BCfg<128, 128, 64, 64, 2, 2>;
+using B64 = BCfg<64, 64, 32, 64, 2, 4>;
 
 // Chunk swizzle of a [k][kCols bytes] tile (see above).
 template <int kCols>
 __device__ __forceinline__ int swz_cols(int n) {
-  return (kCols == 256 ? 2 * (n & 7) : 2 * ((n >> 1) & 3)) ^ ((n >> 4) & 1);
+  const int g = (n >> 4) & 1;
+  return kCols == 256 ? 2 * (n & 7) ^ g : kCols == 128 ? 2 * ((n >> 1) & 3) ^ g : ((n >> 2) & 1) ^ (2 * g);
 }
 
-// Direct loads of one operand.  kKMajor: kMN rows of 128 bytes; otherwise
-// 128 rows of kMN bytes.
-template <bool kKMajor, int kMN>
+// The buffer resource of a window.  Its words must reach the loads' inline
+// assembly from scalar arithmetic (a scalar register written by a vector
+// instruction may be read by a memory instruction only five instructions
+// later, which nothing checks inside inline assembly), so the running
+// addresses below take 32-bit steps and no 64-bit products.
+__device__ __forceinline__ Rsrc window(const uint8_t* base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0, bytes > 0 ? bytes : 0, 0x00020000);
+}
+
+// Direct loads of one operand, stage by stage.  kKMajor: kMN rows of 128
+// bytes; otherwise 128 rows of kMN bytes.  The buffer range of a stage is kept
+// in 32-bit scalars that move on by one stage (a tile's rows span fewer than
+// 2^31 bytes): computed anew with 64-bit clamps for every stage, it cost some
+// 350 cycles a stage.
+// kBlk: 1 KiB blocks per wave (2 or 4).
+template <bool kKMajor, int kMN, int kBlk>
 struct B128Loader {
-  const uint8_t* base;      // first byte of the tile's rows (k-major) or of the tensor's group
-  int64_t bytes;            // k-major: bytes from base to the end of the tile's rows
+  static_assert(kBlk == 2 || kBlk == 4, "the lane offsets below are written for these");
+  const uint8_t* base;      // first byte of the stage's window
+  int32_t bytes;            // k-major: bytes from base to the end of the tile's rows
+  int32_t left;             // contraction elements from the stage's start to the end
   int32_t ld;
   int32_t off[2];           // lane offset of blocks of either parity (128 columns: of blocks 0, 1 and 2, 3)
-  int32_t kcol[2];          // k-major: the lane's first column in the stage
-  static constexpr int kStep = !kKMajor && kMN == 128 ? 2 : 1;   // blocks between the two offsets
+  int32_t kcol;             // k-major: the lane's first column in the stage, even blocks (odd ones: ^ 64)
   int32_t lds;
+  static constexpr int kStep = !kKMajor && kMN == 128 ? 2 : 1;   // blocks between the two offsets
 
-  __device__ __forceinline__ void init(const Op& op, int g, int mn0, int mnend, int wave, int lane) {
+  __device__ __forceinline__ void init(const Op& op, int g, int mn0, int mnend, int kbeg, int kend, int wave, int lane) {
     ld = op.code_ld;
-    lds = 4096 * wave;
+    lds = 1024 * kBlk * wave;
+    left = kend - kbeg;
+    kcol = 0;
+    base = op.codes + (int64_t)g * op.code_batch;
     if constexpr (kKMajor) {
-      base = op.codes + (int64_t)g * op.code_batch + (int64_t)mn0 * ld;
-      bytes = (int64_t)(mnend - mn0) * ld;
-#pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const int row = 8 * (4 * wave + o) + lane / 8;
-        kcol[o] = 16 * ((lane & 7) ^ ((row >> 1) & 7));
-        off[o] = row * ld + kcol[o] - 8 * o * ld;                 // + 8 u ld
-      }
+      base += (int64_t)mn0 * ld + kbeg;
+      bytes = (mnend - mn0 < kMN ? mnend - mn0 : kMN) * ld - kbeg;
+      const int row = 8 * kBlk * wave + lane / 8;
+      kcol = 16 * ((lane & 7) ^ ((row >> 1) & 7));
+      off[0] = row * ld + kcol;                                  // + 8 u ld
+      off[1] = row * ld + (kcol ^ 64);
     } else {
-      base = op.codes + (int64_t)g * op.code_batch;
+      base += (int64_t)kbeg * ld;
       bytes = 0;
       constexpr int LPR = kMN / 16, RPB = 64 / LPR;               // lanes per row, rows per block
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
-        const int n = RPB * (4 * wave + kStep * o) + lane / LPR;
-        kcol[o] = 0;
+        const int n = RPB * (kBlk * wave + kStep * o) + lane / LPR;
         off[o] = (n - RPB * kStep * o) * ld + mn0 + 16 * ((lane % LPR) ^ swz_cols<kMN>(n));
       }
     }
   }
-  // Block u of the stage [k0, k0 + 128); what lies at or past kend reads as zero.
+  // Block u of the stage; what lies past the end of the contraction reads as zero.
   template <int u>
-  __device__ __forceinline__ void load(uint8_t* dst, int k0, int kend) const {
+  __device__ __forceinline__ void load(uint8_t* dst) const {
     if constexpr (kKMajor) {
-      const Rsrc r = make_rsrc(base + k0, bytes - k0);
-      dma<16>(r, (lds_void*)(dst + lds + 1024 * u), k0 + kcol[u & 1] >= kend ? kOOB : off[u & 1], 8 * u * ld);
+      const Rsrc r = window(base, bytes);
+      dma<16>(r, (lds_void*)(dst + lds + 1024 * u), (kcol ^ (64 * (u & 1))) >= left ? kOOB : off[u & 1], 8 * u * ld);
     } else {
-      const Rsrc r = make_rsrc(base + (int64_t)k0 * ld, (int64_t)(kend - k0) * ld);
+      const Rsrc r = window(base, (left < kRun ? left : kRun) * ld);
       dma<16>(r, (lds_void*)(dst + lds + 1024 * u), off[u / kStep & 1], (1024 / kMN) * u * ld);
     }
+  }
+  // On by n stages.
+  __device__ __forceinline__ void advance(int n) {
+    left -= n * kRun;
+    base += kKMajor ? (uint32_t)(n * kRun) : (uint32_t)(n * kRun * ld);
+    bytes -= n * kRun;
   }
 };
 
@@ -158,18 +183,136 @@ struct B128Frag {
   }
 };
 
+// Tiles of a grouped forward or grad_X.  Row tiles of 256 rows or less never
+// straddle a group; the workgroups deal the tiles that exist (their number is
+// known on the device only) to the eight XCDs in contiguous ranges, in each
+// group's blocked order (grouped_order).  Dealing the host's upper bound
+// instead leaves the last XCD idle: 16384 rows in 8 equal groups, 512 tiles
+// bounded by 576, took 163 us for 124.
+//
+// Every wave scans 64 groups at a time: the clamped ends are a running
+// maximum, the row tiles before each group a running sum.
+struct GroupScan {
+  int start, end, seen;      // of this lane's group: first row, end row, row tiles before it
+  int last_end, last_seen;   // after the 64 groups
+};
+template <int BP>
+__device__ __forceinline__ GroupScan scan_groups(const int32_t* ends, int groups, int M, int base, int end0, int seen0) {
+  const int lane = threadIdx.x & 63;
+  int e = base + lane < groups ? ends[base + lane] : 0;
+  e = e > M ? M : e;
+  e = e < end0 ? end0 : e;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(e, d);
+    e = lane >= d && o > e ? o : e;
+  }
+  int s = __shfl_up(e, 1);
+  s = lane == 0 ? end0 : s;
+  const int n = (e - s + BP - 1) / BP;
+  int sum = n;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(sum, d);
+    sum += lane >= d ? o : 0;
+  }
+  return GroupScan{s, e, seen0 + sum - n, __builtin_amdgcn_readlane(e, 63), seen0 + __builtin_amdgcn_readlane(sum, 63)};
+}
+
+// Params::tail: 0, every tile; 1, the whole rounds of kCUs tiles when the
+// last, partial one has at most kCUs / 2 (every tile otherwise); 2 (256 x 128
+// tiles), what 1 leaves, each 256 x 256 tile as its two halves.
+template <class C>
+__device__ __forceinline__ Tile grouped_tile(const Params& p, int32_t* ends) {
+  for (int i = threadIdx.x; i < p.groups; i += blockDim.x) ends[i] = p.offsets[i];
+  __syncthreads();
+  Tile t{0, 0, 0, 0, 0, p.Ktot, 0, 0, false};
+  GroupScan sc{};
+  int end0 = 0, rows = 0;
+  for (int base = 0; base < p.groups; base += 64) {
+    sc = scan_groups<C::BP>(ends, p.groups, p.Ptot, base, end0, rows);
+    end0 = sc.last_end;
+    rows = sc.last_seen;
+  }
+  const bool halves = p.tail == 2;
+  const int nq = halves ? (p.Qtot + 255) / 256 : p.nq;
+  const int all = rows * nq, full = all / kCUs * kCUs, rest = all - full;
+  const bool split = p.tail != 0 && full > 0 && rest > 0 && 2 * rest <= kCUs;
+  const int nt = !halves ? (split ? full : all) : split ? 2 * rest : 0;
+  const int hw = blockIdx.x;
+  if (hw >= nt) return t;
+  int tile = xcd_remap(hw, nt);
+  const int half = tile & 1;
+  if (halves) tile = full + tile / 2;
+  const int pidx = tile / nq;
+  if (p.groups > 64) {
+    end0 = rows = 0;
+    for (int base = 0; base < p.groups; base += 64) {
+      sc = scan_groups<C::BP>(ends, p.groups, p.Ptot, base, end0, rows);
+      if (pidx < sc.last_seen) {
+        t.g = base;
+        break;
+      }
+      end0 = sc.last_end;
+      rows = sc.last_seen;
+    }
+  }
+  // The last group with at most pidx row tiles before it: the later ones of
+  // those are never empty.
+  const int l = 63 - __builtin_clzll(__builtin_amdgcn_ballot_w64(sc.seen <= pidx && sc.end > sc.start));
+  t.g += l;
+  const int start = __builtin_amdgcn_readlane(sc.start, l), seen = __builtin_amdgcn_readlane(sc.seen, l);
+  t.pend = __builtin_amdgcn_readlane(sc.end, l);
+  int2 pq = make_int2(pidx - seen, tile - pidx * nq);
+  if (p.gm > 1) pq = grouped_order(tile - seen * nq, (t.pend - start + C::BP - 1) / C::BP, nq, p.gm);
+  t.p0 = start + pq.x * C::BP;
+  t.q0 = halves ? pq.y * 256 + half * C::BQ : pq.y * C::BQ;
+  t.valid = t.q0 < p.Qtot;
+  return t;
+}
+
+// Tiles of a grouped grad_W over at most 64 groups, every group having the
+// same number: longest contraction first (ties by group index), which keeps
+// the last round short.  Inside a group each XCD takes one contiguous range of
+// the tiles, row tiles fastest, so that it reads few of the group's gradient
+// and input columns more than once.
+template <class C>
+__device__ __forceinline__ Tile grouped_dw_tile(const Params& p, int32_t* ends) {
+  for (int i = threadIdx.x; i < p.groups; i += blockDim.x) ends[i] = p.offsets[i];
+  __syncthreads();
+  const int lane = threadIdx.x & 63;
+  const GroupScan sc = scan_groups<C::BP>(ends, p.groups, p.Ktot, 0, 0, 0);
+  const int size = sc.end - sc.start;
+  const int per = p.ntiles / p.groups, hw = blockIdx.x, want = hw / per;
+  int rank = 0;
+  for (int j = 0; j < p.groups; ++j) {
+    const int sj = __builtin_amdgcn_readlane(size, j);
+    rank += sj > size || (sj == size && j < lane) ? 1 : 0;
+  }
+  const int g = __builtin_ctzll(__builtin_amdgcn_ballot_w64(rank == want && lane < p.groups));
+  const int tile = xcd_remap(hw - want * per, per), np = per / p.nq;
+  return Tile{g, (tile % np) * C::BP, p.Ptot, (tile / np) * C::BQ, __builtin_amdgcn_readlane(sc.start, g),
+              __builtin_amdgcn_readlane(sc.end, g), 0, 0, true};
+}
+
 template <class C, int kOp>
-__global__ __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void b128_kernel(Params p) {
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void b128_kernel(Params p) {
   constexpr bool kDW = kOp == kB128Dw;
   constexpr bool kPK = !kDW, kQK = kOp == kB128Fwd;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * C::STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t all_smem[C::KW * C::NS * C::STAGE];
   static_assert(kMaxGroups * 4 <= C::STAGE, "group ends alias stage 0");
-  static_assert(C::BP * C::BQ * 2 <= 2 * C::STAGE, "the epilogue staging fits the stages");
+  static_assert(C::BP * C::BQ * (C::KW > 1 ? 4 : 2) <= C::NS * C::STAGE, "the epilogue staging fits the stages");
 
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int gwave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kw = gwave / C::NW, wave = gwave % C::NW;            // group, and wave in the group
   const int wp = wave / C::NWQ, wq = wave % C::NWQ;
-  Tile t = select_tile<C, kDW>(p, reinterpret_cast<int32_t*>(smem));
+  uint8_t* const smem = all_smem + kw * (C::NS * C::STAGE);      // the group's stages
+  int32_t* const ends = reinterpret_cast<int32_t*>(all_smem);
+  Tile t;
+  if (!kDW && p.offsets != nullptr) t = grouped_tile<C>(p, ends);
+  else if (kDW && p.offsets != nullptr && p.groups <= 64) t = grouped_dw_tile<C>(p, ends);
+  else t = select_tile<C, kDW>(p, ends);
   if (!t.valid) return;
   // The same in every lane, which the compiler cannot see through the LDS
   // reads behind it: in scalar registers from here on.
@@ -177,45 +320,63 @@ __global__ __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2
   __syncthreads();                                               // group ends read; stage 0 reusable
 
   const int kbeg = t.kbeg, kend = t.kend;
-  B128Loader<kPK, C::BP> lp;
-  B128Loader<kQK, C::BQ> lq;
-  lp.init(p.P, 0, t.p0, t.pend, wave, lane);
-  lq.init(p.Q, kDW ? 0 : t.g, t.q0, p.Qtot, wave, lane);
+  B128Loader<kPK, C::BP, C::PB> lp;
+  B128Loader<kQK, C::BQ, C::QB> lq;
+  lp.init(p.P, 0, t.p0, t.pend, kbeg, kend, wave, lane);
+  lq.init(p.Q, kDW ? 0 : t.g, t.q0, p.Qtot, kbeg, kend, wave, lane);
+  lp.advance(kw);
+  lq.advance(kw);
 
   // Scales of the stage, one fp32 per row of the P tile then one per column
   // of the Q tile, 64 a wave.
   const bool sp_wave = wave < C::BP / 64;
   const int64_t run0 = kDW ? (kbeg / kRun + t.g) : 0;            // first scale row of the contraction
-  const int sv = sp_wave ? wave : wave - C::BP / 64;
-  const uint8_t* sbase;
-  int64_t sstep;                                                 // bytes per stage
-  int32_t soff;
-  int64_t slen;
+  const int sv = sp_wave ? wave : (wave - C::BP / 64) % (C::BQ / 64);   // (spare waves load a Q part once more)
+  const uint8_t* sbase;                                          // of the stage
+  uint32_t sstep;                                                // bytes per stage
+  int32_t soff, slen;                                            // lane offset, bytes that exist
   if (sp_wave || kDW) {
-    const Op& o = sp_wave ? p.P : p.Q;
-    const int first = (sp_wave ? t.p0 : t.q0) + 64 * sv;
-    sbase = o.scales + run0 * o.scale_ld;
-    sstep = o.scale_ld;
-    soff = (first + lane) * 4;
-    slen = o.scale_ld;
+    const int first = (sp_wave ? t.p0 : t.q0) + 64 * sv, cols = (sp_wave ? p.Ptot : p.Qtot) - first;
+    sstep = sp_wave ? p.P.scale_ld : p.Q.scale_ld;
+    sbase = (sp_wave ? p.P.scales : p.Q.scales) + run0 * sstep + (int64_t)first * 4;
+    soff = lane * 4;
+    slen = (cols < 0 ? 0 : cols < 64 ? cols : 64) * 4;
   } else {
     const int qb = (t.q0 + 64 * sv) / kRun;                      // the 128-column block of these 64 columns
-    sbase = p.Q.scales + (int64_t)t.g * p.Q.scale_batch + (kQK ? (int64_t)qb * p.Q.scale_ld : 0);
+    sbase = p.Q.scales + (int64_t)t.g * p.Q.scale_batch + (kQK ? (int64_t)qb * p.Q.scale_ld : qb * 4);
     sstep = kQK ? 4 : p.Q.scale_ld;
-    soff = kQK ? 0 : qb * 4;
-    slen = kQK ? (qb * kRun < p.Qtot ? 4 : 0) : p.Q.scale_ld;
+    soff = 0;
+    slen = qb * kRun < p.Qtot ? 4 : 0;
+  }
+  sbase += (uint64_t)kw * sstep;
+  {
+    // Through readfirstlane once, here, far from the loads that use them.
+    const uint64_t a = reinterpret_cast<uint64_t>(sbase);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)a), hi = __builtin_amdgcn_readfirstlane((int)(a >> 32));
+    sbase = reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
+    sstep = __builtin_amdgcn_readfirstlane((int)sstep) * C::KW;
+    slen = __builtin_amdgcn_readfirstlane(slen);
+    __builtin_amdgcn_sched_barrier(0);
   }
 
-  const int nk = (kend - kbeg + kRun - 1) / kRun;
-  // Load u of stage kb: blocks of P, blocks of Q, scales.  Stages at or past
-  // the end of the contraction read nothing (zeros).
+  const int nk = (kend - kbeg + C::KW * kRun - 1) / (C::KW * kRun);   // stages of a group
+  // Load u of the next stage to be loaded: blocks of P, blocks of Q, scales
+  // (the last one moves on to the stage after).  Stages past the end of the
+  // contraction read nothing (zeros).
   constexpr int kLoads = C::PB + C::QB + 1;
-  auto issue = [&](auto ui, uint8_t* sb, int kb) {
+  auto issue = [&](auto ui, uint8_t* sb) {
     constexpr int u = decltype(ui)::value;
-    const int k0 = kbeg + kb * kRun;
-    if constexpr (u < C::PB) lp.template load<u>(sb + C::kP, k0, kend);
-    else if constexpr (u < C::PB + C::QB) lq.template load<u - C::PB>(sb + C::kQ, k0, kend);
-    else dma<4>(make_rsrc(sbase + kb * sstep, kb < nk ? slen : 0), (lds_void*)(sb + C::kPS + 256 * wave), soff, 0);
+    if constexpr (u < C::PB) {
+      lp.template load<u>(sb + C::kP);
+    } else if constexpr (u < C::PB + C::QB) {
+      lq.template load<u - C::PB>(sb + C::kQ);
+    } else {
+      const Rsrc r = window(sbase, lp.left > 0 ? slen : 0);
+      dma<4>(r, (lds_void*)(sb + (sp_wave ? C::kPS : C::kQS) + 256 * sv), soff, 0);
+      sbase += sstep;
+      lp.advance(C::KW);
+      lq.advance(C::KW);
+    }
   };
 
   B128Frag<kPK, C::BP> fp;
@@ -237,8 +398,8 @@ __global__ __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2
   // barrier says both that every wave is done with this buffer and that the
   // next stage has landed.  The rows that remain cover the next stage's first
   // reads: P's first fragments and each Q fragment after its last MFMA.  The
-  // loads of the stage after that go into this buffer, one per MFMA from the
-  // barrier on: a wave that issues them in one go waits for the memory
+  // loads of stage kb + NS go into this buffer, one per MFMA from the barrier
+  // on: a wave that issues them in one go waits for the memory
   // pipeline to take them, with its MFMAs behind them.
   constexpr int kLag = 2, kRing = kLag + 1, NM = C::FP * C::FQ;
   constexpr int kAhead = 1, kSlots = 2 * kAhead, kSync = C::FP - kAhead;
@@ -246,16 +407,21 @@ __global__ __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2
   static_assert(C::FP % kSlots == 0, "a row's slot is the same in every stage");
   i32x8b q[C::FQ], pf[kSlots];
   if (nk > 0) {
-    static_for<kLoads>([&](auto u) { issue(u, smem, 0); });
-    static_for<kEarly>([&](auto u) { issue(u, smem + C::STAGE, 1); });
-    barrier_vm<kEarly>();
+    static_for<C::NS - 1>([&](auto si) {
+      constexpr int st = decltype(si)::value;
+      static_for<kLoads>([&](auto u) { issue(u, smem + st * C::STAGE); });
+    });
+    static_for<kEarly>([&](auto u) { issue(u, smem + (C::NS - 1) * C::STAGE); });
+    barrier_vm<(C::NS - 2) * kLoads + kEarly>();
     static_for<kAhead>([&](auto i) { pf[decltype(i)::value] = fp.template read<decltype(i)::value>(smem + C::kP); });
     static_for<C::FQ>([&](auto j) { q[decltype(j)::value] = fq.template read<decltype(j)::value>(smem + C::kQ); });
   }
   int cur = 0;
   for (int kb = 0; kb < nk; ++kb) {
     uint8_t* const sb = smem + cur;
-    uint8_t* const nx = smem + (C::STAGE - cur);
+    const int next = cur + C::STAGE < C::NS * C::STAGE ? cur + C::STAGE : 0;
+    uint8_t* const nx = smem + next;
+    uint8_t* const pv = smem + (cur > 0 ? cur - C::STAGE : (C::NS - 1) * C::STAGE);   // the stage before
     float sp[C::FP], w;
     f32x4 sq[kDW ? C::FQ : 1];
 #pragma unroll
@@ -270,7 +436,7 @@ __global__ __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2
     static_for<NM + kLag>([&](auto mi) {
       constexpr int m = decltype(mi)::value;
       constexpr int i = m / C::FQ, j = m % C::FQ;
-      if constexpr (m == kSync * C::FQ) barrier_vm<0>();
+      if constexpr (m == kSync * C::FQ) barrier_vm<(C::NS - 2) * kLoads>();
       if constexpr (m < NM) {
         if constexpr (j == 0) {
           constexpr int n = i + kAhead;
@@ -280,10 +446,15 @@ __global__ __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2
         part[m % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q[j], pf[i % kSlots], f32x4{}, 0, 0, 0, 0, 0, 0);
         if constexpr (i == C::FP - 1) q[j] = fq.template read<j>(nx + C::kQ);
         if constexpr (m >= kSync * C::FQ && m - kSync * C::FQ < kEarly) {
-          issue(IC<m - kSync * C::FQ>{}, sb, kb + 2);
+          issue(IC<m - kSync * C::FQ>{}, sb);
         }
-        if constexpr (m < kLoads - kEarly) {
-          issue(IC<m + kEarly>{}, nx, kb + 1);
+        // The rest of the stage begun in the row before, all ahead of the barrier,
+        // which counts whole stages.
+        if constexpr (m < kSync * C::FQ) {
+          static_for<kLoads - kEarly>([&](auto li) {
+            constexpr int l = decltype(li)::value;
+            if constexpr ((l < kSync * C::FQ ? l : kSync * C::FQ - 1) == m) issue(IC<l + kEarly>{}, pv);
+          });
         }
       }
       if constexpr (m >= kLag) {
@@ -297,9 +468,43 @@ __global__ __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2
       }
       __builtin_amdgcn_sched_barrier(0);
     });
-    cur = C::STAGE - cur;
+    cur = next;
   }
   barrier_vm<0>();                                               // the last loads (zeros) have landed
+
+  uint16_t* const out = p.C + (kDW ? (int64_t)t.g * p.c_batch : 0);
+  if constexpr (C::KW > 1) {
+    // The groups' sums through LDS, added in group order: 16-byte piece c of
+    // row r of a group's tile at c ^ (r & 15).
+    float* const mine = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FQ; ++j) {
+        const int r = wp * C::WP + 16 * i + (lane & 15), c = (wq * C::WQ) / 4 + 4 * j + (lane >> 4);
+        *reinterpret_cast<f32x4*>(mine + r * C::BQ + 4 * (c ^ (r & 15))) = acc[i][j];
+      }
+    __syncthreads();
+    for (int u = tid; u < C::BP * C::BQ / 8; u += 64 * C::NW * C::KW) {
+      const int r = u / (C::BQ / 8), c = 2 * (u % (C::BQ / 8));
+      float e[8];
+#pragma unroll
+      for (int g = 0; g < C::KW; ++g) {
+        const float* src = reinterpret_cast<const float*>(all_smem + g * (C::NS * C::STAGE)) + r * C::BQ;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(src + 4 * ((c + h) ^ (r & 15)));
+#pragma unroll
+          for (int d = 0; d < 4; ++d) e[4 * h + d] = g == 0 ? v[d] : e[4 * h + d] + v[d];
+        }
+      }
+      const int row = t.p0 + r, col = t.q0 + 4 * c;
+      if (row < t.pend && col < p.Qtot)
+        *reinterpret_cast<u32x4*>(out + (int64_t)row * p.ldc + col) =
+            u32x4{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])};
+    }
+    return;
+  }
 
   // bf16 results through LDS, so that each row of the wave tile is stored as
   // one 128-byte line: 8-byte slot s of row r at s ^ (r & 15).
@@ -317,7 +522,6 @@ __global__ __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2
     }
   }
   __builtin_amdgcn_s_waitcnt(0xC07F);                            // lgkmcnt(0): own staging writes done
-  uint16_t* const out = p.C + (kDW ? (int64_t)t.g * p.c_batch : 0);
   const int c16 = lane & 7, col = t.q0 + wq * C::WQ + 8 * c16;
 #pragma unroll 4
   for (int it = 0; it < C::WP / 8; ++it) {
@@ -333,7 +537,7 @@ __global__ __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2
 template <class C, int kOp>
 inline hipError_t run_b128(const Params& prm, hipStream_t s) {
   if (prm.ntiles <= 0) return hipSuccess;
-  b128_kernel<C, kOp><<<dim3(prm.ntiles), dim3(64 * C::NW), 0, s>>>(prm);
+  b128_kernel<C, kOp><<<dim3(prm.ntiles), dim3(64 * C::NW * C::KW), 0, s>>>(prm);
   return hipGetLastError();
 }
 

@@ -3,7 +3,7 @@
 // expert).
 //
 // The weight is read once and everything else is small, so the call is a
-// stream over W.  A wave owns 16 columns of y (16 rows of W), up to 16 kTT rows
+// stream over W.  A wave owns 16 columns of y (16 rows of W), up to 16 rows
 // of x and every kWK-th 128-deep block of the contraction, which it takes
 // straight from global memory into the operand registers of
 // v_mfma_f32_16x16x128_f8f6f4 (no LDS: nothing is shared), kDepth blocks in
@@ -25,6 +25,8 @@ namespace gk {
 namespace {
 
 constexpr int kWaves = 8;
+constexpr int kRows = 16;                       // rows of x per workgroup
+constexpr int kDepth = 4;                       // contraction blocks in flight per wave
 constexpr int kFuseLds = 64 * 1024;             // codes of a fused x
 
 struct SkinnyArgs {
@@ -33,24 +35,22 @@ struct SkinnyArgs {
   int32_t row_tiles;                            // row tiles of the grid
 };
 
-template <int kTT>
 struct Block {                                  // one contraction block's operands
-  u32x4 w[2], x[kTT][2];
-  float sw, sx[kTT];
+  u32x4 w[2], x[2];
+  float sw, sx;
 };
 
 __device__ __forceinline__ float bload_f32(Rsrc r, int32_t off) {
   return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
 }
 
-template <int kTT, int kWK, bool kFuse>
+template <int kWK, bool kFuse>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4))) void b128_skinny(SkinnyArgs a) {
   const Params& p = a.p;
-  constexpr int BP = 16 * kTT, WN = kWaves / kWK;
-  constexpr int kDepth = kTT == 1 ? 4 : kTT == 2 ? 3 : 2;        // blocks in flight: at most 128 registers a wave
+  constexpr int WN = kWaves / kWK;
   __shared__ union {
     int32_t ends[kMaxGroups];
-    f32x4 sum[kWK == 1 ? 1 : kWaves][kTT][64];
+    f32x4 sum[kWK == 1 ? 1 : kWaves][64];
   } sh;
   extern __shared__ __attribute__((aligned(16))) uint8_t xq[];   // kFuse: scales [blocks][kFuseRows], codes [rows][K]
   const int tid = threadIdx.x, lane = tid & 63;
@@ -60,14 +60,14 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4))
   // tile share an XCD, whose L2 then serves the weight's second reads.
   const int xcd = blockIdx.x % 8, j = blockIdx.x / 8;
   const int rt = j % a.row_tiles, n0 = (((j / a.row_tiles) * 8 + xcd) * WN + wn) * 16;
-  int g = 0, p0 = rt * BP, pend = p.Ptot;
+  int g = 0, p0 = rt * kRows, pend = p.Ptot;
   if (p.offsets != nullptr) {
     for (int i = tid; i < p.groups; i += 64 * kWaves) sh.ends[i] = p.offsets[i];
     __syncthreads();
-    const GroupHit hit = find_row_tile<BP>(sh.ends, p.groups, p.Ptot, rt, [](int) { return true; });
+    const GroupHit hit = find_row_tile<kRows>(sh.ends, p.groups, p.Ptot, rt, [](int) { return true; });
     if (!hit.found) return;
     g = __builtin_amdgcn_readfirstlane(hit.g);
-    p0 = __builtin_amdgcn_readfirstlane(hit.start + (rt - hit.seen) * BP);
+    p0 = __builtin_amdgcn_readfirstlane(hit.start + (rt - hit.seen) * kRows);
     pend = __builtin_amdgcn_readfirstlane(hit.end);
   }
   if (p0 >= pend) return;
@@ -82,51 +82,43 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4))
   const int nbk = (K + kRun - 1) / kRun;
 
   // Block kb of the contraction; blocks and columns past the end read as zero.
-  auto load = [&](Block<kTT>& b, int kb) {
+  auto load = [&](Block& b, int kb) {
     const int k0 = kb * kRun + 16 * h;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const bool in = kb < nb && k0 + 64 * e < K;
       b.w[e] = bload16(wr, in ? r * K + k0 + 64 * e : kOOB);
-      if constexpr (!kFuse)
-#pragma unroll
-        for (int t = 0; t < kTT; ++t) b.x[t][e] = bload16(xr, in ? (16 * t + r) * K + k0 + 64 * e : kOOB);
+      if constexpr (!kFuse) b.x[e] = bload16(xr, in ? r * K + k0 + 64 * e : kOOB);
     }
     b.sw = bload_f32(swr, kb < nb ? 4 * kb : kOOB);
     if constexpr (!kFuse) {
       const Rsrc sxr = make_rsrc(sxp + (int64_t)kb * p.P.scale_ld, kb < nb ? (int64_t)(pend - p0) * 4 : 0);
-#pragma unroll
-      for (int t = 0; t < kTT; ++t) b.sx[t] = bload_f32(sxr, (16 * t + r) * 4);
+      b.sx = bload_f32(sxr, r * 4);
     }
   };
 
-  f32x4 acc[kTT];
-#pragma unroll
-  for (int t = 0; t < kTT; ++t) acc[t] = f32x4{};
-  auto multiply = [&](Block<kTT>& b, int kb) {
+  f32x4 acc = {};
+  auto multiply = [&](Block& b, int kb) {
     if constexpr (kFuse) {
       const int row = r < pend - p0 ? r : 0;                     // rows past the end: not stored
       const uint8_t* src = xq + 4 * kFuseRows * nbk + row * nbk * kRun + kb * kRun + 16 * h;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) b.x[0][e] = *reinterpret_cast<const u32x4*>(src + 64 * e);
-      b.sx[0] = xs[kb * kFuseRows + row];
+      for (int e = 0; e < 2; ++e) b.x[e] = *reinterpret_cast<const u32x4*>(src + 64 * e);
+      b.sx = xs[kb * kFuseRows + row];
     }
-    i32x8b w;
+    i32x8b w, x;
 #pragma unroll
-    for (int d = 0; d < 8; ++d) w[d] = (int)b.w[d / 4][d % 4];
-#pragma unroll
-    for (int t = 0; t < kTT; ++t) {
-      i32x8b x;
-#pragma unroll
-      for (int d = 0; d < 8; ++d) x[d] = (int)b.x[t][d / 4][d % 4];
-      const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{}, 0, 0, 0, 0, 0, 0);
-      const float s = b.sx[t] * b.sw;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) acc[t][d] = __builtin_fmaf(part[d], s, acc[t][d]);
+    for (int d = 0; d < 8; ++d) {
+      w[d] = (int)b.w[d / 4][d % 4];
+      x[d] = (int)b.x[d / 4][d % 4];
     }
+    const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{}, 0, 0, 0, 0, 0, 0);
+    const float s = b.sx * b.sw;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) acc[d] = __builtin_fmaf(part[d], s, acc[d]);
   };
 
-  Block<kTT> ring[kDepth];
+  Block ring[kDepth];
 #pragma unroll
   for (int i = 0; i < kDepth; ++i) load(ring[i], wk + i * kWK);
   if constexpr (kFuse) {
@@ -153,45 +145,32 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4))
 
   if constexpr (kWK > 1) {
     __syncthreads();                                             // group ends read
-#pragma unroll
-    for (int t = 0; t < kTT; ++t) sh.sum[wave][t][lane] = acc[t];
+    sh.sum[wave][lane] = acc;
     __syncthreads();
     if (wk != 0) return;
 #pragma unroll
-    for (int w = 1; w < kWK; ++w)
+    for (int w = 1; w < kWK; ++w) {
+      const f32x4 o = sh.sum[wave + w][lane];
 #pragma unroll
-      for (int t = 0; t < kTT; ++t) {
-        const f32x4 o = sh.sum[wave + w][t][lane];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) acc[t][d] += o[d];
-      }
+      for (int d = 0; d < 4; ++d) acc[d] += o[d];
+    }
   }
-#pragma unroll
-  for (int t = 0; t < kTT; ++t) {
-    const int row = p0 + 16 * t + r;
-    if (row < pend && n0 < p.Qtot)
-      *reinterpret_cast<u32x2*>(p.C + (int64_t)row * p.ldc + n0 + 4 * h) =
-          u32x2{pack_bf16x2(acc[t][0], acc[t][1]), pack_bf16x2(acc[t][2], acc[t][3])};
-  }
+  if (p0 + r < pend && n0 < p.Qtot)
+    *reinterpret_cast<u32x2*>(p.C + (int64_t)(p0 + r) * p.ldc + n0 + 4 * h) =
+        u32x2{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
 }
 
-int64_t row_tiles(const Params& p, int tiles) {
-  return p.offsets ? p.Ptot / (16 * tiles) + p.groups : (p.Ptot + 16 * tiles - 1) / (16 * tiles);
+int64_t row_tiles(const Params& p) {
+  return p.offsets ? p.Ptot / kRows + p.groups : (p.Ptot + kRows - 1) / kRows;
 }
 
-template <int kTT, int kWK, bool kFuse>
+template <int kWK, bool kFuse>
 hipError_t launch(SkinnyArgs a, size_t lds, hipStream_t s) {
-  const int64_t rt = row_tiles(a.p, kTT), cols = 16 * kWaves / kWK;
+  const int64_t rt = row_tiles(a.p), cols = 16 * kWaves / kWK;
   a.row_tiles = (int32_t)rt;
   const int64_t nt = ((a.p.Qtot + cols - 1) / cols + 7) / 8 * 8;
-  b128_skinny<kTT, kWK, kFuse><<<dim3((uint32_t)(rt * nt)), dim3(64 * kWaves), lds, s>>>(a);
+  b128_skinny<kWK, kFuse><<<dim3((uint32_t)(rt * nt)), dim3(64 * kWaves), lds, s>>>(a);
   return hipGetLastError();
-}
-
-template <int kTT>
-hipError_t run(const SkinnyArgs& a, hipStream_t s) {
-  const int64_t waves = row_tiles(a.p, kTT) * (a.p.Qtot / 16);
-  return waves >= 4096 ? launch<kTT, 1, false>(a, 0, s) : waves >= 1024 ? launch<kTT, 4, false>(a, 0, s) : launch<kTT, 8, false>(a, 0, s);
 }
 
 }  // namespace
@@ -203,12 +182,13 @@ bool b128_can_fuse(const Params& prm) {
 
 hipError_t b128_fwd_fused(const Params& prm, const void* x, hipStream_t s) {
   const size_t nb = ((size_t)prm.Ktot + kRun - 1) / kRun;
-  return launch<1, 8, true>(SkinnyArgs{prm, static_cast<const uint16_t*>(x), 0}, nb * (4 * kFuseRows + (size_t)prm.Ptot * kRun), s);
+  return launch<8, true>(SkinnyArgs{prm, static_cast<const uint16_t*>(x), 0}, nb * (4 * kFuseRows + (size_t)prm.Ptot * kRun), s);
 }
 
-hipError_t b128_fwd_skinny(const Params& prm, int tiles, hipStream_t s) {
+hipError_t b128_fwd_skinny(const Params& prm, hipStream_t s) {
   const SkinnyArgs a{prm, nullptr, 0};
-  return tiles == 1 ? run<1>(a, s) : tiles == 2 ? run<2>(a, s) : run<4>(a, s);
+  const int64_t waves = row_tiles(prm) * (prm.Qtot / 16);
+  return waves >= 4096 ? launch<1, false>(a, 0, s) : waves >= 1024 ? launch<4, false>(a, 0, s) : launch<8, false>(a, 0, s);
 }
 
 }  // namespace gk

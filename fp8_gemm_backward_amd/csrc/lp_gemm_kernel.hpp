@@ -1004,18 +1004,20 @@ hipError_t pt_pair(const Params& dx, const Params& dw, int fmt_p, int fmt_q, hip
 // in one launch, grad_X's tiles first; W and X both LP_MXFP4 or both
 // LP_NVFP4 (fmt_q), scaled along their last axis.
 hipError_t dec_pair(const Params& dx, const Params& dw, int fmt_q, hipStream_t s);
-// Products of E4M3 operands with fp32 scales per 128, on 256 x 256 (big) or
-// 128 x 128 tiles.
-hipError_t b128_fwd(const Params& prm, bool big, hipStream_t s);
-// The forward of few rows: row tiles of 16 `tiles` (1, 2 or 4) rows; and from
-// a bf16 x of at most kFuseRows rows that the kernel quantizes itself, when
-// b128_can_fuse says so.
+// Products of E4M3 operands with fp32 scales per 128, on tile x tile output
+// tiles (256, 128 or 64).
+hipError_t b128_fwd(const Params& prm, int tile, hipStream_t s);
+// The forward of few rows; and from a bf16 x of at most kFuseRows rows that
+// the kernel quantizes itself, when b128_can_fuse says so.
 constexpr int kFuseRows = 4;
-hipError_t b128_fwd_skinny(const Params& prm, int tiles, hipStream_t s);
+hipError_t b128_fwd_skinny(const Params& prm, hipStream_t s);
 bool b128_can_fuse(const Params& prm);
 hipError_t b128_fwd_fused(const Params& prm, const void* x, hipStream_t s);
-hipError_t b128_dx(const Params& prm, bool big, hipStream_t s);
-hipError_t b128_dw(const Params& prm, bool big, hipStream_t s);
+hipError_t b128_dx(const Params& prm, int tile, hipStream_t s);
+hipError_t b128_dw(const Params& prm, int tile, hipStream_t s);
+// The last dispatch round of a grouped call on 256 x 128 tiles (Params::tail).
+hipError_t b128_fwd_tail(const Params& prm, hipStream_t s);
+hipError_t b128_dx_tail(const Params& prm, hipStream_t s);
 
 }  // namespace gk
 }  // namespace lp

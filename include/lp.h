@@ -77,6 +77,7 @@
  *                -1 -> scales[batch][ceil(cols/128)][rows],
  *                -2 -> scales[batch][ceil(rows/128)][cols]
  *                (the product reads one run's scales of many rows at a time).
+ *                rows < 2^29.
  *                The activations and gradients that go with an LP_FP8_B128
  *                weight in FP8 products (lp_train.h has the quantizers).
  *
