@@ -1,7 +1,6 @@
 // Host side of the fused backward GEMMs: operand descriptors, tile-size
 // choice and dispatch to the per-format kernel instantiations.
 #include "lp_gemm_kernel.hpp"
-#include <cstdlib>
 
 namespace lp {
 namespace gk {
@@ -265,11 +264,15 @@ void b128_tiles(Params& prm, int b, bool dw) {
   prm.ntiles = (int32_t)(pt * prm.nq);
 }
 
-// Grouped grad_X and forward split by dispatch round, as tile_split does.
-// (Measured with the split / without: 16384 rows over 8 experts, forward 2048 x
-// 4096 TODO.)
+// Grouped grad_X and forward split by dispatch round, as tile_split does: the
+// whole rounds of 256 x 256 tiles, then a short last round as 256 x 128 tiles in
+// a second launch (grouped_tile has the rule).  For contractions of at least
+// 16 stages over at most five rounds: 16384 rows over 8 uneven experts, forward
+// 2048 x 4096 159 -> 149 us, grad_X of 4096 x 2048 161 -> 150; shorter ones and
+// more rounds only pay for the second launch (grad_X of 1536 x 6144, 10000 rows:
+// 103 -> 110; forward of 64 experts, six rounds: 568 -> 573).
 bool b128_split(Params& prm) {
-  if (prm.offsets == nullptr || prm.ntiles < kCUs || getenv("NOTAIL")) return false;
+  if (prm.offsets == nullptr || prm.ntiles < kCUs || prm.ntiles > 5 * kCUs || prm.Ktot < 16 * 128) return false;
   prm.tail = 1;
   return true;
 }
@@ -284,7 +287,6 @@ bool b128_split(Params& prm) {
 // tokens: grad_X 293 us on 256 x 256 tiles, 377 us on 128 x 128).
 enum class B128Op { kFwd, kDx, kDw };
 int b128_tile(const Params& prm, B128Op op) {
-  if (const char* e = getenv("LPT")) return atoi(e);
   auto count = [&](int b) {
     Params t = prm;
     b128_tiles(t, b, op == B128Op::kDw);

@@ -78,11 +78,24 @@ __device__ __forceinline__ int swz_cols(int n) {
   return kCols == 256 ? 2 * (n & 7) ^ g : kCols == 128 ? 2 * ((n >> 1) & 3) ^ g : ((n >> 2) & 1) ^ (2 * g);
 }
 
+// A value that is the same in every lane, in scalar registers.
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<const uint8_t*>(((uint64_t)(uint32_t)scalar((int)(v >> 32)) << 32) | (uint32_t)scalar((int)v));
+}
+
 // The buffer resource of a window.  Its words must reach the loads' inline
-// assembly from scalar arithmetic (a scalar register written by a vector
+// assembly from scalar arithmetic: a scalar register written by a vector
 // instruction may be read by a memory instruction only five instructions
-// later, which nothing checks inside inline assembly), so the running
-// addresses below take 32-bit steps and no 64-bit products.
+// later, which nothing checks inside inline assembly.  So a tile's addresses
+// go through scalar() once, five instructions ahead of every load
+// (scalars_settle), and move on by 32-bit steps.
+__device__ __forceinline__ void scalars_settle() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 4");
+  __builtin_amdgcn_sched_barrier(0);
+}
 __device__ __forceinline__ Rsrc window(const uint8_t* base, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0, bytes > 0 ? bytes : 0, 0x00020000);
 }
@@ -100,34 +113,37 @@ struct B128Loader {
   int32_t bytes;            // k-major: bytes from base to the end of the tile's rows
   int32_t left;             // contraction elements from the stage's start to the end
   int32_t ld;
+  int32_t mn;               // otherwise: the tile's first column
   int32_t off[2];           // lane offset of blocks of either parity (128 columns: of blocks 0, 1 and 2, 3)
   int32_t kcol;             // k-major: the lane's first column in the stage, even blocks (odd ones: ^ 64)
   int32_t lds;
   static constexpr int kStep = !kKMajor && kMN == 128 ? 2 : 1;   // blocks between the two offsets
 
-  __device__ __forceinline__ void init(const Op& op, int g, int mn0, int mnend, int kbeg, int kend, int wave, int lane) {
+  __device__ __forceinline__ void init(const Op& op, int wave, int lane) {
     ld = op.code_ld;
     lds = 1024 * kBlk * wave;
-    left = kend - kbeg;
     kcol = 0;
-    base = op.codes + (int64_t)g * op.code_batch;
     if constexpr (kKMajor) {
-      base += (int64_t)mn0 * ld + kbeg;
-      bytes = (mnend - mn0 < kMN ? mnend - mn0 : kMN) * ld - kbeg;
       const int row = 8 * kBlk * wave + lane / 8;
       kcol = 16 * ((lane & 7) ^ ((row >> 1) & 7));
       off[0] = row * ld + kcol;                                  // + 8 u ld
       off[1] = row * ld + (kcol ^ 64);
     } else {
-      base += (int64_t)kbeg * ld;
-      bytes = 0;
       constexpr int LPR = kMN / 16, RPB = 64 / LPR;               // lanes per row, rows per block
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
         const int n = RPB * (kBlk * wave + kStep * o) + lane / LPR;
-        off[o] = (n - RPB * kStep * o) * ld + mn0 + 16 * ((lane % LPR) ^ swz_cols<kMN>(n));
+        off[o] = (n - RPB * kStep * o) * ld + 16 * ((lane % LPR) ^ swz_cols<kMN>(n));
       }
     }
+  }
+  // To the first stage of a tile: rows (columns) mn0 .. of group g, contraction [kbeg, kend).
+  __device__ __forceinline__ void start(const Op& op, int g, int mn0, int mnend, int kbeg, int kend) {
+    asm volatile("" : "+s"(ld), "+s"(lds));                      // (keeps what follows from them out of the tile loop's registers)
+    left = kend - kbeg;
+    mn = mn0;
+    base = scalar(op.codes + (int64_t)g * op.code_batch + (kKMajor ? (int64_t)mn0 * ld + kbeg : (int64_t)kbeg * ld + mn0));
+    bytes = kKMajor ? scalar((mnend - mn0 < kMN ? mnend - mn0 : kMN) * ld - kbeg) : 0;
   }
   // Block u of the stage; what lies past the end of the contraction reads as zero.
   template <int u>
@@ -136,7 +152,11 @@ struct B128Loader {
       const Rsrc r = window(base, bytes);
       dma<16>(r, (lds_void*)(dst + lds + 1024 * u), (kcol ^ (64 * (u & 1))) >= left ? kOOB : off[u & 1], 8 * u * ld);
     } else {
-      const Rsrc r = window(base, (left < kRun ? left : kRun) * ld);
+      // The rows that exist, 0 .. 128.  (Written as one expression, the clamp
+      // to both ends becomes a vector instruction.)
+      int rows;
+      asm("s_min_i32 %0, %1, %2" : "=s"(rows) : "s"(left), "s"(kRun) : "scc");
+      const Rsrc r = window(base, (rows > 0 ? rows : 0) * ld - mn);
       dma<16>(r, (lds_void*)(dst + lds + 1024 * u), off[u / kStep & 1], (1024 / kMN) * u * ld);
     }
   }
@@ -190,32 +210,34 @@ struct B128Frag {
 // instead leaves the last XCD idle: 16384 rows in 8 equal groups, 512 tiles
 // bounded by 576, took 163 us for 124.
 //
-// Every wave scans 64 groups at a time: the clamped ends are a running
-// maximum, the row tiles before each group a running sum.
+// Every wave scans 64 groups at a time, one a lane: the clamped ends are a
+// running maximum, the row tiles before each group a running sum, both by DPP
+// shifts inside the lane rows and broadcasts across them.
+template <class F>
+__device__ __forceinline__ int wave_scan(int v, F op) {          // inclusive; 0 is neutral
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false));   // row_shr:1
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false));   // row_shr:2
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false));   // row_shr:4
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false));   // row_shr:8
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));   // row_bcast:15 into rows 1 and 3
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));   // row_bcast:31 into rows 2 and 3
+  return v;
+}
 struct GroupScan {
   int start, end, seen;      // of this lane's group: first row, end row, row tiles before it
   int last_end, last_seen;   // after the 64 groups
 };
 template <int BP>
-__device__ __forceinline__ GroupScan scan_groups(const int32_t* ends, int groups, int M, int base, int end0, int seen0) {
+__device__ __forceinline__ GroupScan scan_groups(const Params& p, int M, int base, int end0, int seen0) {
   const int lane = threadIdx.x & 63;
-  int e = base + lane < groups ? ends[base + lane] : 0;
+  int e = base + lane < p.groups ? p.offsets[base + lane] : 0;
   e = e > M ? M : e;
   e = e < end0 ? end0 : e;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(e, d);
-    e = lane >= d && o > e ? o : e;
-  }
+  e = wave_scan(e, [](int a, int b) { return a > b ? a : b; });
   int s = __shfl_up(e, 1);
   s = lane == 0 ? end0 : s;
   const int n = (e - s + BP - 1) / BP;
-  int sum = n;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(sum, d);
-    sum += lane >= d ? o : 0;
-  }
+  const int sum = wave_scan(n, [](int a, int b) { return a + b; });
   return GroupScan{s, e, seen0 + sum - n, __builtin_amdgcn_readlane(e, 63), seen0 + __builtin_amdgcn_readlane(sum, 63)};
 }
 
@@ -223,14 +245,12 @@ __device__ __forceinline__ GroupScan scan_groups(const int32_t* ends, int groups
 // last, partial one has at most kCUs / 2 (every tile otherwise); 2 (256 x 128
 // tiles), what 1 leaves, each 256 x 256 tile as its two halves.
 template <class C>
-__device__ __forceinline__ Tile grouped_tile(const Params& p, int32_t* ends) {
-  for (int i = threadIdx.x; i < p.groups; i += blockDim.x) ends[i] = p.offsets[i];
-  __syncthreads();
+__device__ __forceinline__ Tile grouped_tile(const Params& p) {
   Tile t{0, 0, 0, 0, 0, p.Ktot, 0, 0, false};
   GroupScan sc{};
   int end0 = 0, rows = 0;
   for (int base = 0; base < p.groups; base += 64) {
-    sc = scan_groups<C::BP>(ends, p.groups, p.Ptot, base, end0, rows);
+    sc = scan_groups<C::BP>(p, p.Ptot, base, end0, rows);
     end0 = sc.last_end;
     rows = sc.last_seen;
   }
@@ -248,7 +268,7 @@ __device__ __forceinline__ Tile grouped_tile(const Params& p, int32_t* ends) {
   if (p.groups > 64) {
     end0 = rows = 0;
     for (int base = 0; base < p.groups; base += 64) {
-      sc = scan_groups<C::BP>(ends, p.groups, p.Ptot, base, end0, rows);
+      sc = scan_groups<C::BP>(p, p.Ptot, base, end0, rows);
       if (pidx < sc.last_seen) {
         t.g = base;
         break;
@@ -277,19 +297,22 @@ __device__ __forceinline__ Tile grouped_tile(const Params& p, int32_t* ends) {
 // the tiles, row tiles fastest, so that it reads few of the group's gradient
 // and input columns more than once.
 template <class C>
-__device__ __forceinline__ Tile grouped_dw_tile(const Params& p, int32_t* ends) {
-  for (int i = threadIdx.x; i < p.groups; i += blockDim.x) ends[i] = p.offsets[i];
-  __syncthreads();
+__device__ __forceinline__ Tile grouped_dw_tile(const Params& p) {
   const int lane = threadIdx.x & 63;
-  const GroupScan sc = scan_groups<C::BP>(ends, p.groups, p.Ktot, 0, 0, 0);
-  const int size = sc.end - sc.start;
+  const GroupScan sc = scan_groups<C::BP>(p, p.Ktot, 0, 0, 0);
+  const int size = lane < p.groups ? sc.end - sc.start : -1;
   const int per = p.ntiles / p.groups, hw = blockIdx.x, want = hw / per;
-  int rank = 0;
-  for (int j = 0; j < p.groups; ++j) {
-    const int sj = __builtin_amdgcn_readlane(size, j);
-    rank += sj > size || (sj == size && j < lane) ? 1 : 0;
+  // The size with `want` larger ones before it, bit by bit, then which of the
+  // groups of that size.
+  int v = 0;
+  for (int bit = p.Ktot > 0 ? 31 - __builtin_clz(p.Ktot) : -1; bit >= 0; --bit) {
+    const int more = v | (1 << bit);
+    if (__builtin_popcountll(__builtin_amdgcn_ballot_w64(size >= more)) > want) v = more;
   }
-  const int g = __builtin_ctzll(__builtin_amdgcn_ballot_w64(rank == want && lane < p.groups));
+  const int nth = want - __builtin_popcountll(__builtin_amdgcn_ballot_w64(size > v));
+  const uint64_t same = __builtin_amdgcn_ballot_w64(size == v);
+  const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
+  const int g = __builtin_ctzll(__builtin_amdgcn_ballot_w64(size == v && before == nth));
   const int tile = xcd_remap(hw - want * per, per), np = per / p.nq;
   return Tile{g, (tile % np) * C::BP, p.Ptot, (tile / np) * C::BQ, __builtin_amdgcn_readlane(sc.start, g),
               __builtin_amdgcn_readlane(sc.end, g), 0, 0, true};
@@ -310,56 +333,52 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   uint8_t* const smem = all_smem + kw * (C::NS * C::STAGE);      // the group's stages
   int32_t* const ends = reinterpret_cast<int32_t*>(all_smem);
   Tile t;
-  if (!kDW && p.offsets != nullptr) t = grouped_tile<C>(p, ends);
-  else if (kDW && p.offsets != nullptr && p.groups <= 64) t = grouped_dw_tile<C>(p, ends);
+  if (!kDW && p.offsets != nullptr) t = grouped_tile<C>(p);
+  else if (kDW && p.offsets != nullptr && p.groups <= 64) t = grouped_dw_tile<C>(p);
   else t = select_tile<C, kDW>(p, ends);
   if (!t.valid) return;
-  // The same in every lane, which the compiler cannot see through the LDS
-  // reads behind it: in scalar registers from here on.
-  for (int* v : {&t.g, &t.p0, &t.pend, &t.q0, &t.kbeg, &t.kend}) *v = __builtin_amdgcn_readfirstlane(*v);
+  // The same in every lane, which the compiler cannot see: in scalar registers
+  // from here on.
+  for (int* v : {&t.g, &t.p0, &t.pend, &t.q0, &t.kbeg, &t.kend}) *v = scalar(*v);
   __syncthreads();                                               // group ends read; stage 0 reusable
 
-  const int kbeg = t.kbeg, kend = t.kend;
   B128Loader<kPK, C::BP, C::PB> lp;
   B128Loader<kQK, C::BQ, C::QB> lq;
-  lp.init(p.P, 0, t.p0, t.pend, kbeg, kend, wave, lane);
-  lq.init(p.Q, kDW ? 0 : t.g, t.q0, p.Qtot, kbeg, kend, wave, lane);
-  lp.advance(kw);
-  lq.advance(kw);
+  lp.init(p.P, wave, lane);
+  lq.init(p.Q, wave, lane);
 
   // Scales of the stage, one fp32 per row of the P tile then one per column
   // of the Q tile, 64 a wave.
   const bool sp_wave = wave < C::BP / 64;
-  const int64_t run0 = kDW ? (kbeg / kRun + t.g) : 0;            // first scale row of the contraction
   const int sv = sp_wave ? wave : (wave - C::BP / 64) % (C::BQ / 64);   // (spare waves load a Q part once more)
   const uint8_t* sbase;                                          // of the stage
   uint32_t sstep;                                                // bytes per stage
-  int32_t soff, slen;                                            // lane offset, bytes that exist
-  if (sp_wave || kDW) {
-    const int first = (sp_wave ? t.p0 : t.q0) + 64 * sv, cols = (sp_wave ? p.Ptot : p.Qtot) - first;
-    sstep = sp_wave ? p.P.scale_ld : p.Q.scale_ld;
-    sbase = (sp_wave ? p.P.scales : p.Q.scales) + run0 * sstep + (int64_t)first * 4;
-    soff = lane * 4;
-    slen = (cols < 0 ? 0 : cols < 64 ? cols : 64) * 4;
-  } else {
-    const int qb = (t.q0 + 64 * sv) / kRun;                      // the 128-column block of these 64 columns
-    sbase = p.Q.scales + (int64_t)t.g * p.Q.scale_batch + (kQK ? (int64_t)qb * p.Q.scale_ld : qb * 4);
-    sstep = kQK ? 4 : p.Q.scale_ld;
-    soff = 0;
-    slen = qb * kRun < p.Qtot ? 4 : 0;
-  }
-  sbase += (uint64_t)kw * sstep;
+  const int32_t soff = sp_wave || kDW ? lane * 4 : 0;            // lane offset
+  int32_t slen;                                                  // bytes that exist
+  lp.start(p.P, 0, t.p0, t.pend, t.kbeg, t.kend);
+  lq.start(p.Q, kDW ? 0 : t.g, t.q0, p.Qtot, t.kbeg, t.kend);
+  lp.advance(kw);
+  lq.advance(kw);
   {
-    // Through readfirstlane once, here, far from the loads that use them.
-    const uint64_t a = reinterpret_cast<uint64_t>(sbase);
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)a), hi = __builtin_amdgcn_readfirstlane((int)(a >> 32));
-    sbase = reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
-    sstep = __builtin_amdgcn_readfirstlane((int)sstep) * C::KW;
-    slen = __builtin_amdgcn_readfirstlane(slen);
-    __builtin_amdgcn_sched_barrier(0);
+    const int64_t run0 = kDW ? (t.kbeg / kRun + t.g) : 0;        // first scale row of the contraction
+    if (sp_wave || kDW) {
+      const int first = (sp_wave ? t.p0 : t.q0) + 64 * sv, cols = (sp_wave ? p.Ptot : p.Qtot) - first;
+      sstep = sp_wave ? p.P.scale_ld : p.Q.scale_ld;
+      sbase = (sp_wave ? p.P.scales : p.Q.scales) + run0 * sstep + (int64_t)first * 4;
+      slen = (cols < 0 ? 0 : cols < 64 ? cols : 64) * 4;
+    } else {
+      const int qb = (t.q0 + 64 * sv) / kRun;                    // the 128-column block of these 64 columns
+      sbase = p.Q.scales + (int64_t)t.g * p.Q.scale_batch + (kQK ? (int64_t)qb * p.Q.scale_ld : qb * 4);
+      sstep = kQK ? 4 : p.Q.scale_ld;
+      slen = qb * kRun < p.Qtot ? 4 : 0;
+    }
+    sbase += (uint64_t)kw * sstep;
+    sbase = scalar(sbase);
+    sstep = scalar((int)sstep) * C::KW;
+    slen = scalar(slen);
+    scalars_settle();
   }
 
-  const int nk = (kend - kbeg + C::KW * kRun - 1) / (C::KW * kRun);   // stages of a group
   // Load u of the next stage to be loaded: blocks of P, blocks of Q, scales
   // (the last one moves on to the stage after).  Stages past the end of the
   // contraction read nothing (zeros).
@@ -386,12 +405,6 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const int psa = C::kPS + (wp * C::WP + (lane & 15)) * 4;
   const int qsa = C::kQS + (wq * C::WQ + (kDW ? 4 * (lane >> 4) : 0)) * 4;
 
-  f32x4 acc[C::FP][C::FQ];
-#pragma unroll
-  for (int i = 0; i < C::FP; ++i)
-#pragma unroll
-    for (int j = 0; j < C::FQ; ++j) acc[i][j] = f32x4{};
-
   // One stage: FP x FQ MFMAs (rows of FQ), the products of MFMA m added to
   // the sums after MFMA m + kLag has been issued.  P fragments are read kAhead
   // rows early; once the stage's last one is in registers, in row kSync, one
@@ -405,7 +418,13 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   constexpr int kAhead = 1, kSlots = 2 * kAhead, kSync = C::FP - kAhead;
   constexpr int kEarly = NM - kSync * C::FQ < kLoads ? NM - kSync * C::FQ : kLoads;   // loads before the stage's end
   static_assert(C::FP % kSlots == 0, "a row's slot is the same in every stage");
+  f32x4 acc[C::FP][C::FQ];
+#pragma unroll
+  for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FQ; ++j) acc[i][j] = f32x4{};
   i32x8b q[C::FQ], pf[kSlots];
+  const int nk = (t.kend - t.kbeg + C::KW * kRun - 1) / (C::KW * kRun);   // stages of a group
   if (nk > 0) {
     static_for<C::NS - 1>([&](auto si) {
       constexpr int st = decltype(si)::value;
@@ -506,31 +525,32 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     return;
   }
 
-  // bf16 results through LDS, so that each row of the wave tile is stored as
-  // one 128-byte line: 8-byte slot s of row r at s ^ (r & 15).
-  constexpr int ROWB = C::WQ * 2;
-  static_assert(ROWB == 128, "one line per row");
-  uint8_t* const stg = smem + wave * (C::WP * ROWB);
+  // bf16 results through LDS, so that a store writes whole rows of the tile:
+  // 8-byte slot s of row r at s ^ 2 (r & 15).
+  constexpr int ROWB = C::BQ * 2, LPR = ROWB / 16, RPI = 64 / LPR;   // lanes per row, rows per store
+  const int c16 = lane % LPR, col = t.q0 + 8 * c16;
 #pragma unroll
   for (int i = 0; i < C::FP; ++i) {
-    const int r = lane & 15;
+    const int r = wp * C::WP + 16 * i + (lane & 15);
 #pragma unroll
     for (int j = 0; j < C::FQ; ++j) {
-      const int slot = 4 * j + (lane >> 4);
-      *reinterpret_cast<u32x2*>(stg + (16 * i + r) * ROWB + 8 * (slot ^ r)) =
+      const int slot = wq * (C::WQ / 4) + 4 * j + (lane >> 4);
+      *reinterpret_cast<u32x2*>(smem + r * ROWB + 8 * (slot ^ (2 * (r & 15)))) =
           u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
     }
   }
-  __builtin_amdgcn_s_waitcnt(0xC07F);                            // lgkmcnt(0): own staging writes done
-  const int c16 = lane & 7, col = t.q0 + wq * C::WQ + 8 * c16;
+  __syncthreads();
 #pragma unroll 4
-  for (int it = 0; it < C::WP / 8; ++it) {
-    const int r = 8 * it + lane / 8;
-    const u32x2 lo = *reinterpret_cast<const u32x2*>(stg + r * ROWB + 8 * ((2 * c16) ^ (r & 15)));
-    const u32x2 hi = *reinterpret_cast<const u32x2*>(stg + r * ROWB + 8 * ((2 * c16 + 1) ^ (r & 15)));
-    const int row = t.p0 + wp * C::WP + r;
-    if (row < t.pend && col < p.Qtot)
-      *reinterpret_cast<u32x4*>(out + (int64_t)row * p.ldc + col) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+  for (int it = 0; it < C::BP / (RPI * C::NW); ++it) {
+    const int r = (it * C::NW + wave) * RPI + lane / LPR, row = t.p0 + r;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(smem + r * ROWB + 16 * (c16 ^ (r & 15)));
+    if (row < t.pend && col < p.Qtot) {
+      u32x4* const dst = reinterpret_cast<u32x4*>(out + (int64_t)row * p.ldc + col);
+      // grad_W is often larger than the caches: streamed (64 experts of 2048 x
+      // 7168, 32768 rows: 1008 us without, 911 us).
+      if constexpr (kDW) __builtin_nontemporal_store(v, dst);
+      else *dst = v;
+    }
   }
 }
 
