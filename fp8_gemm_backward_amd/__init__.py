@@ -72,14 +72,15 @@ def _load() -> ctypes.CDLL:
     lib.lp_linear_fwd_dyn.argtypes = [v, i64, P, v, v, v, v]
     lib.lp_grouped_fwd_dyn.argtypes = [v, i64, P, v, i64, v, v, v, v]
     f64 = ctypes.c_double
-    lib.lp_adamw.argtypes = [v, i64, i32, i32, i32, f64, f64, f64, f64, i64, v, v]
+    lib.lp_adamw_plan.argtypes = [v, i64, i32, i32, i32, v, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(i64)]
+    lib.lp_adamw.argtypes = [v, i64, i64, i32, i32, i32, f64, f64, f64, f64, i64, v, v]
     lib.lp_status_string.argtypes = [i32]
     lib.lp_status_string.restype = ctypes.c_char_p
     for f in ("lp_dequant", "lp_mx_quant", "lp_mx_quant_dual", "lp_linear_bwd", "lp_grouped_bwd",
               "lp_linear_bwd_workspace", "lp_linear_bwd_ws", "lp_linear_bwd_noalloc", "lp_grouped_dx_deferred", "lp_tensor_amax", "lp_tensor_quant",
               "lp_scale_from_history", "lp_linear_fwd", "lp_grouped_fwd", "lp_tensor_quant_delayed",
               "lp_r128_quant", "lp_r128_quant_dual", "lp_b128_quant", "lp_linear_fwd_dyn", "lp_grouped_fwd_dyn",
-              "lp_adamw"):
+              "lp_adamw_plan", "lp_adamw"):
         getattr(lib, f).restype = ctypes.c_int32
     return lib
 
@@ -89,6 +90,7 @@ lib = _load()
 
 _CODE_BITS = {"bf16": 16, "mxfp4": 4, "nvfp4": 4, "fp8_b128": 8, "mxfp8": 8, "fp8t_e4m3": 8, "fp8t_e5m2": 8,
               "fp8_r128": 8}
+_NAMES = {f: (f"{f} codes", f"{f} scales", f"{f} tensor scale") for f in FMT}
 
 
 def _scale_bytes(fmt: str, axis: int, b: int, r: int, c: int) -> int:
@@ -106,13 +108,18 @@ def _scale_bytes(fmt: str, axis: int, b: int, r: int, c: int) -> int:
     return 0
 
 
-def _device(t: Optional[torch.Tensor], name: str, nbytes: int, dtype=None) -> None:
+def _device(t: Optional[torch.Tensor], name, nbytes: int, dtype=None) -> None:
     """A tensor the library reads or writes `nbytes` of: on the GPU,
     contiguous, large enough (and of `dtype` where its element count is what
     the call passes).  Checked here because the C calls take bare pointers:
-    a host pointer or a short buffer would reach a kernel as it is."""
+    a host pointer or a short buffer would reach a kernel as it is.  name: a
+    string, or a list's name and an index."""
     if nbytes <= 0:
         return
+    if t is not None and t.is_cuda and (dtype is None or t.dtype == dtype) and t.is_contiguous() and t.nbytes >= nbytes:
+        return
+    if isinstance(name, tuple):
+        name = "%s[%d]" % name
     if t is None:
         raise ValueError(f"{name}: a device tensor of {nbytes} bytes is required")
     if not t.is_cuda:
@@ -121,8 +128,7 @@ def _device(t: Optional[torch.Tensor], name: str, nbytes: int, dtype=None) -> No
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.numel() * t.element_size() < nbytes:
-        raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, the call needs {nbytes}")
+    raise ValueError(f"{name} holds {t.nbytes} bytes, the call needs {nbytes}")
 
 
 def header_functions() -> list[str]:
@@ -166,20 +172,19 @@ class QTensor:
     def c(self) -> _QTensorC:
         b, r, c = self.shape
         n = b * r * c
-        _device(self.codes, f"{self.fmt} codes", n * _CODE_BITS[self.fmt] // 8)
-        _device(self.scales, f"{self.fmt} scales", _scale_bytes(self.fmt, self.axis, b, r, c))
-        if self.fmt in ("nvfp4", "fp8t_e4m3", "fp8t_e5m2"):
-            _device(self.tensor_scale, f"{self.fmt} tensor scale", 4 if n else 0, torch.float32)
-
-        def ptr(t):
-            return None if t is None else t.data_ptr()
-        return _QTensorC(FMT[self.fmt], self.axis, self.shape[0], self.shape[1], self.shape[2],
-                         ptr(self.codes), ptr(self.scales), ptr(self.tensor_scale))
+        fmt, codes, scales, ts = self.fmt, self.codes, self.scales, self.tensor_scale
+        _device(codes, _NAMES[fmt][0], n * _CODE_BITS[fmt] // 8)
+        _device(scales, _NAMES[fmt][1], _scale_bytes(fmt, self.axis, b, r, c))
+        if fmt in ("nvfp4", "fp8t_e4m3", "fp8t_e5m2"):
+            _device(ts, _NAMES[fmt][2], 4 if n else 0, torch.float32)
+        return _QTensorC(FMT[fmt], self.axis, b, r, c, None if codes is None else codes.data_ptr(),
+                         None if scales is None else scales.data_ptr(), None if ts is None else ts.data_ptr())
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without the Stream object (2.8 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -500,8 +505,7 @@ def lp_r128_quant_dual(src: torch.Tensor, offsets: Optional[torch.Tensor] = None
     the last offset are left unwritten in both."""
     b, r, c = shape = _shape3(src)
     dev = src.device
-    codes_c = torch.empty(shape, dtype=torch.uint8, device=dev)
-    codes_r = torch.empty(shape, dtype=torch.uint8, device=dev)
+    codes_c, codes_r = (torch.empty(shape, dtype=torch.uint8, device=dev) for _ in range(2))
     scales_c = torch.empty((b, -(-c // 128), r), dtype=torch.float32, device=dev)
     scales_r = torch.empty((b, _runs(r, offsets), c), dtype=torch.float32, device=dev)
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
@@ -536,10 +540,16 @@ def _fwd_dyn(x: torch.Tensor, w: QTensor, offsets: Optional[torch.Tensor], y: Op
         y = torch.empty((M, w.rows), dtype=torch.bfloat16, device=x.device)
     _device(y, "y", 2 * M * w.rows)
     nb = -(-K // 128)
-    scales = 4 * nb * M                                      # scratch: scales, then (16-byte aligned) codes
-    scratch = torch.empty(-(-scales // 16) * 16 + M * K, dtype=torch.uint8, device=x.device)
-    at = scratch.data_ptr()
-    args = (at + -(-scales // 16) * 16, at, y.data_ptr(), _stream(stream))
+    if offsets is None and M <= 4 and M * nb <= 512:         # quantized inside the product
+        codes = scales = None
+    else:
+        at = -(-4 * nb * M // 16) * 16                       # scratch: scales, then (16-byte aligned) codes
+        scratch = torch.empty(at + M * K, dtype=torch.uint8, device=x.device)
+        if stream is not None:                               # not to be reused before that stream is done with it
+            scratch.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream))
+        scales = scratch.data_ptr()
+        codes = scales + at
+    args = (codes, scales, y.data_ptr(), _stream(stream))
     wc = w.c()
     if offsets is None:
         _check(lib.lp_linear_fwd_dyn(x.data_ptr(), M, ctypes.byref(wc), *args), "lp_linear_fwd_dyn")
@@ -577,8 +587,10 @@ class AdamWPlan:
     uint8 E4M3 codes with float32 scales per 128 elements
     (exp_avg_sq_scales: of sqrt(v)).  copies: bfloat16 tensors that receive
     the new float32 parameters.  weight_decay, lr_scale: one number or one
-    per tensor.  The plan keeps the tensors alive; gradients may be replaced
-    with set_grads."""
+    per tensor.  The plan keeps the tensors alive and holds the device table
+    that the step reads; set_grads makes a new one, so gradients that stay
+    where they are from step to step are the cheaper way, and set_grads
+    cannot be captured into a graph (the step can)."""
 
     def __init__(self, params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales=None, exp_avg_sq_scales=None, copies=None,
                  weight_decay=0.0, lr_scale=1.0):
@@ -602,24 +614,26 @@ class AdamWPlan:
         if len(wd) != k or len(ls) != k:
             raise ValueError("weight_decay and lr_scale: one number, or one per parameter")
         state = torch.uint8 if self.bits8 else torch.float32
-        for i, (p, n) in enumerate(zip(params, self._n)):
-            c = self._c[i]
-            runs = -(-n // 128)
-
-            def ptr(t, name, count, dtype):
-                size = torch.empty((), dtype=dtype).element_size()
-                _device(t, f"{name}[{i}]", count * size, dtype)
-                return t.data_ptr()
-            c.param = ptr(p, "params", n, self.param_dtype)
-            c.exp_avg = ptr(exp_avgs[i], "exp_avgs", n, state)
-            c.exp_avg_sq = ptr(exp_avg_sqs[i], "exp_avg_sqs", n, state)
-            if self.bits8:
-                c.exp_avg_scales = ptr(exp_avg_scales[i], "exp_avg_scales", runs, torch.float32)
-                c.exp_avg_sq_scales = ptr(exp_avg_sq_scales[i], "exp_avg_sq_scales", runs, torch.float32)
-            if copies is not None:
-                c.param_copy = ptr(copies[i], "copies", n, torch.bfloat16)
-            c.n, c.weight_decay, c.lr_scale = n, wd[i], ls[i]
+        runs = [-(-n // 128) for n in self._n]
+        self._pointers("param", params, "params", self._n, self.param_dtype)
+        self._pointers("exp_avg", exp_avgs, "exp_avgs", self._n, state)
+        self._pointers("exp_avg_sq", exp_avg_sqs, "exp_avg_sqs", self._n, state)
+        if self.bits8:
+            self._pointers("exp_avg_scales", exp_avg_scales, "exp_avg_scales", runs, torch.float32)
+            self._pointers("exp_avg_sq_scales", exp_avg_sq_scales, "exp_avg_sq_scales", runs, torch.float32)
+        if copies is not None:
+            self._pointers("param_copy", copies, "copies", self._n, torch.bfloat16)
+        for c, n, d, s in zip(self._c, self._n, wd, ls):
+            c.n, c.weight_decay, c.lr_scale = n, d, s
         self.set_grads(grads)
+
+    def _pointers(self, field, tensors, name, counts, dtype) -> None:
+        """Checks one kind of tensors, then puts their addresses into the C array."""
+        size = dtype.itemsize
+        for i, (t, n) in enumerate(zip(tensors, counts)):
+            _device(t, (name, i), n * size, dtype)
+        for c, t in zip(self._c, tensors):
+            setattr(c, field, t.data_ptr())
 
     def set_grads(self, grads) -> None:
         """Use these gradients from now on (all of one dtype)."""
@@ -628,12 +642,16 @@ class AdamWPlan:
         dtype = grads[0].dtype if grads else torch.float32
         if dtype not in _ADAMW_DTYPE:
             raise ValueError(f"gradients must be float32 or bfloat16, not {dtype}")
-        size = 4 if dtype == torch.float32 else 2
-        for i, (g, n) in enumerate(zip(grads, self._n)):
-            _device(g, f"grads[{i}]", n * size, dtype)
-        for c, g in zip(self._c, grads):
-            c.grad = g.data_ptr()
+        self._pointers("grad", grads, "grads", self._n, dtype)
         self.grad_dtype, self._grads = dtype, list(grads)
+        nbytes, chunks = ctypes.c_size_t(0), ctypes.c_int64(0)
+        args = (self._c, len(self._n), _ADAMW_DTYPE[self.param_dtype], _ADAMW_DTYPE[dtype], int(self.bits8))
+        _check(lib.lp_adamw_plan(*args, None, ctypes.byref(nbytes), ctypes.byref(chunks)), "lp_adamw_plan")
+        self._chunks, self._table = chunks.value, None
+        if self._chunks:
+            table = torch.empty(-(-nbytes.value // 8), dtype=torch.int64)
+            _check(lib.lp_adamw_plan(*args, table.data_ptr(), ctypes.byref(nbytes), ctypes.byref(chunks)), "lp_adamw_plan")
+            self._table, self._home = table.to(self._kept[0][0].device), _stream(None)
 
 
 _ADAMW_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
@@ -645,6 +663,9 @@ def lp_adamw(plan: AdamWPlan, lr: float, beta1: float = 0.9, beta2: float = 0.99
     first; grad_scale: a float32 device scalar that multiplies every gradient."""
     if grad_scale is not None:
         _device(grad_scale, "grad_scale", 4, torch.float32)
-    _check(lib.lp_adamw(plan._c, len(plan._n), _ADAMW_DTYPE[plan.param_dtype], _ADAMW_DTYPE[plan.grad_dtype],
-                        int(plan.bits8), lr, beta1, beta2, eps, step,
-                        None if grad_scale is None else grad_scale.data_ptr(), _stream(stream)), "lp_adamw")
+    t, s = plan._table, _stream(stream)
+    if t is not None and s != plan._home:        # not to be reused before that stream is done with it
+        t.record_stream(torch.cuda.ExternalStream(s))
+    _check(lib.lp_adamw(None if t is None else t.data_ptr(), len(plan._n), plan._chunks, _ADAMW_DTYPE[plan.param_dtype],
+                        _ADAMW_DTYPE[plan.grad_dtype], int(plan.bits8), lr, beta1, beta2, eps, step,
+                        None if grad_scale is None else grad_scale.data_ptr(), s), "lp_adamw")

@@ -15,11 +15,12 @@
 // a positive sqrt(v) is never stored as 0 (at least code 1), or the next step
 // would divide by eps alone.
 //
-// Up to kEntries tensors ride in the kernel arguments, so that a call needs
-// no device table and no copy; a workgroup takes one chunk of kChunk elements
-// of one tensor.  A lane holds four consecutive elements (16 bytes of fp32,
-// so every access of a wave is one contiguous KiB), kUnits times, with all
-// loads issued first; 32 lanes hold a run.
+// A table in device memory, made once (lp_adamw_plan), lists the tensors and
+// the tensor of each chunk of kChunk elements, so that a step is one launch
+// whatever the number of tensors, with one lookup per workgroup.  A lane holds
+// four consecutive elements (16 bytes of fp32, so every access of a wave is
+// one contiguous KiB), kUnits times, with all loads issued first; 32 lanes
+// hold a run.
 #include "lp_internal.hpp"
 #include "lp_r128.hpp"
 
@@ -32,8 +33,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnits = 4;
 constexpr int kChunk = kThreads * 4 * kUnits;
-constexpr int kEntries = 48;
-constexpr uint32_t kMaxChunks = 1u << 24;                // a launch has fewer than 2^32 threads; a tensor, at most 2^22 chunks
 
 struct Entry {
   void* p;
@@ -42,18 +41,18 @@ struct Entry {
   float *ms, *vs;
   uint16_t* copy;
   int64_t n;
-  float decay, step;
+  float lr_scale, weight_decay;
   uint32_t first;        // the tensor's first chunk
   int32_t vec;           // every pointer is aligned for four-element accesses
 };
 
 struct Args {
+  const Entry* e;
+  const uint32_t* tensor;                // of each chunk
   float b1, c1, b2, c2, inv_bc2, eps;    // c = 1 - b; inv_bc2 = 1 / sqrt(1 - b2^t)
-  int32_t count;
+  double lr, bc1;                        // bc1 = 1 - b1^t
   const float* grad_scale;
-  Entry e[kEntries];
 };
-static_assert(sizeof(Args) <= 4096, "kernel arguments");
 
 __device__ __forceinline__ uint16_t bf16_bits(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
 
@@ -163,13 +162,9 @@ __device__ __forceinline__ uint32_t quant4(f32x4 x, const RunScale& q) {
 
 template <bool kBf16P, bool kBf16G, bool k8>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args a) {
-  int lo = 0, hi = a.count - 1;                          // the last tensor whose first chunk is at or before this one
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (a.e[mid].first <= blockIdx.x) lo = mid;
-    else hi = mid - 1;
-  }
-  const Entry& e = a.e[lo];
+  const Entry e = a.e[__builtin_amdgcn_readfirstlane((int)a.tensor[blockIdx.x])];
+  const double lr = a.lr * (double)e.lr_scale;
+  const float decay = (float)(1.0 - lr * (double)e.weight_decay), step = (float)(lr / a.bc1);
   const int64_t n = e.n, i0 = (int64_t)(blockIdx.x - e.first) * kChunk + 4 * threadIdx.x;
   const bool vec = e.vec != 0;
   f32x4 p[kUnits], g[kUnits], m[kUnits], v[kUnits];
@@ -209,7 +204,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args a) {
       r[d] = __builtin_sqrtf(vv);
       m[u][d] = mm;
       v[u][d] = vv;
-      p[u][d] = p[u][d] * e.decay - mm / (r[d] * a.inv_bc2 + a.eps) * e.step;
+      p[u][d] = p[u][d] * decay - mm / (r[d] * a.inv_bc2 + a.eps) * step;
     }
     store4<kBf16P>(e.p, i, n, vec, p[u]);
     if (!kBf16P && e.copy != nullptr) store4<true>(e.copy, i, n, vec, p[u]);
@@ -238,46 +233,53 @@ void launch(const Args& a, uint32_t chunks, bool bits8, hipStream_t s) {
 
 bool is_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
+size_t map_offset(int64_t count) { return (size_t)count * sizeof(Entry); }
+
 }  // namespace
 
-hipError_t launch_adamw(const AdamwCall& c, hipStream_t stream) {
-  Args a{};
-  a.b1 = (float)c.beta1;
-  a.c1 = (float)(1.0 - c.beta1);
-  a.b2 = (float)c.beta2;
-  a.c2 = (float)(1.0 - c.beta2);
-  a.inv_bc2 = (float)(1.0 / __builtin_sqrt(1.0 - __builtin_pow(c.beta2, (double)c.step)));
-  a.eps = (float)c.eps;
-  a.grad_scale = c.grad_scale;
-  const double bc1 = 1.0 - __builtin_pow(c.beta1, (double)c.step);
-  int64_t k = 0;
-  while (k < c.count) {
-    uint32_t chunks = 0;
-    a.count = 0;
-    for (; k < c.count && a.count < kEntries; ++k) {
-      const lp_adamw_tensor& t = c.tensors[k];
-      if (t.n == 0) continue;
-      const uint32_t own = (uint32_t)((t.n + kChunk - 1) / kChunk);
-      if (chunks + own >= kMaxChunks) break;
-      Entry& e = a.e[a.count++];
-      const double lr = c.lr * t.lr_scale;
-      e = Entry{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scales, t.exp_avg_sq_scales,
-                static_cast<uint16_t*>(t.param_copy), t.n, (float)(1.0 - lr * t.weight_decay), (float)(lr / bc1),
-                chunks, 0};
-      const uintptr_t state = c.bits8 ? 4 : 16;
-      e.vec = is_aligned(t.param, c.bf16_param ? 8 : 16) && is_aligned(t.grad, c.bf16_grad ? 8 : 16) &&
-              is_aligned(t.exp_avg, state) && is_aligned(t.exp_avg_sq, state) && is_aligned(t.param_copy, 8);
-      chunks += own;
-    }
-    if (chunks == 0) continue;
-    if (c.bf16_param)
-      c.bf16_grad ? launch<true, true>(a, chunks, c.bits8, stream) : launch<true, false>(a, chunks, c.bits8, stream);
-    else
-      c.bf16_grad ? launch<false, true>(a, chunks, c.bits8, stream) : launch<false, false>(a, chunks, c.bits8, stream);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
+int64_t adamw_chunks(const lp_adamw_tensor* tensors, int64_t count) {
+  int64_t chunks = 0;
+  for (int64_t k = 0; k < count; ++k) chunks += chunks_of(tensors[k].n);
+  return chunks;
+}
+
+size_t adamw_table_bytes(int64_t count, int64_t chunks) { return map_offset(count) + (size_t)chunks * 4; }
+
+void adamw_fill(const lp_adamw_tensor* tensors, int64_t count, bool bf16_param, bool bf16_grad, bool bits8, void* table) {
+  Entry* const entries = static_cast<Entry*>(table);
+  uint32_t* map = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(table) + map_offset(count));
+  uint32_t first = 0;
+  for (int64_t k = 0; k < count; ++k) {
+    const lp_adamw_tensor& t = tensors[k];
+    const uintptr_t state = bits8 ? 4 : 16;
+    const bool vec = is_aligned(t.param, bf16_param ? 8 : 16) && is_aligned(t.grad, bf16_grad ? 8 : 16) &&
+                     is_aligned(t.exp_avg, state) && is_aligned(t.exp_avg_sq, state) && is_aligned(t.param_copy, 8);
+    entries[k] = Entry{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scales, t.exp_avg_sq_scales,
+                       static_cast<uint16_t*>(t.param_copy), t.n, t.lr_scale, t.weight_decay, first, vec};
+    for (int64_t c = chunks_of(t.n); c > 0; --c, ++first) *map++ = (uint32_t)k;
   }
-  return hipSuccess;
+}
+
+hipError_t launch_adamw(const AdamwCall& c, hipStream_t stream) {
+  const uint8_t* const table = static_cast<const uint8_t*>(c.table);
+  const Args a{reinterpret_cast<const Entry*>(table),
+               reinterpret_cast<const uint32_t*>(table + map_offset(c.count)),
+               (float)c.beta1,
+               (float)(1.0 - c.beta1),
+               (float)c.beta2,
+               (float)(1.0 - c.beta2),
+               (float)(1.0 / __builtin_sqrt(1.0 - __builtin_pow(c.beta2, (double)c.step))),
+               (float)c.eps,
+               c.lr,
+               1.0 - __builtin_pow(c.beta1, (double)c.step),
+               c.grad_scale};
+  const uint32_t chunks = (uint32_t)c.chunks;
+  if (c.bf16_param)
+    c.bf16_grad ? launch<true, true>(a, chunks, c.bits8, stream) : launch<true, false>(a, chunks, c.bits8, stream);
+  else
+    c.bf16_grad ? launch<false, true>(a, chunks, c.bits8, stream) : launch<false, false>(a, chunks, c.bits8, stream);
+  return hipGetLastError();
 }
 
 }  // namespace lp

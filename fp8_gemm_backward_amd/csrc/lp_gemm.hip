@@ -394,7 +394,7 @@ hipError_t launch_fwd(const lp_qtensor& x, const lp_qtensor& w, const int32_t* o
 hipError_t launch_fwd_dyn(const void* x, const lp_qtensor& xq, const lp_qtensor& w, const int32_t* offsets,
                           int32_t groups, void* x_codes, void* x_scales, void* y, hipStream_t stream) {
   const Params prm = fwd_params(xq, w, offsets, groups, y);
-  if (b128_can_fuse(prm)) return b128_fwd_fused(prm, x, stream);
+  if (fwd_dyn_fuses(xq.rows, xq.cols, offsets != nullptr)) return b128_fwd_fused(prm, x, stream);
   if (xq.cols > 0) {
     const hipError_t e = launch_r128_cols(x, 1, xq.rows, xq.cols, x_codes, x_scales, stream);
     if (e != hipSuccess) return e;

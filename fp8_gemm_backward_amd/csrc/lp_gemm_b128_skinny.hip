@@ -175,11 +175,6 @@ hipError_t launch(SkinnyArgs a, size_t lds, hipStream_t s) {
 
 }  // namespace
 
-bool b128_can_fuse(const Params& prm) {
-  const int64_t nb = (prm.Ktot + kRun - 1) / kRun;
-  return prm.offsets == nullptr && prm.Ptot <= kFuseRows && prm.Ptot * nb * kRun <= kFuseLds;
-}
-
 hipError_t b128_fwd_fused(const Params& prm, const void* x, hipStream_t s) {
   const size_t nb = ((size_t)prm.Ktot + kRun - 1) / kRun;
   return launch<8, true>(SkinnyArgs{prm, static_cast<const uint16_t*>(x), 0}, nb * (4 * kFuseRows + (size_t)prm.Ptot * kRun), s);
@@ -192,4 +187,9 @@ hipError_t b128_fwd_skinny(const Params& prm, hipStream_t s) {
 }
 
 }  // namespace gk
+
+bool fwd_dyn_fuses(int64_t M, int64_t K, bool grouped) {
+  return !grouped && M <= gk::kFuseRows && M * ((K + gk::kRun - 1) / gk::kRun) * gk::kRun <= gk::kFuseLds;
+}
+
 }  // namespace lp

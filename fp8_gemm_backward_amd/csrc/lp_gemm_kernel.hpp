@@ -1008,10 +1008,9 @@ hipError_t dec_pair(const Params& dx, const Params& dw, int fmt_q, hipStream_t s
 // tiles (256, 128 or 64).
 hipError_t b128_fwd(const Params& prm, int tile, hipStream_t s);
 // The forward of few rows; and from a bf16 x of at most kFuseRows rows that
-// the kernel quantizes itself, when b128_can_fuse says so.
+// the kernel quantizes itself, when fwd_dyn_fuses says so.
 constexpr int kFuseRows = 4;
 hipError_t b128_fwd_skinny(const Params& prm, hipStream_t s);
-bool b128_can_fuse(const Params& prm);
 hipError_t b128_fwd_fused(const Params& prm, const void* x, hipStream_t s);
 hipError_t b128_dx(const Params& prm, int tile, hipStream_t s);
 hipError_t b128_dw(const Params& prm, int tile, hipStream_t s);

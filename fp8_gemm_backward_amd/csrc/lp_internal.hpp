@@ -115,10 +115,18 @@ hipError_t launch_r128_tiles(const void* src, int64_t batch, int64_t rows, int64
 hipError_t launch_fwd_dyn(const void* x, const lp_qtensor& xq, const lp_qtensor& w, const int32_t* offsets,
                           int32_t groups, void* x_codes, void* x_scales, void* y, hipStream_t stream);
 
-// One AdamW step (lp_adamw.hip); arguments checked by the caller.
+// Whether that forward takes x as it is, quantizing inside the product.
+bool fwd_dyn_fuses(int64_t M, int64_t K, bool grouped);
+
+// The AdamW step's table (lp_adamw.hip): its size, its chunks, its contents.
+// Arguments checked by the caller.
+int64_t adamw_chunks(const lp_adamw_tensor* tensors, int64_t count);
+size_t adamw_table_bytes(int64_t count, int64_t chunks);
+void adamw_fill(const lp_adamw_tensor* tensors, int64_t count, bool bf16_param, bool bf16_grad, bool bits8, void* table);
+// One step with the device copy of the table.
 struct AdamwCall {
-  const lp_adamw_tensor* tensors;
-  int64_t count;
+  const void* table;
+  int64_t count, chunks;
   bool bf16_param, bf16_grad, bits8;
   double lr, beta1, beta2, eps;
   int64_t step;

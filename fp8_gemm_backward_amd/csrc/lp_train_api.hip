@@ -8,6 +8,7 @@
 namespace {
 
 constexpr int64_t kMaxElems = (int64_t)1 << 34;
+constexpr int64_t kMaxChunks = (int64_t)1 << 24;   // workgroups of 256 threads: a launch has fewer than 2^32 threads
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 lp_status hip_status(hipError_t e) { return e == hipSuccess ? LP_OK : LP_ERR_HIP; }
@@ -48,6 +49,8 @@ lp_status fwd_dyn(const void* x, int64_t M, const lp_qtensor* w, const int32_t* 
   if (w->fmt != LP_FP8_B128) return LP_ERR_FORMAT;
   lp_status st = check_quant(1, M, w->cols, true, nullptr, 0);
   if (st != LP_OK) return st;
+  const bool fused = lp::fwd_dyn_fuses(M, w->cols, groups != 0);
+  if (fused) x_codes = x_scales = const_cast<void*>(x);          // not touched: stand-ins for the checks
   const void* ptrs[] = {x, x_codes, x_scales};
   if ((st = check_buffers(M * w->cols, ptrs, 3)) != LP_OK) return st;
   const lp_qtensor xq{LP_FP8_R128, -1, 1, M, w->cols, x_codes, x_scales, nullptr};
@@ -62,6 +65,12 @@ lp_status fwd_dyn(const void* x, int64_t M, const lp_qtensor* w, const int32_t* 
 }
 
 bool bad_factor(double v) { return !(v >= 0.0) || isinf(v); }
+
+lp_status check_dtypes(int32_t param, int32_t grad, int32_t state) {
+  for (int32_t d : {param, grad})
+    if (d != LP_DTYPE_F32 && d != LP_DTYPE_BF16) return LP_ERR_FORMAT;
+  return state == LP_STATE_F32 || state == LP_STATE_E4M3 ? LP_OK : LP_ERR_FORMAT;
+}
 
 }  // namespace
 
@@ -116,16 +125,12 @@ lp_status lp_grouped_fwd_dyn(const void* x, int64_t M, const lp_qtensor* w, cons
   return fwd_dyn(x, M, w, offsets, groups, x_codes, x_scales, y, stream);
 }
 
-lp_status lp_adamw(const lp_adamw_tensor* tensors, int64_t count, int32_t param_dtype, int32_t grad_dtype,
-                   int32_t state_dtype, double lr, double beta1, double beta2, double eps, int64_t step,
-                   const float* grad_scale, void* stream) {
-  if (count < 0 || step < 1 || bad_factor(lr) || bad_factor(eps)) return LP_ERR_SHAPE;
-  if (!(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0)) return LP_ERR_SHAPE;
-  for (int32_t d : {param_dtype, grad_dtype})
-    if (d != LP_DTYPE_F32 && d != LP_DTYPE_BF16) return LP_ERR_FORMAT;
-  if (state_dtype != LP_STATE_F32 && state_dtype != LP_STATE_E4M3) return LP_ERR_FORMAT;
-  if (count > 0 && tensors == nullptr) return LP_ERR_NULL;
-  if (!aligned(grad_scale, 4)) return LP_ERR_ALIGN;
+lp_status lp_adamw_plan(const lp_adamw_tensor* tensors, int64_t count, int32_t param_dtype, int32_t grad_dtype,
+                        int32_t state_dtype, void* table, size_t* table_bytes, int64_t* chunks) {
+  if (count < 0 || count >= kMaxChunks) return LP_ERR_SHAPE;
+  lp_status st = check_dtypes(param_dtype, grad_dtype, state_dtype);
+  if (st != LP_OK) return st;
+  if (table_bytes == nullptr || chunks == nullptr || (count > 0 && tensors == nullptr)) return LP_ERR_NULL;
   const bool bits8 = state_dtype == LP_STATE_E4M3, bp = param_dtype == LP_DTYPE_BF16, bg = grad_dtype == LP_DTYPE_BF16;
   for (int64_t k = 0; k < count; ++k) {
     const lp_adamw_tensor& t = tensors[k];
@@ -138,7 +143,30 @@ lp_status lp_adamw(const lp_adamw_tensor* tensors, int64_t count, int32_t param_
     if (!bits8 && (!aligned(t.exp_avg, 4) || !aligned(t.exp_avg_sq, 4))) return LP_ERR_ALIGN;
     if (bits8 && (!aligned(t.exp_avg_scales, 4) || !aligned(t.exp_avg_sq_scales, 4))) return LP_ERR_ALIGN;
   }
-  const lp::AdamwCall c{tensors, count, bp, bg, bits8, lr, beta1, beta2, eps, step, grad_scale};
+  const int64_t n = lp::adamw_chunks(tensors, count);
+  if (n >= kMaxChunks) return LP_ERR_SHAPE;
+  const size_t need = lp::adamw_table_bytes(count, n), have = *table_bytes;
+  *table_bytes = need;
+  *chunks = n;
+  if (table == nullptr) return LP_OK;
+  if (!aligned(table, 8)) return LP_ERR_ALIGN;
+  if (have < need) return LP_ERR_SHAPE;
+  lp::adamw_fill(tensors, count, bp, bg, bits8, table);
+  return LP_OK;
+}
+
+lp_status lp_adamw(const void* table, int64_t count, int64_t chunks, int32_t param_dtype, int32_t grad_dtype,
+                   int32_t state_dtype, double lr, double beta1, double beta2, double eps, int64_t step,
+                   const float* grad_scale, void* stream) {
+  if (count < 0 || chunks < 0 || chunks >= kMaxChunks || step < 1 || bad_factor(lr) || bad_factor(eps)) return LP_ERR_SHAPE;
+  if (!(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0)) return LP_ERR_SHAPE;
+  lp_status st = check_dtypes(param_dtype, grad_dtype, state_dtype);
+  if (st != LP_OK) return st;
+  if (chunks > 0 && table == nullptr) return LP_ERR_NULL;
+  if (!aligned(table, 8) || !aligned(grad_scale, 4)) return LP_ERR_ALIGN;
+  if (chunks == 0) return LP_OK;
+  const lp::AdamwCall c{table, count, chunks, param_dtype == LP_DTYPE_BF16, grad_dtype == LP_DTYPE_BF16,
+                        state_dtype == LP_STATE_E4M3, lr, beta1, beta2, eps, step, grad_scale};
   return hip_status(lp::launch_adamw(c, static_cast<hipStream_t>(stream)));
 }
 

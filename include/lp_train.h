@@ -82,7 +82,9 @@ lp_status lp_b128_quant(const void* src_bf16, int64_t batch, int64_t rows, int64
  * x_codes   device bytes [M][K] and
  * x_scales  device fp32 [ceil(K/128)][M]: caller-owned scratch, not to be
  *           shared by calls that may overlap; its contents afterwards are
- *           unspecified (calls of few rows quantize x inside the product).
+ *           unspecified.  lp_linear_fwd_dyn of M <= 4 rows with M * 128 *
+ *           ceil(K/128) <= 65536 quantizes x inside the product and needs none
+ *           (both may be NULL).
  * y         device bf16 [M][N]; lp_grouped_fwd_dyn leaves rows at or past
  *           the last offset unwritten.
  * Errors as lp_r128_quant and lp_linear_fwd / lp_grouped_fwd, found before
@@ -94,7 +96,8 @@ lp_status lp_grouped_fwd_dyn(const void* x_bf16, int64_t M, const lp_qtensor* w,
                              int64_t groups, void* x_codes, void* x_scales, void* y, void* stream);
 
 /*
- * lp_adamw - one AdamW step (decoupled weight decay) over many tensors.
+ * lp_adamw_plan, lp_adamw - one AdamW step (decoupled weight decay) over many
+ * tensors, in one launch.
  *
  *   g = grad * grad_scale
  *   m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
@@ -103,26 +106,38 @@ lp_status lp_grouped_fwd_dyn(const void* x_bf16, int64_t M, const lp_qtensor* w,
  * with lr = lr * lr_scale and wd = weight_decay of the tensor.  Each operation
  * is rounded to fp32 by itself; the factors that depend on the step only are
  * computed in double, then rounded.  An fp32 or bf16 parameter, an fp32 or
- * bf16 gradient; one combination per call.
+ * bf16 gradient; one combination per plan.
  *
+ * lp_adamw_plan writes the table that lp_adamw reads: which tensors, and which
+ * part of them each workgroup takes.  It runs on the host and touches no GPU.
+ * The caller copies the table to device memory once and keeps it (and the
+ * tensors) as long as it steps with it; a plan is made anew when a tensor moves.
+ *
+ * tensors      HOST array of `count`, not kept.  Pointers need the alignment of
+ *              their element only; tensors whose pointers are all aligned to
+ *              four elements (param, grad, exp_avg, exp_avg_sq, param_copy) take
+ *              wider accesses.  Tensors of one plan must not overlap.
  * state_dtype  LP_STATE_F32: exp_avg and exp_avg_sq are fp32 [n].
  *              LP_STATE_E4M3: exp_avg holds E4M3 codes of m, exp_avg_sq those
  *              of sqrt(v), bytes [n], in runs of 128 consecutive elements by
  *              the quantization rule above, with fp32 scales
  *              [ceil(n/128)] each; a positive sqrt(v) never becomes 0 (at
  *              least code 1).  All-zero codes and scales are the initial state.
- * grad_scale   device fp32, or NULL for 1 (loss scaling, clipping).
- * step         1 for the first step.
- * tensors      HOST array of `count`; the struct is not kept after the call.
- *              Pointers need the alignment of their element only; tensors
- *              whose pointers are all aligned to four elements (param, grad,
- *              exp_avg, exp_avg_sq, param_copy) take wider accesses.
- * Tensors of one call must not overlap.  Nothing is read or written for n = 0.
- * Errors: LP_ERR_SHAPE for count < 0, n < 0 or n >= 2^34, step < 1, betas
- * outside [0, 1), a negative or non-finite lr, eps, lr_scale or weight_decay;
- * LP_ERR_FORMAT for an unknown dtype, or a param_copy beside a bf16
- * parameter; LP_ERR_NULL, LP_ERR_ALIGN as usual.  Checked for every tensor
- * before anything is enqueued.
+ * table        HOST buffer, 8-byte aligned, or NULL to ask for its size only.
+ * table_bytes  in: the buffer's size; out: the bytes needed.
+ * chunks       out: the number of workgroups, an argument of lp_adamw.
+ * Errors: LP_ERR_SHAPE for count < 0, n < 0 or n >= 2^34, a negative or
+ * non-finite lr_scale or weight_decay, 2^24 chunks or more (a chunk is 4096
+ * elements of one tensor), or a buffer too small; LP_ERR_FORMAT for an unknown
+ * dtype, or a param_copy beside a bf16 parameter; LP_ERR_NULL, LP_ERR_ALIGN as
+ * usual.
+ *
+ * lp_adamw     table is the DEVICE copy (8-byte aligned); count, chunks and the
+ *              dtypes those of its plan.  grad_scale: device fp32, or NULL for 1
+ *              (loss scaling, clipping).  step: 1 for the first.
+ * Errors: LP_ERR_SHAPE for step < 1, betas outside [0, 1), a negative or
+ * non-finite lr or eps, count < 0, chunks outside [0, 2^24); LP_ERR_FORMAT,
+ * LP_ERR_NULL, LP_ERR_ALIGN.
  */
 enum { LP_STATE_F32 = 0, LP_STATE_E4M3 = 1 };
 enum { LP_DTYPE_F32 = 0, LP_DTYPE_BF16 = 1 };
@@ -140,7 +155,9 @@ typedef struct {
   float weight_decay;
 } lp_adamw_tensor;
 
-lp_status lp_adamw(const lp_adamw_tensor* tensors, int64_t count, int32_t param_dtype, int32_t grad_dtype,
+lp_status lp_adamw_plan(const lp_adamw_tensor* tensors, int64_t count, int32_t param_dtype, int32_t grad_dtype,
+                        int32_t state_dtype, void* table, size_t* table_bytes, int64_t* chunks);
+lp_status lp_adamw(const void* table, int64_t count, int64_t chunks, int32_t param_dtype, int32_t grad_dtype,
                    int32_t state_dtype, double lr, double beta1, double beta2, double eps, int64_t step,
                    const float* grad_scale, void* stream);
 

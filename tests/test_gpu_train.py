@@ -350,7 +350,7 @@ def adam_inputs(rng, n, first=False):
 @pytest.mark.parametrize("param_bf16", [False, True])
 @pytest.mark.parametrize("shift", [0, 1])
 def test_adamw_bit_exact(lp, bits8, grad_bf16, param_bf16, shift):
-    """Many tensors of odd sizes at once (more than one launch takes), aligned or one element off; against the fp32
+    """Many tensors of odd sizes at once, aligned or one element off; against the fp32
     operations one by one, and their distance from the fp64 formula."""
     rng = np.random.default_rng(7 + shift)
     step, wd = 3, 0.1
@@ -474,3 +474,90 @@ def test_adamw_set_grads_and_empty(lp):
     lp.lp_adamw(lp.AdamWPlan([e], [e], [e], [e]), lr=0.1)
     lp.lp_adamw(lp.AdamWPlan([], [], [], []), lr=0.1)
     torch.cuda.synchronize()
+
+
+def test_adamw_other_stream_and_replaced_gradients(lp):
+    """A step on another stream, then new gradients (a new table) while it may still run, then another step."""
+    rng = np.random.default_rng(11)
+    sizes = [5000, 1, 300]
+    start = [adam_inputs(rng, n) for n in sizes]
+    second = [adam_inputs(rng, n)[1] for n in sizes]
+
+    def run(stream, direct):
+        p, m, v = ([dev(t[k] if k < 3 else t[k] * t[k]) for t in start] for k in (0, 2, 3))
+        g1, g2 = [bf16_dev(t[1]) for t in start], [bf16_dev(t) for t in second]
+        plan = lp.AdamWPlan(p, g1, m, v, weight_decay=[0.1, 0.0, 0.2], lr_scale=[1.0, 2.0, 0.5])
+        torch.cuda.synchronize()
+        with torch.cuda.stream(torch.cuda.current_stream() if direct else stream):
+            lp.lp_adamw(plan, step=1, stream=stream if direct else None, **HYPER)
+        plan.set_grads(g2)
+        junk = torch.full((4096,), -1, dtype=torch.int64, device="cuda")        # would take a table freed too early
+        lp.lp_adamw(plan, step=2, stream=stream, **HYPER)
+        torch.cuda.synchronize()
+        del junk
+        return p + m + v
+
+    want = run(torch.cuda.current_stream(), True)
+    for direct in (True, False):
+        got = run(torch.cuda.Stream(), direct)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("sizes", [[130, 0, 1, 300], [2, 0, 0, 1]])
+def test_training_step_in_a_graph(lp, sizes):
+    """Forward, quantized gradients, both products, AdamW with 8-bit moments and the new weight's quantization, captured
+    once: every replay equals the same step done eagerly."""
+    rng = np.random.default_rng(13)
+    G, N, K, M = 4, 272, 400, sum(sizes)
+    off = dev(ends_of(sizes))
+    master = dev(f32(rng.standard_normal((G, N, K)) * 0.05))
+    xs = [bf16_dev(bits(rng, (M, K))) for _ in range(4)]
+    gs = [bf16_dev(bits(rng, (M, N), 1e-3)) for _ in range(4)]
+
+    def fresh():
+        n = G * N * K
+        s = dict(p=master.clone(), copy=torch.zeros((G, N, K), dtype=torch.bfloat16, device="cuda"),
+                 m=torch.zeros(n, dtype=torch.uint8, device="cuda"), v=torch.zeros(n, dtype=torch.uint8, device="cuda"),
+                 ms=torch.zeros(-(-n // 128), device="cuda"), vs=torch.zeros(-(-n // 128), device="cuda"),
+                 x=xs[0].clone(), g=gs[0].clone(), dw=torch.zeros((G, N, K), dtype=torch.bfloat16, device="cuda"))
+        s["w"] = lp.lp_b128_quant(master.bfloat16())
+        s["plan"] = lp.AdamWPlan([s["p"]], [s["dw"]], [s["m"]], [s["v"]], exp_avg_scales=[s["ms"]],
+                                 exp_avg_sq_scales=[s["vs"]], copies=[s["copy"]], weight_decay=0.1)
+        return s
+
+    def step(s):
+        y = lp.lp_grouped_fwd_dyn(s["x"], s["w"], off)
+        _, xr = lp.lp_r128_quant_dual(s["x"], off)
+        gc, gr = lp.lp_r128_quant_dual(s["g"], off)
+        dx, _ = lp.lp_grouped_bwd(gc, None, s["w"], off, need_dw=False)
+        lp.lp_grouped_bwd(gr, xr, None, off, need_dx=False, grad_w=s["dw"])
+        lp.lp_adamw(s["plan"], step=1, **HYPER)
+        s["w"].codes.copy_((q := lp.lp_b128_quant(s["copy"])).codes)
+        s["w"].scales.copy_(q.scales)
+        return y, dx
+
+    def outputs(s, out):
+        return [t.clone() for t in (*out, s["dw"], s["p"], s["copy"], s["m"], s["v"], s["ms"], s["vs"], s["w"].codes, s["w"].scales)]
+
+    eager = fresh()
+    want = []
+    for x, g in zip(xs, gs):
+        eager["x"].copy_(x), eager["g"].copy_(g)
+        want.append(outputs(eager, step(eager)))
+    s = fresh()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(fresh())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(s)
+    for k, (x, g) in enumerate(zip(xs, gs)):
+        s["x"].copy_(x), s["g"].copy_(g)
+        graph.replay()
+        got = outputs(s, out)
+        step(fresh())                                    # eager work between the replays
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(want[k], got)):
+            assert torch.equal(a, b), (k, i)

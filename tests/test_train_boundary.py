@@ -26,9 +26,9 @@ def q(fmt, rows, cols, batch=1, axis=-1, codes=FAKE, scales=FAKE):
 def test_library_exports_every_function_of_the_header():
     text = open(os.path.join(os.path.dirname(lp.HEADER_PATH), "lp_train.h")).read()
     names = re.findall(r"^lp_status\s+(lp_\w+)\s*\(", text, re.M)
-    assert len(names) == 6
+    assert len(names) == 7
     for n in names:
-        assert hasattr(lp.lib, n) and hasattr(lp, n), n
+        assert hasattr(lp.lib, n) and hasattr(lp, "AdamWPlan" if n == "lp_adamw_plan" else n), n
 
 
 @pytest.mark.parametrize("args,expect", [
@@ -128,6 +128,8 @@ def test_forwards_that_quantize_reject():
         assert lin_(*a) == NULL
         a[at] = FAKE + 2
         assert lin_(*a) == ALIGN
+    assert lin_(FAKE, 4, w(), None, None, None, None) == NULL      # few rows need no scratch, but an output
+    assert lin_(FAKE, 4, w(cols=16400), None, None, FAKE, None) == NULL
     assert lin_(FAKE, 8, w(fmt="bf16"), FAKE, FAKE, FAKE, None) == FORMAT
     assert lin_(FAKE, -1, w(), FAKE, FAKE, FAKE, None) == SHAPE
     assert lin_(FAKE, 8, w(rows=40), FAKE, FAKE, FAKE, None) == SHAPE
@@ -140,33 +142,58 @@ def test_forwards_that_quantize_reject():
     assert grp(FAKE, 8, w(batch=2), FAKE + 2, 2, FAKE, FAKE, FAKE, None) == ALIGN
 
 
-def adamw(tensors=None, count=None, pd=0, gd=0, sd=0, lr=1e-3, b1=0.9, b2=0.99, eps=1e-8, step=1, gs=None):
-    tensors = [tensor()] if tensors is None else tensors
-    c = (_AdamWTensorC * max(len(tensors), 1))(*tensors)
-    return lp.lib.lp_adamw(c, len(tensors) if count is None else count, pd, gd, sd, lr, b1, b2, eps, step, gs, None)
-
-
 def tensor(n=8, param=FAKE, grad=FAKE, m=FAKE, v=FAKE, ms=None, vs=None, copy=None, ls=1.0, wd=0.0):
     return _AdamWTensorC(param, grad, m, v, ms, vs, copy, n, ls, wd)
 
 
+def plan(tensors=None, count=None, pd=0, gd=0, sd=0, table=None, size=0):
+    tensors = [tensor()] if tensors is None else tensors
+    c = (_AdamWTensorC * max(len(tensors), 1))(*tensors)
+    need, chunks = ctypes.c_size_t(size), ctypes.c_int64(-1)
+    st = lp.lib.lp_adamw_plan(c, len(tensors) if count is None else count, pd, gd, sd, table, ctypes.byref(need),
+                              ctypes.byref(chunks))
+    return st, need.value, chunks.value
+
+
 @pytest.mark.parametrize("kw,expect", [
-    (dict(count=-1), SHAPE), (dict(step=0), SHAPE), (dict(b1=1.0), SHAPE), (dict(b2=-0.1), SHAPE),
-    (dict(lr=-1.0), SHAPE), (dict(lr=float("nan")), SHAPE), (dict(eps=float("inf")), SHAPE), (dict(b1=float("nan")), SHAPE),
-    (dict(pd=2), FORMAT), (dict(gd=-1), FORMAT), (dict(sd=2), FORMAT), (dict(gs=FAKE + 2), ALIGN),
+    (dict(count=-1), SHAPE), (dict(pd=2), FORMAT), (dict(gd=-1), FORMAT), (dict(sd=2), FORMAT),
     (dict(tensors=[tensor(n=-1)]), SHAPE), (dict(tensors=[tensor(n=1 << 34)]), SHAPE),
+    (dict(tensors=[tensor(n=(1 << 34) - 1)] * 4), SHAPE),          # too many chunks together
     (dict(tensors=[tensor(wd=-1.0)]), SHAPE), (dict(tensors=[tensor(ls=float("inf"))]), SHAPE),
+    (dict(tensors=[tensor(wd=float("nan"))]), SHAPE),
     (dict(tensors=[tensor(param=None)]), NULL), (dict(tensors=[tensor(grad=None)]), NULL),
     (dict(tensors=[tensor(m=None)]), NULL), (dict(tensors=[tensor(v=None)]), NULL),
     (dict(sd=1), NULL), (dict(sd=1, tensors=[tensor(ms=FAKE)]), NULL),
     (dict(tensors=[tensor(param=FAKE + 2)]), ALIGN), (dict(gd=1, tensors=[tensor(grad=FAKE + 1)]), ALIGN),
     (dict(tensors=[tensor(m=FAKE + 1)]), ALIGN), (dict(sd=1, tensors=[tensor(ms=FAKE, vs=FAKE + 2)]), ALIGN),
     (dict(pd=1, tensors=[tensor(copy=FAKE)]), FORMAT),
-    (dict(tensors=[tensor(n=0), tensor(m=None)]), NULL),           # every tensor is checked first
+    (dict(tensors=[tensor(n=0), tensor(m=None)]), NULL),           # every tensor is checked
+    (dict(table=FAKE + 4), ALIGN), (dict(table=FAKE, size=8), SHAPE),
     (dict(tensors=[tensor(n=0, param=None, grad=None, m=None, v=None)]), OK), (dict(tensors=[]), OK),
 ])
+def test_adamw_plan_rejects(kw, expect):
+    assert plan(**kw)[0] == expect
+
+
+def test_adamw_plan_chunks_and_size():
+    st, need, chunks = plan([tensor(n=n) for n in (1, 4096, 4097, 0, 10000)])
+    assert (st, chunks) == (OK, 1 + 1 + 2 + 0 + 3) and need >= 5 * 64 + 7 * 4
+    buf = ctypes.create_string_buffer(need + 8)
+    assert plan([tensor(n=n) for n in (1, 4096, 4097, 0, 10000)], table=(ctypes.addressof(buf) + 7) // 8 * 8, size=need)[0] == OK
+    c = (_AdamWTensorC * 1)(tensor())
+    assert lp.lib.lp_adamw_plan(c, 1, 0, 0, 0, None, None, ctypes.byref(ctypes.c_int64())) == NULL
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(count=-1), SHAPE), (dict(chunks=-1), SHAPE), (dict(chunks=1 << 24), SHAPE), (dict(step=0), SHAPE),
+    (dict(b1=1.0), SHAPE), (dict(b2=-0.1), SHAPE), (dict(b1=float("nan")), SHAPE), (dict(lr=-1.0), SHAPE),
+    (dict(lr=float("nan")), SHAPE), (dict(eps=float("inf")), SHAPE), (dict(pd=2), FORMAT), (dict(gd=-1), FORMAT),
+    (dict(sd=2), FORMAT), (dict(table=None), NULL), (dict(table=FAKE + 4), ALIGN), (dict(gs=FAKE + 2), ALIGN),
+    (dict(table=None, chunks=0), OK),
+])
 def test_adamw_rejects(kw, expect):
-    assert adamw(**kw) == expect
+    a = {**dict(table=FAKE, count=1, chunks=1, pd=0, gd=0, sd=0, lr=1e-3, b1=0.9, b2=0.99, eps=1e-8, step=1, gs=None), **kw}
+    assert lp.lib.lp_adamw(*a.values(), None) == expect
 
 
 def test_binding_rejects_host_tensors_and_mismatches():
