@@ -105,4 +105,17 @@ __device__ __forceinline__ uint32_t fix_nan_pair(uint32_t v, uint32_t sign_lo, u
   return lo | (hi << 16);
 }
 
+// Inclusive scan over the wave by DPP shifts inside the lane rows and
+// broadcasts across them.
+template <class F>
+__device__ __forceinline__ int wave_scan(int v, F op) {          // 0 is neutral
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false));   // row_shr:1
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false));   // row_shr:2
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false));   // row_shr:4
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false));   // row_shr:8
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));   // row_bcast:15 into rows 1 and 3
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));   // row_bcast:31 into rows 2 and 3
+  return v;
+}
+
 }  // namespace lp

@@ -211,18 +211,7 @@ struct B128Frag {
 // bounded by 576, took 163 us for 124.
 //
 // Every wave scans 64 groups at a time, one a lane: the clamped ends are a
-// running maximum, the row tiles before each group a running sum, both by DPP
-// shifts inside the lane rows and broadcasts across them.
-template <class F>
-__device__ __forceinline__ int wave_scan(int v, F op) {          // inclusive; 0 is neutral
-  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false));   // row_shr:1
-  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false));   // row_shr:2
-  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false));   // row_shr:4
-  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false));   // row_shr:8
-  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));   // row_bcast:15 into rows 1 and 3
-  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));   // row_bcast:31 into rows 2 and 3
-  return v;
-}
+// running maximum, the row tiles before each group a running sum (wave_scan).
 struct GroupScan {
   int start, end, seen;      // of this lane's group: first row, end row, row tiles before it
   int last_end, last_seen;   // after the 64 groups
