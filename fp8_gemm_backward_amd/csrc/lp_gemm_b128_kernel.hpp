@@ -21,7 +21,9 @@
 // sums must be ordinary vector registers (vector instructions cannot use
 // accumulation registers), which sets the tile shape: 256 x 256 outputs by
 // eight waves of 128 x 64 (128 registers of sums, two waves per SIMD), or,
-// for few tiles, 128 x 128 by four waves of 64 x 64.
+// for few tiles, 128 x 128 by two groups of four waves of 64 x 64, or 64 x 64 by
+// four groups of two waves of 32 x 64; the groups of waves share the
+// contraction.
 //
 // A 128-deep stage of both operands and its scales goes from global memory
 // straight into LDS, two stages deep; one barrier per stage.  LDS layouts:
@@ -192,9 +194,11 @@ struct B128Frag {
         for (int d = 0; d < 4; ++d) v[4 * e + d] = (int)x[d];
       }
     } else {
+      // (tile is a multiple of 256: one sum for all f, where a ^ 16 f would keep a register each)
+      const uint32_t at = ((uint32_t)(uintptr_t)(lds_i32x2b*)tile + (uint32_t)a) ^ (16 * f);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const i32x2b x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2b*)(tile + (a ^ (16 * f)) + (64 * (t / 2) + 8 * (t % 2)) * kMN));
+        const i32x2b x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2b*)(at + (64 * (t / 2) + 8 * (t % 2)) * kMN));
         v[2 * t] = x[0];
         v[2 * t + 1] = x[1];
       }
@@ -202,6 +206,16 @@ struct B128Frag {
     return v;
   }
 };
+
+// Tiles of a dense product: a contiguous range for each XCD, in blocks that
+// share operand rows and columns.
+template <class C>
+__device__ __forceinline__ Tile dense_tile(const Params& p, int hw) {
+  const int tile = xcd_remap(hw, p.ntiles);
+  int2 pq = make_int2(tile / p.nq, tile % p.nq);
+  if (p.gm > 1) pq = grouped_order(tile, (p.Ptot + C::BP - 1) / C::BP, p.nq, p.gm);
+  return Tile{0, pq.x * C::BP, p.Ptot, pq.y * C::BQ, 0, p.Ktot, tile, 0, true};
+}
 
 // Tiles of a grouped forward or grad_X.  Row tiles of 256 rows or less never
 // straddle a group; the workgroups deal the tiles that exist (their number is
@@ -233,22 +247,26 @@ __device__ __forceinline__ GroupScan scan_groups(const Params& p, int M, int bas
 // Params::tail: 0, every tile; 1, the whole rounds of kCUs tiles when the
 // last, partial one has at most kCUs / 2 (every tile otherwise); 2 (256 x 128
 // tiles), what 1 leaves, each 256 x 256 tile as its two halves.
+//
+// sc0: the scan of at most 64 groups, unless there are more.
 template <class C>
-__device__ __forceinline__ Tile grouped_tile(const Params& p) {
+__device__ __forceinline__ Tile grouped_tile(const Params& p, const GroupScan& sc0, int hw) {
   Tile t{0, 0, 0, 0, 0, p.Ktot, 0, 0, false};
-  GroupScan sc{};
-  int end0 = 0, rows = 0;
-  for (int base = 0; base < p.groups; base += 64) {
-    sc = scan_groups<C::BP>(p, p.Ptot, base, end0, rows);
-    end0 = sc.last_end;
-    rows = sc.last_seen;
+  GroupScan sc = sc0;
+  int end0 = 0, rows = sc0.last_seen;
+  if (p.groups > 64) {
+    rows = 0;
+    for (int base = 0; base < p.groups; base += 64) {
+      sc = scan_groups<C::BP>(p, p.Ptot, base, end0, rows);
+      end0 = sc.last_end;
+      rows = sc.last_seen;
+    }
   }
   const bool halves = p.tail == 2;
   const int nq = halves ? (p.Qtot + 255) / 256 : p.nq;
   const int all = rows * nq, full = all / kCUs * kCUs, rest = all - full;
   const bool split = p.tail != 0 && full > 0 && rest > 0 && 2 * rest <= kCUs;
   const int nt = !halves ? (split ? full : all) : split ? 2 * rest : 0;
-  const int hw = blockIdx.x;
   if (hw >= nt) return t;
   int tile = xcd_remap(hw, nt);
   const int half = tile & 1;
@@ -284,36 +302,47 @@ __device__ __forceinline__ Tile grouped_tile(const Params& p) {
 // same number: longest contraction first (ties by group index), which keeps
 // the last round short.  Inside a group each XCD takes one contiguous range of
 // the tiles, row tiles fastest, so that it reads few of the group's gradient
-// and input columns more than once.
+// and input columns more than once.  rank: the lane's group's place.
+__device__ __forceinline__ int size_rank(const GroupScan& sc, int groups) {
+  const int lane = threadIdx.x & 63, size = sc.end - sc.start;
+  int rank = 0;
+  for (int j = 0; j < groups; ++j) rank += __builtin_amdgcn_readlane(size, j) >= size + (lane <= j);
+  return rank;
+}
 template <class C>
-__device__ __forceinline__ Tile grouped_dw_tile(const Params& p) {
+__device__ __forceinline__ Tile grouped_dw_tile(const Params& p, const GroupScan& sc, int rank, int hw) {
   const int lane = threadIdx.x & 63;
-  const GroupScan sc = scan_groups<C::BP>(p, p.Ktot, 0, 0, 0);
-  const int size = lane < p.groups ? sc.end - sc.start : -1;
-  const int per = p.ntiles / p.groups, hw = blockIdx.x, want = hw / per;
-  // The size with `want` larger ones before it, bit by bit, then which of the
-  // groups of that size.
-  int v = 0;
-  for (int bit = p.Ktot > 0 ? 31 - __builtin_clz(p.Ktot) : -1; bit >= 0; --bit) {
-    const int more = v | (1 << bit);
-    if (__builtin_popcountll(__builtin_amdgcn_ballot_w64(size >= more)) > want) v = more;
-  }
-  const int nth = want - __builtin_popcountll(__builtin_amdgcn_ballot_w64(size > v));
-  const uint64_t same = __builtin_amdgcn_ballot_w64(size == v);
-  const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
-  const int g = __builtin_ctzll(__builtin_amdgcn_ballot_w64(size == v && before == nth));
+  const int per = p.ntiles / p.groups, want = hw / per;
+  const int g = __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < p.groups && rank == want));
   const int tile = xcd_remap(hw - want * per, per), np = per / p.nq;
   return Tile{g, (tile % np) * C::BP, p.Ptot, (tile / np) * C::BQ, __builtin_amdgcn_readlane(sc.start, g),
               __builtin_amdgcn_readlane(sc.end, g), 0, 0, true};
+}
+
+// Whether a launch's workgroups take one tile after another, 256 of them side
+// by side: on 256 x 256 tiles, and where the tiles can be told from registers
+// (no more than 64 groups).  The next tile's loads then start before a tile's
+// results are stored, and groups are scanned once: grad_W of 64 experts of
+// 2048 x 7168, 1024 rows 387 -> 335 us, 32768 rows 850 -> 779; their grad_X of
+// 32768 rows 606 -> 585; dense 8192 x 4096 x 4096 forward 121.8 -> 117.4,
+// grad_X 120.2 -> 115.9, grad_W 139.9 -> 134.9.
+// A grouped grad_W's tiles differ in length, and dealt ahead they end less
+// evenly than dispatched one by one; it takes turns from eight rounds on (8
+// uneven experts, four rounds: 164 us against 154).
+template <class C, int kOp>
+__host__ __device__ __forceinline__ bool takes_turns(const Params& p) {
+  if (C::KW > 1 || C::NS > 2 || (p.offsets != nullptr && p.groups > 64)) return false;
+  return p.ntiles > (kOp == kB128Dw && p.offsets != nullptr ? 8 : 1) * kCUs;
 }
 
 template <class C, int kOp>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void b128_kernel(Params p) {
   constexpr bool kDW = kOp == kB128Dw;
   constexpr bool kPK = !kDW, kQK = kOp == kB128Fwd;
-  __shared__ __attribute__((aligned(1024))) uint8_t all_smem[C::KW * C::NS * C::STAGE];
+  constexpr bool kOwnRows = C::KW == 1 && C::NS == 2;            // results pass through LDS of their own, 2 KiB a wave
+  __shared__ __attribute__((aligned(1024))) uint8_t all_smem[C::KW * C::NS * C::STAGE + (kOwnRows ? C::NW * 2048 : 0)];
   static_assert(kMaxGroups * 4 <= C::STAGE, "group ends alias stage 0");
-  static_assert(C::BP * C::BQ * (C::KW > 1 ? 4 : 2) <= C::NS * C::STAGE, "the epilogue staging fits the stages");
+  static_assert(kOwnRows || C::BP * C::BQ * (C::KW > 1 ? 4 : 2) <= C::NS * C::STAGE, "the epilogue staging fits the stages");
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int gwave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -321,15 +350,26 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const int wp = wave / C::NWQ, wq = wave % C::NWQ;
   uint8_t* const smem = all_smem + kw * (C::NS * C::STAGE);      // the group's stages
   int32_t* const ends = reinterpret_cast<int32_t*>(all_smem);
+  const bool turns = takes_turns<C, kOp>(p);
+  GroupScan sc{};
+  int rank = 0;
+  if (p.offsets != nullptr && p.groups <= 64) {
+    sc = scan_groups<C::BP>(p, kDW ? p.Ktot : p.Ptot, 0, 0, 0);
+    if (kDW) rank = size_rank(sc, p.groups);
+  }
+  auto pick = [&](int hw) {                                      // of a dense product or at most 64 groups
+    if (p.offsets == nullptr) return dense_tile<C>(p, hw);
+    return kDW ? grouped_dw_tile<C>(p, sc, rank, hw) : grouped_tile<C>(p, sc, hw);
+  };
+  int hw = blockIdx.x;
   Tile t;
-  if (!kDW && p.offsets != nullptr) t = grouped_tile<C>(p);
-  else if (kDW && p.offsets != nullptr && p.groups <= 64) t = grouped_dw_tile<C>(p);
-  else t = select_tile<C, kDW>(p, ends);
+  if (kDW && p.offsets != nullptr && p.groups > 64) {
+    t = select_tile<C, kDW>(p, ends);
+    __syncthreads();                                             // group ends read; stage 0 reusable
+  } else {
+    t = pick(hw);
+  }
   if (!t.valid) return;
-  // The same in every lane, which the compiler cannot see: in scalar registers
-  // from here on.
-  for (int* v : {&t.g, &t.p0, &t.pend, &t.q0, &t.kbeg, &t.kend}) *v = scalar(*v);
-  __syncthreads();                                               // group ends read; stage 0 reusable
 
   B128Loader<kPK, C::BP, C::PB> lp;
   B128Loader<kQK, C::BQ, C::QB> lq;
@@ -344,11 +384,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   uint32_t sstep;                                                // bytes per stage
   const int32_t soff = sp_wave || kDW ? lane * 4 : 0;            // lane offset
   int32_t slen;                                                  // bytes that exist
-  lp.start(p.P, 0, t.p0, t.pend, t.kbeg, t.kend);
-  lq.start(p.Q, kDW ? 0 : t.g, t.q0, p.Qtot, t.kbeg, t.kend);
-  lp.advance(kw);
-  lq.advance(kw);
-  {
+  auto begin = [&] {                                             // to tile t
+    // The same in every lane, which the compiler cannot see: in scalar registers
+    // from here on.
+    for (int* v : {&t.g, &t.p0, &t.pend, &t.q0, &t.kbeg, &t.kend}) *v = scalar(*v);
+    lp.start(p.P, 0, t.p0, t.pend, t.kbeg, t.kend);
+    lq.start(p.Q, kDW ? 0 : t.g, t.q0, p.Qtot, t.kbeg, t.kend);
+    lp.advance(kw);
+    lq.advance(kw);
     const int64_t run0 = kDW ? (t.kbeg / kRun + t.g) : 0;        // first scale row of the contraction
     if (sp_wave || kDW) {
       const int first = (sp_wave ? t.p0 : t.q0) + 64 * sv, cols = (sp_wave ? p.Ptot : p.Qtot) - first;
@@ -366,7 +409,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     sstep = scalar((int)sstep) * C::KW;
     slen = scalar(slen);
     scalars_settle();
-  }
+  };
 
   // Load u of the next stage to be loaded: blocks of P, blocks of Q, scales
   // (the last one moves on to the stage after).  Stages past the end of the
@@ -408,145 +451,219 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   constexpr int kEarly = NM - kSync * C::FQ < kLoads ? NM - kSync * C::FQ : kLoads;   // loads before the stage's end
   static_assert(C::FP % kSlots == 0, "a row's slot is the same in every stage");
   f32x4 acc[C::FP][C::FQ];
-#pragma unroll
-  for (int i = 0; i < C::FP; ++i)
-#pragma unroll
-    for (int j = 0; j < C::FQ; ++j) acc[i][j] = f32x4{};
-  i32x8b q[C::FQ], pf[kSlots];
-  const int nk = (t.kend - t.kbeg + C::KW * kRun - 1) / (C::KW * kRun);   // stages of a group
-  if (nk > 0) {
+  int nk;                                                        // stages of a group of waves
+  auto first_loads = [&] {
+    nk = (t.kend - t.kbeg + C::KW * kRun - 1) / (C::KW * kRun);
+    if (nk <= 0) return;
     static_for<C::NS - 1>([&](auto si) {
       constexpr int st = decltype(si)::value;
       static_for<kLoads>([&](auto u) { issue(u, smem + st * C::STAGE); });
     });
     static_for<kEarly>([&](auto u) { issue(u, smem + (C::NS - 1) * C::STAGE); });
-    barrier_vm<(C::NS - 2) * kLoads + kEarly>();
-    static_for<kAhead>([&](auto i) { pf[decltype(i)::value] = fp.template read<decltype(i)::value>(smem + C::kP); });
-    static_for<C::FQ>([&](auto j) { q[decltype(j)::value] = fq.template read<decltype(j)::value>(smem + C::kQ); });
-  }
-  int cur = 0;
-  for (int kb = 0; kb < nk; ++kb) {
-    uint8_t* const sb = smem + cur;
-    const int next = cur + C::STAGE < C::NS * C::STAGE ? cur + C::STAGE : 0;
-    uint8_t* const nx = smem + next;
-    uint8_t* const pv = smem + (cur > 0 ? cur - C::STAGE : (C::NS - 1) * C::STAGE);   // the stage before
-    float sp[C::FP], w;
-    f32x4 sq[kDW ? C::FQ : 1];
-#pragma unroll
-    for (int i = 0; i < C::FP; ++i) sp[i] = *reinterpret_cast<const float*>(sb + psa + 64 * i);
-    if constexpr (kDW) {
-#pragma unroll
-      for (int j = 0; j < C::FQ; ++j) sq[j] = *reinterpret_cast<const f32x4*>(sb + qsa + 64 * j);
-    } else {
-      w = *reinterpret_cast<const float*>(sb + qsa);
-    }
-    f32x4 part[kRing];
-    static_for<NM + kLag>([&](auto mi) {
-      constexpr int m = decltype(mi)::value;
-      constexpr int i = m / C::FQ, j = m % C::FQ;
-      if constexpr (m == kSync * C::FQ) barrier_vm<(C::NS - 2) * kLoads>();
-      if constexpr (m < NM) {
-        if constexpr (j == 0) {
-          constexpr int n = i + kAhead;
-          if constexpr (n < C::FP) pf[n % kSlots] = fp.template read<n>(sb + C::kP);
-          else pf[n % kSlots] = fp.template read<n - C::FP>(nx + C::kP);
-        }
-        part[m % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q[j], pf[i % kSlots], f32x4{}, 0, 0, 0, 0, 0, 0);
-        if constexpr (i == C::FP - 1) q[j] = fq.template read<j>(nx + C::kQ);
-        if constexpr (m >= kSync * C::FQ && m - kSync * C::FQ < kEarly) {
-          issue(IC<m - kSync * C::FQ>{}, sb);
-        }
-        // The rest of the stage begun in the row before, all ahead of the barrier,
-        // which counts whole stages.
-        if constexpr (m < kSync * C::FQ) {
-          static_for<kLoads - kEarly>([&](auto li) {
-            constexpr int l = decltype(li)::value;
-            if constexpr ((l < kSync * C::FQ ? l : kSync * C::FQ - 1) == m) issue(IC<l + kEarly>{}, pv);
-          });
-        }
-      }
-      if constexpr (m >= kLag) {
-        constexpr int d = m - kLag, di = d / C::FQ, dj = d % C::FQ;
-        if constexpr (!kDW && dj == 0) sp[di] *= w;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float f = kDW ? sp[di] * sq[kDW ? dj : 0][r] : sp[di];
-          acc[di][dj][r] = __builtin_fmaf(part[d % kRing][r], f, acc[di][dj][r]);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    });
-    cur = next;
-  }
-  barrier_vm<0>();                                               // the last loads (zeros) have landed
-
-  uint16_t* const out = p.C + (kDW ? (int64_t)t.g * p.c_batch : 0);
-  if constexpr (C::KW > 1) {
-    // The groups' sums through LDS, added in group order: 16-byte piece c of
-    // row r of a group's tile at c ^ (r & 15).
-    float* const mine = reinterpret_cast<float*>(smem);
+  };
+  begin();
+  first_loads();
+  bool stores_behind = false;                                    // the last tile's, 2 FP a wave, issued after the first loads
+  for (;;) {
+    int cur = 0;
+    asm volatile("" : "+s"(cur));                                // (its multiples stay out of the registers of the tile loop)
+    i32x8b q[C::FQ], pf[kSlots];
 #pragma unroll
     for (int i = 0; i < C::FP; ++i)
 #pragma unroll
-      for (int j = 0; j < C::FQ; ++j) {
-        const int r = wp * C::WP + 16 * i + (lane & 15), c = (wq * C::WQ) / 4 + 4 * j + (lane >> 4);
-        *reinterpret_cast<f32x4*>(mine + r * C::BQ + 4 * (c ^ (r & 15))) = acc[i][j];
+      for (int j = 0; j < C::FQ; ++j) acc[i][j] = f32x4{};
+    if (nk > 0) {
+      constexpr int kWait = (C::NS - 2) * kLoads + kEarly;
+      if (kOwnRows && stores_behind) barrier_vm<kWait + 2 * C::FP>();
+      else barrier_vm<kWait>();
+      static_for<kAhead>([&](auto i) { pf[decltype(i)::value] = fp.template read<decltype(i)::value>(smem + cur + C::kP); });
+      static_for<C::FQ>([&](auto j) { q[decltype(j)::value] = fq.template read<decltype(j)::value>(smem + cur + C::kQ); });
+    }
+    for (int kb = 0; kb < nk; ++kb) {
+      uint8_t* const sb = smem + cur;
+      const int next = cur + C::STAGE < C::NS * C::STAGE ? cur + C::STAGE : 0;
+      uint8_t* const nx = smem + next;
+      uint8_t* const pv = smem + (cur > 0 ? cur - C::STAGE : (C::NS - 1) * C::STAGE);   // the stage before
+      float sp[C::FP], w;
+      f32x4 sq[kDW ? C::FQ : 1];
+#pragma unroll
+      for (int i = 0; i < C::FP; ++i) sp[i] = *reinterpret_cast<const float*>(sb + psa + 64 * i);
+      if constexpr (kDW) {
+#pragma unroll
+        for (int j = 0; j < C::FQ; ++j) sq[j] = *reinterpret_cast<const f32x4*>(sb + qsa + 64 * j);
+      } else {
+        w = *reinterpret_cast<const float*>(sb + qsa);
       }
-    __syncthreads();
-    for (int u = tid; u < C::BP * C::BQ / 8; u += 64 * C::NW * C::KW) {
-      const int r = u / (C::BQ / 8), c = 2 * (u % (C::BQ / 8));
-      float e[8];
+      f32x4 part[kRing], fac{};
+      static_for<NM + kLag>([&](auto mi) {
+        constexpr int m = decltype(mi)::value;
+        constexpr int i = m / C::FQ, j = m % C::FQ;
+        if constexpr (m == kSync * C::FQ) barrier_vm<(C::NS - 2) * kLoads>();
+        if constexpr (m < NM) {
+          if constexpr (j == 0) {
+            constexpr int n = i + kAhead;
+            if constexpr (n < C::FP) pf[n % kSlots] = fp.template read<n>(sb + C::kP);
+            else pf[n % kSlots] = fp.template read<n - C::FP>(nx + C::kP);
+          }
+          part[m % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q[j], pf[i % kSlots], f32x4{}, 0, 0, 0, 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (i == C::FP - 1) q[j] = fq.template read<j>(nx + C::kQ);
+          if constexpr (m >= kSync * C::FQ && m - kSync * C::FQ < kEarly) {
+            issue(IC<m - kSync * C::FQ>{}, sb);
+          }
+          // The rest of the stage begun in the row before, all ahead of the barrier,
+          // which counts whole stages.
+          if constexpr (m < kSync * C::FQ) {
+            static_for<kLoads - kEarly>([&](auto li) {
+              constexpr int l = decltype(li)::value;
+              if constexpr ((l < kSync * C::FQ ? l : kSync * C::FQ - 1) == m) issue(IC<l + kEarly>{}, pv);
+            });
+          }
+        }
+        if constexpr (m >= kLag) {
+          constexpr int d = m - kLag, di = d / C::FQ, dj = d % C::FQ;
+          if constexpr (!kDW && dj == 0) sp[di] *= w;
 #pragma unroll
-      for (int g = 0; g < C::KW; ++g) {
-        const float* src = reinterpret_cast<const float*>(all_smem + g * (C::NS * C::STAGE)) + r * C::BQ;
+          for (int r = 0; r < 4; ++r) {
+            const float f = kDW ? fac[r] : sp[di];
+            acc[di][dj][r] = __builtin_fmaf(part[d % kRing][r], f, acc[di][dj][r]);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // The next product's factors, one step ahead of their use (right before it:
+        // 8192 x 4096 x 8192 272 us, 267).
+        if constexpr (kDW && m + 1 >= kLag && m + 1 - kLag < NM) {
+          constexpr int d = m + 1 - kLag;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const f32x4 v = *reinterpret_cast<const f32x4*>(src + 4 * ((c + h) ^ (r & 15)));
+          for (int r = 0; r < 4; ++r) fac[r] = sp[d / C::FQ] * sq[kDW ? d % C::FQ : 0][r];
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      });
+      cur = next;
+    }
+    barrier_vm<0>();                                             // the last loads (zeros) have landed
+
+    uint16_t* const out = p.C + (kDW ? (int64_t)t.g * p.c_batch : 0);
+    if constexpr (C::KW > 1) {
+      // The groups' sums through LDS, added in group order: 16-byte piece c of
+      // row r of a group's tile at c ^ (r & 15).
+      float* const mine = reinterpret_cast<float*>(smem);
 #pragma unroll
-          for (int d = 0; d < 4; ++d) e[4 * h + d] = g == 0 ? v[d] : e[4 * h + d] + v[d];
+      for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FQ; ++j) {
+          const int r = wp * C::WP + 16 * i + (lane & 15), c = (wq * C::WQ) / 4 + 4 * j + (lane >> 4);
+          *reinterpret_cast<f32x4*>(mine + r * C::BQ + 4 * (c ^ (r & 15))) = acc[i][j];
+        }
+      __syncthreads();
+      for (int u = tid; u < C::BP * C::BQ / 8; u += 64 * C::NW * C::KW) {
+        const int r = u / (C::BQ / 8), c = 2 * (u % (C::BQ / 8));
+        float e[8];
+#pragma unroll
+        for (int g = 0; g < C::KW; ++g) {
+          const float* src = reinterpret_cast<const float*>(all_smem + g * (C::NS * C::STAGE)) + r * C::BQ;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(src + 4 * ((c + h) ^ (r & 15)));
+#pragma unroll
+            for (int d = 0; d < 4; ++d) e[4 * h + d] = g == 0 ? v[d] : e[4 * h + d] + v[d];
+          }
+        }
+        const int row = t.p0 + r, col = t.q0 + 4 * c;
+        if (row < t.pend && col < p.Qtot)
+          *reinterpret_cast<u32x4*>(out + (int64_t)row * p.ldc + col) =
+              u32x4{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])};
+      }
+      return;
+    }
+
+    if constexpr (kOwnRows) {
+      // The next tile's first loads go ahead of this one's stores.
+      const Tile done = t;
+      bool more = false;
+      if (turns) {
+        hw += gridDim.x;
+        more = hw < p.ntiles;
+        if (more) {
+          t = pick(hw);
+          more = t.valid;
+        }
+        if (more) {
+          begin();
+          first_loads();
         }
       }
-      const int row = t.p0 + r, col = t.q0 + 4 * c;
-      if (row < t.pend && col < p.Qtot)
-        *reinterpret_cast<u32x4*>(out + (int64_t)row * p.ldc + col) =
-            u32x4{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])};
+      // bf16 results, 16 rows at a time, through the wave's own 2 KiB of LDS, so
+      // that a store of eight lanes writes a row's 128 bytes: 8-byte slot s of row
+      // r at s ^ 2 (r & 7).  No barrier, and the stages stay free for the loads.
+      // (The whole tile through the stages, rows of 512 bytes: grad_W of 8192 x 4096
+      // x 128 24.5 us, 20.1 this way.)
+      uint8_t* const mine = all_smem + C::NS * C::STAGE + wave * 2048;
+      int el = lane;
+      asm volatile("" : "+v"(el));                               // (keeps the addresses below out of the main loop's registers)
+      const int c8 = el & 7, r8 = el >> 3, r16 = el & 15;
+      const int col = done.q0 + wq * C::WQ + 8 * c8, row = done.p0 + wp * C::WP + r8;
+      const bool whole = done.p0 + C::BP <= done.pend && done.q0 + C::BQ <= p.Qtot;
+      uint8_t* to = reinterpret_cast<uint8_t*>(out + (int64_t)(done.p0 + wp * C::WP) * p.ldc + done.q0 + wq * C::WQ);
+      const uint32_t lane_to = 2u * ((uint32_t)r8 * p.ldc + 8 * c8);
+      auto store = [&](auto all) {
+#pragma unroll
+        for (int i = 0; i < C::FP; ++i) {
+#pragma unroll
+          for (int j = 0; j < C::FQ; ++j)
+            *reinterpret_cast<u32x2*>(mine + r16 * 128 + 8 * ((4 * j + (el >> 4)) ^ (2 * (r16 & 7)))) =
+                u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(mine + (8 * h + r8) * 128 + 16 * (c8 ^ r8));
+            if (decltype(all)::value || (row + 16 * i + 8 * h < done.pend && col < p.Qtot)) {
+              u32x4* const dst = reinterpret_cast<u32x4*>(to + lane_to);
+              // grad_W is often larger than the caches: streamed (64 experts of 2048 x
+              // 7168, 32768 rows: 1008 us without, 911 us, both by whole rows).
+              if constexpr (kDW) __builtin_nontemporal_store(v, dst);
+              else *dst = v;
+            }
+            to += (int64_t)16 * p.ldc;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      if (whole) store(IC<1>{});
+      else store(IC<0>{});
+      if (!more) return;
+      stores_behind = whole;
+      continue;
+    }
+
+    // bf16 results through LDS, so that a store writes whole rows of the tile:
+    // 8-byte slot s of row r at s ^ 2 (r & 15).
+    constexpr int ROWB = C::BQ * 2, LPR = ROWB / 16, RPI = 64 / LPR;   // lanes per row, rows per store
+    const int c16 = lane % LPR, col = t.q0 + 8 * c16;
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i) {
+      const int r = wp * C::WP + 16 * i + (lane & 15);
+#pragma unroll
+      for (int j = 0; j < C::FQ; ++j) {
+        const int slot = wq * (C::WQ / 4) + 4 * j + (lane >> 4);
+        *reinterpret_cast<u32x2*>(smem + r * ROWB + 8 * (slot ^ (2 * (r & 15)))) =
+            u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+      }
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int it = 0; it < C::BP / (RPI * C::NW); ++it) {
+      const int r = (it * C::NW + wave) * RPI + lane / LPR, row = t.p0 + r;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(smem + r * ROWB + 16 * (c16 ^ (r & 15)));
+      if (row < t.pend && col < p.Qtot) *reinterpret_cast<u32x4*>(out + (int64_t)row * p.ldc + col) = v;
     }
     return;
-  }
-
-  // bf16 results through LDS, so that a store writes whole rows of the tile:
-  // 8-byte slot s of row r at s ^ 2 (r & 15).
-  constexpr int ROWB = C::BQ * 2, LPR = ROWB / 16, RPI = 64 / LPR;   // lanes per row, rows per store
-  const int c16 = lane % LPR, col = t.q0 + 8 * c16;
-#pragma unroll
-  for (int i = 0; i < C::FP; ++i) {
-    const int r = wp * C::WP + 16 * i + (lane & 15);
-#pragma unroll
-    for (int j = 0; j < C::FQ; ++j) {
-      const int slot = wq * (C::WQ / 4) + 4 * j + (lane >> 4);
-      *reinterpret_cast<u32x2*>(smem + r * ROWB + 8 * (slot ^ (2 * (r & 15)))) =
-          u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
-    }
-  }
-  __syncthreads();
-#pragma unroll 4
-  for (int it = 0; it < C::BP / (RPI * C::NW); ++it) {
-    const int r = (it * C::NW + wave) * RPI + lane / LPR, row = t.p0 + r;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(smem + r * ROWB + 16 * (c16 ^ (r & 15)));
-    if (row < t.pend && col < p.Qtot) {
-      u32x4* const dst = reinterpret_cast<u32x4*>(out + (int64_t)row * p.ldc + col);
-      // grad_W is often larger than the caches: streamed (64 experts of 2048 x
-      // 7168, 32768 rows: 1008 us without, 911 us).
-      if constexpr (kDW) __builtin_nontemporal_store(v, dst);
-      else *dst = v;
-    }
   }
 }
 
 template <class C, int kOp>
 inline hipError_t run_b128(const Params& prm, hipStream_t s) {
   if (prm.ntiles <= 0) return hipSuccess;
-  b128_kernel<C, kOp><<<dim3(prm.ntiles), dim3(64 * C::NW * C::KW), 0, s>>>(prm);
+  b128_kernel<C, kOp><<<dim3(takes_turns<C, kOp>(prm) ? kCUs : prm.ntiles), dim3(64 * C::NW * C::KW), 0, s>>>(prm);
   return hipGetLastError();
 }
 
