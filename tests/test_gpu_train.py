@@ -170,10 +170,11 @@ def decoded_rows(q, ends=None):
     return O.values_rows(q.codes.cpu().numpy()[0], q.scales.cpu().numpy()[0], ends)
 
 
-# one row to several tiles, sizes off every tile, one long contraction, 256 tiles of 256 x 256
+# one row to several tiles, sizes off every tile, one long contraction, 256 tiles of 256 x 256, then more of them (ragged
+# at both edges) for each product in turn
 DENSE = [(1, 16, 16), (1, 512, 2048), (2, 144, 128), (5, 272, 1040), (16, 4096, 512), (17, 400, 400), (33, 128, 144),
          (64, 272, 272), (65, 528, 656), (128, 128, 128), (129, 272, 400), (300, 1040, 144), (700, 512, 4112),
-         (4096, 4096, 144)]
+         (4096, 4096, 144), (4112, 4368, 272), (4112, 272, 4368), (272, 4112, 4368)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -192,7 +193,8 @@ def test_dense_products(lp, M, N, K):
 
 
 GROUPED = [([5], 16, 16), ([0, 0, 3], 144, 128), ([1] * 9, 272, 272), ([0, 1, 127, 128, 129, 0, 300, 5], 272, 400),
-           ([2, 0, 1, 4] * 80, 128, 144), ([900, 30, 0, 600, 257], 1040, 272), ([2500, 1500, 0, 97], 4096, 144)]
+           ([2, 0, 1, 4] * 80, 128, 144), ([900, 30, 0, 600, 257], 1040, 272), ([2500, 1500, 0, 97], 4096, 144),
+           ([2500, 1500, 0, 97], 144, 4096)]
 
 
 @pytest.mark.parametrize("sizes,N,K", GROUPED)
@@ -230,6 +232,25 @@ def test_grouped_products(lp, sizes, N, K, tail):
         assert_product(y2[a:b], xv[a:b], wv[k].T, f"y of group {k} from bf16")
         assert_product(dx[a:b], gv[a:b], wv[k], f"dX of group {k}")
         assert_product(dw[k], grv[a:b].T, xrv[a:b], f"dW of group {k}")
+
+
+def test_grouped_grad_w_of_many_tiles(lp):
+    """More tiles than the workgroups side by side take in eight turns, sizes of empty, short and long groups mixed:
+    bit for bit what the groups give in calls of a few groups (checked above)."""
+    rng = np.random.default_rng(21)
+    sizes = [int(v) for v in rng.choice([0, 1, 40, 128, 129, 300], 40)]
+    M, N, K, ends = sum(sizes), 1800 // 16 * 16, 1808, ends_of(sizes)
+    xb, gb = bits(rng, (M, K)), bits(rng, (M, N), 1e-3)
+
+    def grad_w(a, b, off):
+        (_, gr), (_, xr) = lp.lp_r128_quant_dual(bf16_dev(gb[a:b]), off), lp.lp_r128_quant_dual(bf16_dev(xb[a:b]), off)
+        out = torch.full((off.numel(), N, K), 3.0, dtype=torch.bfloat16, device="cuda")
+        return lp.lp_grouped_bwd(gr, xr, None, off, need_dx=False, grad_w=out)[1]
+    whole = grad_w(0, M, dev(ends))
+    for k in range(0, 40, 4):
+        a = int(ends[k - 1]) if k else 0
+        part = grad_w(a, int(ends[k + 3]), dev((ends[k:k + 4] - a).astype(np.int32)))
+        assert torch.equal(whole[k:k + 4], part), k
 
 
 @pytest.mark.parametrize("M", [1, 40, 200])
