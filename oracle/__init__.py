@@ -26,8 +26,10 @@ Pins (tests/test_oracle_*.py, all CPU):
   float8_e5m2, quantization against torch's casts below saturation and a
   brute-force nearest search, the scale formula and ring update of the
   AstrAI page, triple-loop GEMMs with the scales applied to the sums.
+* training (train.py): hand-made runs and blocks of the quantization rule,
+  run indices of groups written out, the AdamW formula in scalars.
 
 Parity unpinned by the source documents: the E2M1 nibble order and the NVFP4
 tensor-scale reading (see formats.py).
 """
-from . import formats, gemm, pertensor  # noqa: F401
+from . import formats, gemm, pertensor, train  # noqa: F401

@@ -1,6 +1,9 @@
 """FP8 with fp32 scales per 128 elements (lp_train.h) against the fp64 oracle
 (GPU): quantizers and decode bit for bit, products within a bound derived from
 the arithmetic."""
+import os
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -582,3 +585,27 @@ def test_training_step_in_a_graph(lp, sizes):
         torch.cuda.synchronize()
         for i, (a, b) in enumerate(zip(want[k], got)):
             assert torch.equal(a, b), (k, i)
+
+
+# ---------------------------------------------------------------- together
+
+def test_example_trains_and_serves(lp):
+    """The example's training lowers the loss far below the targets' variance, and a token served alone gives the
+    batch's row: both quantize x to the same codes and differ in summation order only (fp32), then by one rounding of
+    the hidden values (2^-8) through the second layer."""
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import train_experts as T
+    up, down, x, offsets, losses = T.train(steps=60)
+    assert losses[-1] < 0.3 * losses[0] and all(np.isfinite(losses))
+    h = torch.relu(up.forward(x, offsets))
+    y = down.forward(h, offsets).float()
+    ends = [0] + offsets.tolist()
+    for expert in range(len(ends) - 1):
+        if ends[expert] == ends[expert + 1]:
+            continue
+        row = ends[expert + 1] - 1
+        alone = T.serve(up, down, x[row:row + 1], expert).float()[0]
+        w = torch.from_numpy(O.values_blocks(down.weight.codes[expert].cpu().numpy(), down.weight.scales[expert].cpu().numpy()))
+        mag = (h[row].double().cpu().abs() @ w.abs().T).cuda()
+        # a hidden value one bf16 step off may take the E4M3 code next to it: 2^-3 of that value, for the few that do
+        assert ((alone - y[row]).abs() <= 2.0 ** -5 * mag + 1e-6).all(), expert
