@@ -310,7 +310,7 @@ hipError_t launch_gemm(const GemmCall& call, hipStream_t stream) {
     if (call.dw) return b128_dw(prm, tile, stream);
     const bool split = tile == 256 && b128_split(prm);
     const hipError_t e = b128_dx(prm, tile, stream);
-    return e != hipSuccess || !split ? e : b128_dx_tail(tail_params(prm), stream);
+    return e != hipSuccess || !split ? e : b128_dx_tail(prm, stream);
   }
   if (native_mx(call) || native_pt(call)) {
     const Params prm = native_params(call);
@@ -372,7 +372,7 @@ hipError_t launch_fwd(const lp_qtensor& x, const lp_qtensor& w, const int32_t* o
     b128_tiles(prm, tile, false);
     const bool split = tile == 256 && b128_split(prm);
     const hipError_t e = b128_fwd(prm, tile, stream);
-    return e != hipSuccess || !split ? e : b128_fwd_tail(tail_params(prm), stream);
+    return e != hipSuccess || !split ? e : b128_fwd_tail(prm, stream);
   }
   // MX operands run on the block-scaled MFMA (256 x 256 tiles); the others
   // through bf16 tiles, 256 x 256 unless both are bf16 (256 x 128: three

@@ -244,38 +244,42 @@ __device__ __forceinline__ GroupScan scan_groups(const Params& p, int M, int bas
   return GroupScan{s, e, seen0 + sum - n, __builtin_amdgcn_readlane(e, 63), seen0 + __builtin_amdgcn_readlane(sum, 63)};
 }
 
-// Params::tail: 0, every tile; 1, the whole rounds of kCUs tiles when the
-// last, partial one has at most kCUs / 2 (every tile otherwise); 2 (256 x 128
-// tiles), what 1 leaves, each 256 x 256 tile as its two halves.
+// Params::tail (host's choice to split by round): the whole rounds of kCUs
+// tiles when the last, partial one has at most kCUs / 2, every tile otherwise;
+// what that leaves is taken by a second launch in kParts parts of each
+// 256 x 256 tile, 256 x 128 or 128 x 128.
 //
 // sc0: the scan of at most 64 groups, unless there are more.
-template <class C>
+__device__ __forceinline__ bool rounds_split(const Params& p, int full, int rest) {
+  return p.tail != 0 && full > 0 && rest > 0 && 2 * rest <= kCUs;
+}
+template <class C, int kParts>
 __device__ __forceinline__ Tile grouped_tile(const Params& p, const GroupScan& sc0, int hw) {
+  constexpr int kRows = kParts > 1 ? 256 : C::BP;                // of a whole tile
   Tile t{0, 0, 0, 0, 0, p.Ktot, 0, 0, false};
   GroupScan sc = sc0;
   int end0 = 0, rows = sc0.last_seen;
   if (p.groups > 64) {
     rows = 0;
     for (int base = 0; base < p.groups; base += 64) {
-      sc = scan_groups<C::BP>(p, p.Ptot, base, end0, rows);
+      sc = scan_groups<kRows>(p, p.Ptot, base, end0, rows);
       end0 = sc.last_end;
       rows = sc.last_seen;
     }
   }
-  const bool halves = p.tail == 2;
-  const int nq = halves ? (p.Qtot + 255) / 256 : p.nq;
+  const int nq = kParts > 1 ? (p.Qtot + 255) / 256 : p.nq;
   const int all = rows * nq, full = all / kCUs * kCUs, rest = all - full;
-  const bool split = p.tail != 0 && full > 0 && rest > 0 && 2 * rest <= kCUs;
-  const int nt = !halves ? (split ? full : all) : split ? 2 * rest : 0;
+  const bool split = rounds_split(p, full, rest);
+  const int nt = kParts > 1 ? (split ? kParts * rest : 0) : split ? full : all;
   if (hw >= nt) return t;
   int tile = xcd_remap(hw, nt);
-  const int half = tile & 1;
-  if (halves) tile = full + tile / 2;
+  const int part = tile % kParts;
+  if (kParts > 1) tile = full + tile / kParts;
   const int pidx = tile / nq;
   if (p.groups > 64) {
     end0 = rows = 0;
     for (int base = 0; base < p.groups; base += 64) {
-      sc = scan_groups<C::BP>(p, p.Ptot, base, end0, rows);
+      sc = scan_groups<kRows>(p, p.Ptot, base, end0, rows);
       if (pidx < sc.last_seen) {
         t.g = base;
         break;
@@ -291,10 +295,11 @@ __device__ __forceinline__ Tile grouped_tile(const Params& p, const GroupScan& s
   const int start = __builtin_amdgcn_readlane(sc.start, l), seen = __builtin_amdgcn_readlane(sc.seen, l);
   t.pend = __builtin_amdgcn_readlane(sc.end, l);
   int2 pq = make_int2(pidx - seen, tile - pidx * nq);
-  if (p.gm > 1) pq = grouped_order(tile - seen * nq, (t.pend - start + C::BP - 1) / C::BP, nq, p.gm);
-  t.p0 = start + pq.x * C::BP;
-  t.q0 = halves ? pq.y * 256 + half * C::BQ : pq.y * C::BQ;
-  t.valid = t.q0 < p.Qtot;
+  if (p.gm > 1) pq = grouped_order(tile - seen * nq, (t.pend - start + kRows - 1) / kRows, nq, p.gm);
+  constexpr int kPartCols = kParts > 1 ? 256 / C::BQ : 1;
+  t.p0 = start + pq.x * kRows + part / kPartCols * C::BP;
+  t.q0 = (pq.y * kPartCols + part % kPartCols) * C::BQ;
+  t.valid = t.q0 < p.Qtot && t.p0 < t.pend;
   return t;
 }
 
@@ -335,12 +340,16 @@ __host__ __device__ __forceinline__ bool takes_turns(const Params& p) {
   return p.ntiles > (kOp == kB128Dw && p.offsets != nullptr ? 8 : 1) * kCUs;
 }
 
-template <class C, int kOp>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void b128_kernel(Params p) {
+template <class C>
+inline constexpr bool kOwnRowsOf = C::KW == 1 && C::NS == 2;     // results pass through LDS of their own, 2 KiB a wave
+template <class C>
+inline constexpr int kLdsOf = C::KW * C::NS * C::STAGE + (kOwnRowsOf<C> ? C::NW * 2048 : 0);
+
+template <class C, int kOp, int kParts>
+__device__ __forceinline__ void b128_tiles_of(const Params& p, uint8_t* all_smem) {
   constexpr bool kDW = kOp == kB128Dw;
   constexpr bool kPK = !kDW, kQK = kOp == kB128Fwd;
-  constexpr bool kOwnRows = C::KW == 1 && C::NS == 2;            // results pass through LDS of their own, 2 KiB a wave
-  __shared__ __attribute__((aligned(1024))) uint8_t all_smem[C::KW * C::NS * C::STAGE + (kOwnRows ? C::NW * 2048 : 0)];
+  constexpr bool kOwnRows = kOwnRowsOf<C>;
   static_assert(kMaxGroups * 4 <= C::STAGE, "group ends alias stage 0");
   static_assert(kOwnRows || C::BP * C::BQ * (C::KW > 1 ? 4 : 2) <= C::NS * C::STAGE, "the epilogue staging fits the stages");
 
@@ -354,12 +363,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   GroupScan sc{};
   int rank = 0;
   if (p.offsets != nullptr && p.groups <= 64) {
-    sc = scan_groups<C::BP>(p, kDW ? p.Ktot : p.Ptot, 0, 0, 0);
+    sc = scan_groups<kParts == 1 ? C::BP : 256>(p, kDW ? p.Ktot : p.Ptot, 0, 0, 0);
     if (kDW) rank = size_rank(sc, p.groups);
   }
   auto pick = [&](int hw) {                                      // of a dense product or at most 64 groups
     if (p.offsets == nullptr) return dense_tile<C>(p, hw);
-    return kDW ? grouped_dw_tile<C>(p, sc, rank, hw) : grouped_tile<C>(p, sc, hw);
+    return kDW ? grouped_dw_tile<C>(p, sc, rank, hw) : grouped_tile<C, kParts>(p, sc, hw);
   };
   int hw = blockIdx.x;
   Tile t;
@@ -661,9 +670,37 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 template <class C, int kOp>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void b128_kernel(Params p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kLdsOf<C>];
+  b128_tiles_of<C, kOp, 1>(p, smem);
+}
+
+// The last, partial round of a grouped forward or grad_X: quarters when they
+// fit one round and the contraction has 32 stages, halves otherwise.  (Forward
+// of 2048 x 4096 in 8 groups, two rounds and 48 tiles 150 us with halves, 145
+// with quarters; 56 stages, 64 tiles left, 493 -> 485; grad_X of the former, 16
+// stages and 64 tiles left, 155 -> 158.)
+template <int kOp>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void b128_tail_kernel(Params p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kLdsOf<B128> > kLdsOf<B256N> ? kLdsOf<B128> : kLdsOf<B256N>];
+  GroupScan sc{};
+  for (int base = 0; base < p.groups; base += 64) sc = scan_groups<256>(p, p.Ptot, base, sc.last_end, sc.last_seen);
+  const int all = sc.last_seen * ((p.Qtot + 255) / 256), full = all / kCUs * kCUs, rest = all - full;
+  if (!rounds_split(p, full, rest)) return;
+  if (4 * rest <= kCUs && p.Ktot >= 32 * kRun) b128_tiles_of<B128, kOp, 4>(p, smem);
+  else b128_tiles_of<B256N, kOp, 2>(p, smem);
+}
+
+template <class C, int kOp>
 inline hipError_t run_b128(const Params& prm, hipStream_t s) {
   if (prm.ntiles <= 0) return hipSuccess;
   b128_kernel<C, kOp><<<dim3(takes_turns<C, kOp>(prm) ? kCUs : prm.ntiles), dim3(64 * C::NW * C::KW), 0, s>>>(prm);
+  return hipGetLastError();
+}
+
+template <int kOp>
+inline hipError_t run_b128_tail(const Params& prm, hipStream_t s) {
+  b128_tail_kernel<kOp><<<dim3(kCUs), dim3(512), 0, s>>>(prm);
   return hipGetLastError();
 }
 

@@ -1014,7 +1014,7 @@ hipError_t b128_fwd_skinny(const Params& prm, hipStream_t s);
 hipError_t b128_fwd_fused(const Params& prm, const void* x, hipStream_t s);
 hipError_t b128_dx(const Params& prm, int tile, hipStream_t s);
 hipError_t b128_dw(const Params& prm, int tile, hipStream_t s);
-// The last dispatch round of a grouped call on 256 x 128 tiles (Params::tail).
+// The last dispatch round of a grouped call in parts of tiles (Params::tail).
 hipError_t b128_fwd_tail(const Params& prm, hipStream_t s);
 hipError_t b128_dx_tail(const Params& prm, hipStream_t s);
 

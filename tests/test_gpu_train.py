@@ -197,7 +197,9 @@ def test_dense_products(lp, M, N, K):
 
 GROUPED = [([5], 16, 16), ([0, 0, 3], 144, 128), ([1] * 9, 272, 272), ([0, 1, 127, 128, 129, 0, 300, 5], 272, 400),
            ([2, 0, 1, 4] * 80, 128, 144), ([900, 30, 0, 600, 257], 1040, 272), ([2500, 1500, 0, 97], 4096, 144),
-           ([2500, 1500, 0, 97], 144, 4096)]
+           ([2500, 1500, 0, 97], 144, 4096),
+           # tiles left after one round of 256, forward: 64 and 32 over 33 stages, 50 over 17; grad_X: 84 over 31, 50 over 32
+           ([2500, 0, 2300, 130], 3856, 4112), ([2500, 1700, 0, 97], 4096, 4112), ([2500, 1700, 0, 97], 4112, 2064)]
 
 
 @pytest.mark.parametrize("sizes,N,K", GROUPED)
@@ -254,6 +256,23 @@ def test_grouped_grad_w_of_many_tiles(lp):
         a = int(ends[k - 1]) if k else 0
         part = grad_w(a, int(ends[k + 3]), dev((ends[k:k + 4] - a).astype(np.int32)))
         assert torch.equal(whole[k:k + 4], part), k
+
+
+def test_grouped_forward_of_many_groups_split_by_round(lp):
+    """70 groups (more than one wave's scan holds), 94 tiles left after one round."""
+    rng = np.random.default_rng(31)
+    torch.manual_seed(31)
+    G, N, K = 70, 1040, 2064
+    sizes = [int(v) for v in rng.choice([1, 30, 200], G)]
+    ends = ends_of(sizes)
+    w = lp.lp_b128_quant((torch.randn(G, N, K, device="cuda") * 0.02).bfloat16())
+    x = bf16_dev(bits(rng, (sum(sizes), K)))
+    xq = lp.lp_r128_quant(x, -1)
+    y, xv = lp.lp_grouped_fwd(xq, w, dev(ends)), decoded(xq)
+    for g in (0, 1, 50, 51, 52, 63, 64, 69):             # groups 51 and 52 meet the boundary of the round
+        a, b = int(ends[g]) - sizes[g], int(ends[g])
+        wv = O.values_blocks(w.codes[g].cpu().numpy(), w.scales[g].cpu().numpy())
+        assert_product(y[a:b], xv[a:b], wv.T, f"group {g}")
 
 
 @pytest.mark.parametrize("M", [1, 40, 200])
