@@ -505,7 +505,8 @@ def lp_r128_quant_dual(src: torch.Tensor, offsets: Optional[torch.Tensor] = None
     the last offset are left unwritten in both."""
     b, r, c = shape = _shape3(src)
     dev = src.device
-    codes_c, codes_r = (torch.empty(shape, dtype=torch.uint8, device=dev) for _ in range(2))
+    codes_c = torch.empty(shape, dtype=torch.uint8, device=dev)
+    codes_r = torch.empty_like(codes_c)
     scales_c = torch.empty((b, -(-c // 128), r), dtype=torch.float32, device=dev)
     scales_r = torch.empty((b, _runs(r, offsets), c), dtype=torch.float32, device=dev)
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
@@ -537,8 +538,9 @@ def _fwd_dyn(x: torch.Tensor, w: QTensor, offsets: Optional[torch.Tensor], y: Op
         raise ValueError(f"x has {K} columns, the weight {w.cols}")
     _device(x, "x", 2 * M * K, torch.bfloat16)
     if y is None:
-        y = torch.empty((M, w.rows), dtype=torch.bfloat16, device=x.device)
-    _device(y, "y", 2 * M * w.rows)
+        y = x.new_empty((M, w.rows), dtype=torch.bfloat16)
+    else:
+        _device(y, "y", 2 * M * w.rows)
     nb = -(-K // 128)
     if offsets is None and M <= 4 and M * nb <= 512:         # quantized inside the product
         codes = scales = None

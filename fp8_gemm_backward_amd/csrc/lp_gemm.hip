@@ -353,21 +353,13 @@ Params fwd_params(const lp_qtensor& x, const lp_qtensor& w, const int32_t* offse
   return prm;
 }
 
-// Whether the forward streams the weight past a few rows: up to 16 rows, or
-// 8 in a group's mean.  (16 x 4096 x 4096: 7.5 us against 8.8 us on 64 x 64
-// tiles, 32 rows 10.2 against 8.7; 64 experts of 2048 x 7168: 512 tokens 196 to
-// 235 us against 249 to 259 on 128 x 128 tiles, 1024 tokens 330 against 262.)
-bool skinny(const Params& prm) {
-  return prm.offsets ? prm.Ptot <= 8 * (int64_t)prm.groups : prm.Ptot <= 16;
-}
-
 }  // namespace
 
 hipError_t launch_fwd(const lp_qtensor& x, const lp_qtensor& w, const int32_t* offsets, int32_t groups, void* y,
                       hipStream_t stream) {
   Params prm = fwd_params(x, w, offsets, groups, y);
   if (x.fmt == LP_FP8_R128) {
-    if (skinny(prm)) return b128_fwd_skinny(prm, stream);
+    if (b128_skinny_fits(prm)) return b128_fwd_skinny(prm, stream);
     const int tile = b128_tile(prm, B128Op::kFwd);
     b128_tiles(prm, tile, false);
     const bool split = tile == 256 && b128_split(prm);

@@ -1010,6 +1010,7 @@ hipError_t b128_fwd(const Params& prm, int tile, hipStream_t s);
 // The forward of few rows; and from a bf16 x of at most kFuseRows rows that
 // the kernel quantizes itself, when fwd_dyn_fuses says so.
 constexpr int kFuseRows = 4;
+bool b128_skinny_fits(const Params& prm);
 hipError_t b128_fwd_skinny(const Params& prm, hipStream_t s);
 hipError_t b128_fwd_fused(const Params& prm, const void* x, hipStream_t s);
 hipError_t b128_dx(const Params& prm, int tile, hipStream_t s);

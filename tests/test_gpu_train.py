@@ -175,7 +175,8 @@ def decoded_rows(q, ends=None):
 
 # one row to several tiles, sizes off every tile, one long contraction, 256 tiles of 256 x 256, then more of them (ragged
 # at both edges) for each product in turn
-DENSE = [(1, 16, 16), (1, 512, 2048), (2, 144, 128), (5, 272, 1040), (16, 4096, 512), (17, 400, 400), (33, 128, 144),
+DENSE = [(1, 16, 16), (3, 4112, 272), (1, 8208, 272), (2, 16400, 144), (14, 8208, 528), (9, 16400, 272), (24, 4096, 400),
+         (31, 2064, 2064), (48, 1040, 528), (64, 2048, 144), (61, 784, 4112), (1, 512, 2048), (2, 144, 128), (5, 272, 1040), (16, 4096, 512), (17, 400, 400), (33, 128, 144),
          (64, 272, 272), (65, 528, 656), (128, 128, 128), (129, 272, 400), (300, 1040, 144), (700, 512, 4112),
          (4096, 4096, 144), (4112, 4368, 272), (4112, 272, 4368), (272, 4112, 4368)]
 
