@@ -7,8 +7,9 @@
 //
 // Every operation is an fp32 operation of its own, in this order, with no
 // multiply-add contraction, so that the result does not depend on how the
-// compiler fuses them.  The factors that depend on the step only are computed
-// in double on the host.
+// compiler fuses them.  The factors that depend on the step and the tensor only
+// are computed in double, then rounded to fp32.  The moments and masters stay
+// fp32 inside; 8-bit moments and bf16 copies are rounded once, at the end.
 //
 // 8-bit moments: m, and sqrt(v) in place of v (its range in powers of two is
 // half of v's), are quantized per run of 128 by the rule of lp_r128.hpp;
@@ -20,7 +21,10 @@
 // whatever the number of tensors, with one lookup per workgroup.  A lane holds
 // four consecutive elements (16 bytes of fp32, so every access of a wave is
 // one contiguous KiB), kUnits times, with all loads issued first; 32 lanes
-// hold a run.
+// hold a run.  96 small tensors (1.6 M elements) 10.5 us; with the tensors in the
+// kernel arguments, two launches and a search per workgroup, 18.7.  67 M
+// parameters with bf16 gradients and copies: 354 us with fp32 moments (1.88 GB,
+// 5.3 TB/s), 206 us with 8-bit ones (1.08 GB, 5.3 TB/s): the rate of memory.
 #include "lp_internal.hpp"
 #include "lp_r128.hpp"
 

@@ -265,8 +265,9 @@ void b128_tiles(Params& prm, int b, bool dw) {
 }
 
 // Grouped grad_X and forward split by dispatch round, as tile_split does: the
-// whole rounds of 256 x 256 tiles, then a short last round as 256 x 128 tiles in
-// a second launch (grouped_tile has the rule).  For contractions of at least
+// whole rounds of 256 x 256 tiles, then a short last round in parts of tiles by
+// a second launch (grouped_tile and b128_tail_kernel have the rules; figures with
+// halves).  For contractions of at least
 // 16 stages over at most five rounds: 16384 rows over 8 uneven experts, forward
 // 2048 x 4096 159 -> 149 us, grad_X of 4096 x 2048 161 -> 150; shorter ones and
 // more rounds only pay for the second launch (grad_X of 1536 x 6144, 10000 rows:
@@ -279,9 +280,11 @@ bool b128_split(Params& prm) {
 
 // The tile size of a product with fp32 scales per 128: the least estimated
 // time of one contraction stage over all dispatch rounds, in units of 10 ns
-// (measured per stage and round: 256 x 256 tiles 1.35 us, 128 x 128 0.50 us for
-// up to 128 tiles and 0.62 us above, 64 x 64 0.20 and 0.28 us; a second round
-// of 64 x 64 tiles lost to 128 x 128 in every case).  Grouped grad_X and
+// (measured per stage and round on a GPU that is not yet hot: 256 x 256 tiles
+// 1.35 us, 128 x 128 0.50 us for up to 128 tiles and 0.62 us above, 64 x 64 0.20
+// and 0.28 us; a second round of 64 x 64 tiles lost to 128 x 128 in every
+// case).  Over 24 dense and grouped products the choice was within 6% of the best
+// of the three, but for two (7% and 13%).  Grouped grad_X and
 // grad_W keep 256 x 256 unless 128 x 128 fits one round: their narrow tiles
 // read or write 128-byte pieces of long rows (64 experts of 2048 x 7168, 1024
 // tokens: grad_X 293 us on 256 x 256 tiles, 377 us on 128 x 128).

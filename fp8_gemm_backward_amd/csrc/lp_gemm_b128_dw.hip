@@ -5,7 +5,9 @@ namespace lp {
 namespace gk {
 
 hipError_t b128_dw(const Params& prm, int tile, hipStream_t s) {
-  return tile == 256 ? run_b128<B256, kB128Dw>(prm, s) : tile == 128 ? run_b128<B128, kB128Dw>(prm, s) : run_b128<B64, kB128Dw>(prm, s);
+  return tile == 256   ? run_b128<B256, kB128Dw>(prm, s)
+         : tile == 128 ? run_b128<B128, kB128Dw>(prm, s)
+                       : run_b128<B64, kB128Dw>(prm, s);
 }
 
 }  // namespace gk

@@ -5,7 +5,9 @@ namespace lp {
 namespace gk {
 
 hipError_t b128_fwd(const Params& prm, int tile, hipStream_t s) {
-  return tile == 256 ? run_b128<B256, kB128Fwd>(prm, s) : tile == 128 ? run_b128<B128, kB128Fwd>(prm, s) : run_b128<B64, kB128Fwd>(prm, s);
+  return tile == 256   ? run_b128<B256, kB128Fwd>(prm, s)
+         : tile == 128 ? run_b128<B128, kB128Fwd>(prm, s)
+                       : run_b128<B64, kB128Fwd>(prm, s);
 }
 
 hipError_t b128_fwd_tail(const Params& prm, hipStream_t s) { return run_b128_tail<kB128Fwd>(prm, s); }

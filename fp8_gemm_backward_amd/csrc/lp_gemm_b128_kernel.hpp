@@ -11,8 +11,10 @@
 //   dW:  dw[n][k] = sum_b sg[b][n] * sx[b][k]     * sum_{m in b} cg[m][n] cx[m][k]
 //
 // The inner sum is one v_mfma_f32_16x16x128_f8f6f4 into a fresh fp32
-// accumulator (E4M3 products are exact in fp32); the outer sum is an fp32
-// multiply-add per result.  The scales are general fp32 numbers, which the
+// accumulator (E4M3 products are exact in fp32; inside the instruction the
+// core aligns them and drops low bits, at most 2^-12.6 of their magnitudes' sum
+// on random codes); the outer sum is an fp32 multiply-add per result, rounded
+// once, to bf16, when the contraction is done.  The scales are general fp32 numbers, which the
 // block-scaled MFMA (powers of two) cannot apply.
 //
 // Cost per 16 x 16 x 128: 32 MFMA cycles and 4 multiply-adds (16 cycles of
@@ -24,6 +26,14 @@
 // for few tiles, 128 x 128 by two groups of four waves of 64 x 64, or 64 x 64 by
 // four groups of two waves of 32 x 64; the groups of waves share the
 // contraction.
+//
+// 8192 x 4096 outputs: 1.59 us (forward, grad_X) and 1.86 us (grad_W) per 128 deep
+// stage and round of 256 tiles, 2.69 and 2.31 PFLOP/s asymptotically; with a contraction of 4096
+// 117, 116 and 135 us (2.35, 2.37, 2.04 PFLOP/s).  A plain FP8 product of the vendor's
+// library without block scales reaches 2.83 PFLOP/s at 8192^3.  Bound by power
+// and instruction issue: the clock falls to 1.9 GHz, the matrix cores are busy
+// 55% of the time, LDS 27%; leaving out grad_W's 128 multiplies per wave and stage takes
+// 272 us to 228 over a contraction of 8192.
 //
 // A 128-deep stage of both operands and its scales goes from global memory
 // straight into LDS, two stages deep; one barrier per stage.  LDS layouts:

@@ -11,6 +11,11 @@
 // fp32; the sums of the kWK waves that share 16 columns are added in wave
 // order at the end, so the result does not depend on timing.
 //
+// Bound by HBM where the weight is large (96 tokens over 64 experts of 2048 x
+// 7168: 95 us, 4.8 TB/s of weights), by latency otherwise: 8 x 4096 x 4096
+// 7.7 us with the weight in HBM, of which 3.4 are its bytes, about two the launch
+// and the rest the first loads' way there and back and the joint sums.
+//
 // kFuse (at most kFuseRows rows, dense): x comes as bf16 and every workgroup
 // quantizes it into LDS by the rule of lp_r128.hpp (a few KiB, read from L2)
 // while its first weight loads are in flight, which saves the quantizer's
@@ -193,16 +198,21 @@ template <bool kFuse, int kRT>
 hipError_t launch_split(const SkinnyArgs& a, size_t lds, hipStream_t s) {
   const int64_t waves = row_tiles(a.p, 16 * kRT) * ((a.p.Qtot + 15) / 16);
   if (a.p.offsets != nullptr)
-    return waves >= 4096 ? launch<1, kFuse, kRT>(a, lds, s) : waves >= 1024 ? launch<4, kFuse, kRT>(a, lds, s) : launch<8, kFuse, kRT>(a, lds, s);
-  return waves <= kCUs ? launch<8, kFuse, kRT>(a, lds, s) : waves <= 2 * kCUs ? launch<4, kFuse, kRT>(a, lds, s)
-         : waves <= 4 * kCUs ? launch<2, kFuse, kRT>(a, lds, s) : launch<1, kFuse, kRT>(a, lds, s);
+    return waves >= 4096   ? launch<1, kFuse, kRT>(a, lds, s)
+           : waves >= 1024 ? launch<4, kFuse, kRT>(a, lds, s)
+                           : launch<8, kFuse, kRT>(a, lds, s);
+  return waves <= kCUs       ? launch<8, kFuse, kRT>(a, lds, s)
+         : waves <= 2 * kCUs ? launch<4, kFuse, kRT>(a, lds, s)
+         : waves <= 4 * kCUs ? launch<2, kFuse, kRT>(a, lds, s)
+                             : launch<1, kFuse, kRT>(a, lds, s);
 }
 
 }  // namespace
 
 hipError_t b128_fwd_fused(const Params& prm, const void* x, hipStream_t s) {
   const size_t nb = ((size_t)prm.Ktot + kRun - 1) / kRun;
-  return launch_split<true, 1>(SkinnyArgs{prm, static_cast<const uint16_t*>(x), 0}, nb * (4 * kFuseRows + (size_t)prm.Ptot * kRun), s);
+  const size_t lds = nb * (4 * kFuseRows + (size_t)prm.Ptot * kRun);
+  return launch_split<true, 1>(SkinnyArgs{prm, static_cast<const uint16_t*>(x), 0}, lds, s);
 }
 
 // Whether 32 rows a wave rather than 16: where 16 would make more waves than

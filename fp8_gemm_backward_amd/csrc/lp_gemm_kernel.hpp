@@ -125,7 +125,8 @@ struct Params {
   // Grouped grad_X and forward through bf16 tiles, split by dispatch round
   // (tile_split): 1 takes the whole rounds of kCUs 256-wide tiles (all the
   // tiles when there is no split), 2 the last partial round as 256 x 128
-  // tiles, in a second launch.  0: no split.
+  // tiles, in a second launch.  0: no split.  (Products with fp32 scales per
+  // 128: 1 in both launches.)
   int32_t tail;
 };
 

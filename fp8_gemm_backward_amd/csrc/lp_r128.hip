@@ -14,7 +14,8 @@ constexpr int kRunLen = 128;
 // Runs along the columns.  Sixteen lanes hold a run, eight values each, and
 // take its largest magnitude with lane-row rotations.  A workgroup takes 16
 // rows x 4 runs: a row's four runs are 1 KiB in a line, and the 16 rows'
-// scales of one run index are 64 bytes in a line ([run][row]).
+// scales of one run index are 64 bytes in a line ([run][row]).  8192 x 4096 in
+// 17.6 us (5.7 TB/s), 24 x 2048 in 3.2 us (a launch).
 constexpr int kRunRows = 16, kRunCols = 4;
 
 __global__ __launch_bounds__(kThreads) void r128_cols(const uint16_t* __restrict__ src, uint8_t* __restrict__ codes,
