@@ -229,7 +229,8 @@ static bool wide_rows(const Params& p) {
 // 2048 10.4, 11.4, 9.6.  64 experts of 2048 x 7168: 512 tokens 196 to 235 us against 249 to
 // 259 on 128 x 128 tiles, 1024 tokens 330 against 262.)
 bool b128_skinny_fits(const Params& p) {
-  if (p.offsets != nullptr) return p.Ptot <= 8 * (int64_t)p.groups;
+  if (p.offsets != nullptr)                                      // (a launch has fewer than 2^32 threads)
+    return p.Ptot <= 8 * (int64_t)p.groups && row_tiles(p, 16) * (p.Qtot / 16 + 1) < (int64_t)1 << 25;
   return p.Ptot <= 16 || (p.Ptot <= 64 && row_tiles(p, 32) * ((p.Qtot + 15) / 16) <= kCUs);
 }
 

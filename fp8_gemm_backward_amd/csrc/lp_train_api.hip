@@ -28,10 +28,11 @@ lp_status check_quant(int64_t batch, int64_t rows, int64_t cols, bool by_rows, c
     if (rows >= (int64_t)1 << 30) return LP_ERR_SHAPE;
     if (!aligned(offsets, 4)) return LP_ERR_ALIGN;
   }
-  // One workgroup of 256 threads per tile; a launch has fewer than 2^32 threads.
+  // One workgroup of 256 threads per tile (512 for 128 x 128); a launch has fewer
+  // than 2^32 threads.
   const int64_t tiles = by_rows ? (batch * rows / 16 + 1) * (cols / 512 + 1)
                                 : batch * (rows / 128 + (offsets ? groups : 1)) * (cols / 128 + 1);
-  return tiles >= (int64_t)1 << 24 ? LP_ERR_SHAPE : LP_OK;
+  return tiles >= (int64_t)1 << (by_rows ? 24 : 23) ? LP_ERR_SHAPE : LP_OK;
 }
 
 lp_status check_buffers(int64_t n, const void* const* ptrs, int count) {

@@ -20,8 +20,8 @@
  * each element's sign.  Bit-exact.
  *
  * Sizes of the quantizers: cols % 16 == 0, fewer than 2^34 elements, and fewer
- * than 2^24 tiles of 128 x 128 (axis -1: of 16 x 512), partial ones and one
- * spare per batch entry or group counted (LP_ERR_SHAPE otherwise).
+ * than 2^23 tiles of 128 x 128 (axis -1: 2^24 of 16 x 512), partial ones and
+ * one spare per batch entry or group counted (LP_ERR_SHAPE otherwise).
  */
 #ifndef LP_TRAIN_H
 #define LP_TRAIN_H

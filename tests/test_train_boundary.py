@@ -40,6 +40,7 @@ def test_library_exports_every_function_of_the_header():
     ((FAKE, 1, 1 << 31, 64, -1, None, 0, FAKE, FAKE), SHAPE),
     ((FAKE, 1 << 20, 1 << 10, 16, -1, None, 0, FAKE, FAKE), SHAPE),   # 2^34 elements
     ((FAKE, 1 << 24, 1, 16, -2, None, 0, FAKE, FAKE), SHAPE),     # too many tiles
+    ((FAKE, 1 << 23, 1, 16, -2, None, 0, FAKE, FAKE), SHAPE),
     ((FAKE, 1, 4, 64, 0, None, 0, FAKE, FAKE), FORMAT),
     ((FAKE, 1, 4, 64, -1, FAKE, 2, FAKE, FAKE), FORMAT),          # offsets are for token runs
     ((FAKE, 2, 4, 64, -2, FAKE, 2, FAKE, FAKE), FORMAT),          # one batch entry only
