@@ -350,6 +350,10 @@ __host__ __device__ __forceinline__ bool takes_turns(const Params& p) {
   return p.ntiles > (kOp == kB128Dw && p.offsets != nullptr ? 8 : 1) * kCUs;
 }
 
+// LDS of this wave written and read, and every wave here (loads into the stages
+// go on).
+__device__ __forceinline__ void barrier_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 template <class C>
 inline constexpr bool kOwnRowsOf = C::KW == 1 && C::NS == 2;     // results pass through LDS of their own, 2 KiB a wave
 template <class C>
@@ -647,7 +651,39 @@ __device__ __forceinline__ void b128_tiles_of(const Params& p, uint8_t* all_smem
           __builtin_amdgcn_sched_barrier(0);
         }
       };
-      if (whole) store(IC<1>{});
+      // Rows that begin inside a 128-byte line: the waves that share 16 rows put
+      // them together, so that a row's 512 bytes have two broken lines and not eight.
+      // Memory takes a broken line of streamed stores several times over (57 experts
+      // of 3760 x 1040, 8000 rows 187 us, 156 this way; 3840 x 1024 111).  Stores that are not
+      // streamed meet in L2, which loses more where there is work beside (243 us for
+      // 207, 190 this way, 32 experts of 2064 x 4112).
+      const bool broken = kDW && ((p.ldc & 63) != 0 || (reinterpret_cast<uintptr_t>(p.C) & 127) != 0);
+      auto store_joint = [&] {
+        uint8_t* const joint = all_smem + C::NS * C::STAGE + wp * (C::NWQ * 2048);
+        const int c32 = el & 31, r0 = 4 * wq + (el >> 5), jcol = done.q0 + 8 * c32;
+#pragma unroll
+        for (int i = 0; i < C::FP; ++i) {
+#pragma unroll
+          for (int j = 0; j < C::FQ; ++j)
+            *reinterpret_cast<u32x2*>(joint + r16 * (2 * C::BQ) + 8 * ((wq * (C::WQ / 4) + 4 * j + (el >> 4)) ^ (2 * r16))) =
+                u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+          barrier_lds();
+          u32x4 v[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            v[h] = *reinterpret_cast<const u32x4*>(joint + (r0 + 2 * h) * (2 * C::BQ) + 16 * (c32 ^ (r0 + 2 * h)));
+          barrier_lds();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int at = done.p0 + wp * C::WP + 16 * i + r0 + 2 * h;
+            if (at < done.pend && jcol < p.Qtot)
+              __builtin_nontemporal_store(v[h], reinterpret_cast<u32x4*>(out + (int64_t)at * p.ldc + jcol));
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      if (broken) store_joint();
+      else if (whole) store(IC<1>{});
       else store(IC<0>{});
       if (!more) return;
       stores_behind = whole;
