@@ -264,16 +264,19 @@ void b128_tiles(Params& prm, int b, bool dw) {
   prm.ntiles = (int32_t)(pt * prm.nq);
 }
 
-// Grouped grad_X and forward split by dispatch round, as tile_split does: the
-// whole rounds of 256 x 256 tiles, then a short last round in parts of tiles by
-// a second launch (grouped_tile and b128_tail_kernel have the rules; figures with
-// halves).  For contractions of at least
-// 16 stages over at most five rounds: 16384 rows over 8 uneven experts, forward
-// 2048 x 4096 159 -> 149 us, grad_X of 4096 x 2048 161 -> 150; shorter ones and
-// more rounds only pay for the second launch (grad_X of 1536 x 6144, 10000 rows:
-// 103 -> 110; forward of 64 experts, six rounds: 568 -> 573).
+// Dense products, grouped grad_X and forward split by dispatch round, as
+// tile_split does: the whole rounds of 256 x 256 tiles, then a short last round
+// in parts of tiles by a second launch (rounds_of and b128_tail_kernel have the
+// rules).  For contractions of at least 16 stages over at most five rounds:
+// 4112 x 4112 x 8208 forward 212 -> 168 us, grad_W 198 -> 173; 8192 x 2560 x 4096 98 -> 85;
+// 16384 rows over 8 uneven experts, forward 2048 x 4096 159 -> 149, grad_X of
+// 4096 x 2048 161 -> 150 (in halves); shorter ones and more rounds only pay for the
+// second launch (grad_X of 1536 x 6144, 10000 rows: 103 -> 110; forward of 64
+// experts, six rounds: 568 -> 573).
 bool b128_split(Params& prm) {
-  if (prm.offsets == nullptr || prm.ntiles < kCUs || prm.ntiles > 5 * kCUs || prm.Ktot < 16 * 128) return false;
+  if (prm.ntiles < kCUs || prm.ntiles > 5 * kCUs || prm.Ktot < 16 * 128) return false;
+  const int rest = prm.ntiles % kCUs;                            // dense: known here
+  if (prm.offsets == nullptr && (prm.ntiles == rest || rest == 0 || 2 * rest > kCUs)) return false;
   prm.tail = 1;
   return true;
 }
@@ -310,10 +313,10 @@ hipError_t launch_gemm(const GemmCall& call, hipStream_t stream) {
     Params prm = base_params(call);
     const int tile = b128_tile(prm, call.dw ? B128Op::kDw : B128Op::kDx);
     b128_tiles(prm, tile, call.dw);
-    if (call.dw) return b128_dw(prm, tile, stream);
-    const bool split = tile == 256 && b128_split(prm);
-    const hipError_t e = b128_dx(prm, tile, stream);
-    return e != hipSuccess || !split ? e : b128_dx_tail(prm, stream);
+    const bool split = tile == 256 && !(call.dw && call.offsets != nullptr) && b128_split(prm);
+    const hipError_t e = call.dw ? b128_dw(prm, tile, stream) : b128_dx(prm, tile, stream);
+    if (e != hipSuccess || !split) return e;
+    return call.dw ? b128_dw_tail(prm, stream) : b128_dx_tail(prm, stream);
   }
   if (native_mx(call) || native_pt(call)) {
     const Params prm = native_params(call);

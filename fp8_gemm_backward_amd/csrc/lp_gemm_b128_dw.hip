@@ -10,5 +10,7 @@ hipError_t b128_dw(const Params& prm, int tile, hipStream_t s) {
                        : run_b128<B64, kB128Dw>(prm, s);
 }
 
+hipError_t b128_dw_tail(const Params& prm, hipStream_t s) { return run_b128_tail<kB128Dw>(prm, s); }
+
 }  // namespace gk
 }  // namespace lp

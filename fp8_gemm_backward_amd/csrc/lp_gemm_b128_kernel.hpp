@@ -217,14 +217,44 @@ struct B128Frag {
   }
 };
 
+// Params::tail (the host's choice to split by round): the whole rounds of kCUs
+// tiles when the last, partial one has at most kCUs / 2, every tile otherwise;
+// what that leaves is taken by a second launch in kParts parts of each
+// 256 x 256 tile: 256 x 128, 128 x 128 or 64 x 64.
+struct Rounds {
+  int full, rest;
+  bool split;
+};
+__device__ __forceinline__ Rounds rounds_of(const Params& p, int all) {
+  const int full = all / kCUs * kCUs, rest = all - full;
+  return Rounds{full, rest, p.tail != 0 && full > 0 && rest > 0 && 2 * rest <= kCUs};
+}
+// Workgroup hw's whole tile (-1: none) and part of it.
+template <int kParts>
+__device__ __forceinline__ int2 tile_of(const Params& p, int all, int hw) {
+  const Rounds r = rounds_of(p, all);
+  const int nt = kParts > 1 ? (r.split ? kParts * r.rest : 0) : r.split ? r.full : all;
+  if (hw >= nt) return make_int2(-1, 0);
+  const int i = xcd_remap(hw, nt);
+  return kParts > 1 ? make_int2(r.full + i / kParts, i % kParts) : make_int2(i, 0);
+}
+template <class C, int kParts>
+inline constexpr int kWholeRows = kParts > 1 ? 256 : C::BP;      // of a whole tile
+template <class C, int kParts>
+inline constexpr int kPartCols = kParts > 1 ? 256 / C::BQ : 1;   // parts side by side
+
 // Tiles of a dense product: a contiguous range for each XCD, in blocks that
 // share operand rows and columns.
-template <class C>
+template <class C, int kParts>
 __device__ __forceinline__ Tile dense_tile(const Params& p, int hw) {
-  const int tile = xcd_remap(hw, p.ntiles);
-  int2 pq = make_int2(tile / p.nq, tile % p.nq);
-  if (p.gm > 1) pq = grouped_order(tile, (p.Ptot + C::BP - 1) / C::BP, p.nq, p.gm);
-  return Tile{0, pq.x * C::BP, p.Ptot, pq.y * C::BQ, 0, p.Ktot, tile, 0, true};
+  constexpr int kRows = kWholeRows<C, kParts>, kCols = kPartCols<C, kParts>;
+  const int2 w = tile_of<kParts>(p, p.ntiles, hw);
+  if (w.x < 0) return Tile{0, 0, 0, 0, 0, 0, 0, 0, false};
+  int2 pq = make_int2(w.x / p.nq, w.x % p.nq);
+  if (p.gm > 1) pq = grouped_order(w.x, (p.Ptot + kRows - 1) / kRows, p.nq, p.gm);
+  Tile t{0, pq.x * kRows + w.y / kCols * C::BP, p.Ptot, (pq.y * kCols + w.y % kCols) * C::BQ, 0, p.Ktot, 0, 0, false};
+  t.valid = t.p0 < p.Ptot && t.q0 < p.Qtot;
+  return t;
 }
 
 // Tiles of a grouped forward or grad_X.  Row tiles of 256 rows or less never
@@ -254,18 +284,10 @@ __device__ __forceinline__ GroupScan scan_groups(const Params& p, int M, int bas
   return GroupScan{s, e, seen0 + sum - n, __builtin_amdgcn_readlane(e, 63), seen0 + __builtin_amdgcn_readlane(sum, 63)};
 }
 
-// Params::tail (host's choice to split by round): the whole rounds of kCUs
-// tiles when the last, partial one has at most kCUs / 2, every tile otherwise;
-// what that leaves is taken by a second launch in kParts parts of each
-// 256 x 256 tile, 256 x 128 or 128 x 128.
-//
 // sc0: the scan of at most 64 groups, unless there are more.
-__device__ __forceinline__ bool rounds_split(const Params& p, int full, int rest) {
-  return p.tail != 0 && full > 0 && rest > 0 && 2 * rest <= kCUs;
-}
 template <class C, int kParts>
 __device__ __forceinline__ Tile grouped_tile(const Params& p, const GroupScan& sc0, int hw) {
-  constexpr int kRows = kParts > 1 ? 256 : C::BP;                // of a whole tile
+  constexpr int kRows = kWholeRows<C, kParts>, kCols = kPartCols<C, kParts>;
   Tile t{0, 0, 0, 0, 0, p.Ktot, 0, 0, false};
   GroupScan sc = sc0;
   int end0 = 0, rows = sc0.last_seen;
@@ -278,13 +300,9 @@ __device__ __forceinline__ Tile grouped_tile(const Params& p, const GroupScan& s
     }
   }
   const int nq = kParts > 1 ? (p.Qtot + 255) / 256 : p.nq;
-  const int all = rows * nq, full = all / kCUs * kCUs, rest = all - full;
-  const bool split = rounds_split(p, full, rest);
-  const int nt = kParts > 1 ? (split ? kParts * rest : 0) : split ? full : all;
-  if (hw >= nt) return t;
-  int tile = xcd_remap(hw, nt);
-  const int part = tile % kParts;
-  if (kParts > 1) tile = full + tile / kParts;
+  const int2 whole = tile_of<kParts>(p, rows * nq, hw);
+  if (whole.x < 0) return t;
+  const int tile = whole.x, part = whole.y;
   const int pidx = tile / nq;
   if (p.groups > 64) {
     end0 = rows = 0;
@@ -306,9 +324,8 @@ __device__ __forceinline__ Tile grouped_tile(const Params& p, const GroupScan& s
   t.pend = __builtin_amdgcn_readlane(sc.end, l);
   int2 pq = make_int2(pidx - seen, tile - pidx * nq);
   if (p.gm > 1) pq = grouped_order(tile - seen * nq, (t.pend - start + kRows - 1) / kRows, nq, p.gm);
-  constexpr int kPartCols = kParts > 1 ? 256 / C::BQ : 1;
-  t.p0 = start + pq.x * kRows + part / kPartCols * C::BP;
-  t.q0 = (pq.y * kPartCols + part % kPartCols) * C::BQ;
+  t.p0 = start + pq.x * kRows + part / kCols * C::BP;
+  t.q0 = (pq.y * kCols + part % kCols) * C::BQ;
   t.valid = t.q0 < p.Qtot && t.p0 < t.pend;
   return t;
 }
@@ -381,7 +398,7 @@ __device__ __forceinline__ void b128_tiles_of(const Params& p, uint8_t* all_smem
     if (kDW) rank = size_rank(sc, p.groups);
   }
   auto pick = [&](int hw) {                                      // of a dense product or at most 64 groups
-    if (p.offsets == nullptr) return dense_tile<C>(p, hw);
+    if (p.offsets == nullptr) return dense_tile<C, kParts>(p, hw);
     return kDW ? grouped_dw_tile<C>(p, sc, rank, hw) : grouped_tile<C, kParts>(p, sc, hw);
   };
   int hw = blockIdx.x;
@@ -721,19 +738,26 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   b128_tiles_of<C, kOp, 1>(p, smem);
 }
 
-// The last, partial round of a grouped forward or grad_X: quarters when they
-// fit one round and the contraction has 32 stages, halves otherwise.  (Forward
-// of 2048 x 4096 in 8 groups, two rounds and 48 tiles 150 us with halves, 145
-// with quarters; 56 stages, 64 tiles left, 493 -> 485; grad_X of the former, 16
-// stages and 64 tiles left, 155 -> 158.)
+// The last, partial round, in the smallest parts that fit one round: 64 x 64
+// (the contraction over four groups of waves), then 128 x 128 if it has 32
+// stages, else halves.  (4100 x 4096 x 2048, 16 tiles left, 53.7 us whole, 48.7 in
+// halves, 41.2 in sixteenths; 6000 x 2800 x 2832, 8 left, 82.7, 72.9, 59.3.  Forward of
+// 2048 x 4096 in 8 groups, 48 left, 150 us in halves, 145 in quarters; 56 stages, 64
+// left, 493 -> 485; but 16 stages, 64 left, 155 -> 158.)
 template <int kOp>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void b128_tail_kernel(Params p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kLdsOf<B128> > kLdsOf<B256N> ? kLdsOf<B128> : kLdsOf<B256N>];
-  GroupScan sc{};
-  for (int base = 0; base < p.groups; base += 64) sc = scan_groups<256>(p, p.Ptot, base, sc.last_end, sc.last_seen);
-  const int all = sc.last_seen * ((p.Qtot + 255) / 256), full = all / kCUs * kCUs, rest = all - full;
-  if (!rounds_split(p, full, rest)) return;
-  if (4 * rest <= kCUs && p.Ktot >= 32 * kRun) b128_tiles_of<B128, kOp, 4>(p, smem);
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kLdsOf<B256N>];
+  static_assert(kLdsOf<B128> <= kLdsOf<B256N> && kLdsOf<B64> <= kLdsOf<B256N>);
+  int all = p.ntiles;
+  if (kOp != kB128Dw && p.offsets != nullptr) {
+    GroupScan sc{};
+    for (int base = 0; base < p.groups; base += 64) sc = scan_groups<256>(p, p.Ptot, base, sc.last_end, sc.last_seen);
+    all = sc.last_seen * ((p.Qtot + 255) / 256);
+  }
+  const Rounds r = rounds_of(p, all);
+  if (!r.split) return;
+  if (16 * r.rest <= kCUs) b128_tiles_of<B64, kOp, 16>(p, smem);
+  else if (4 * r.rest <= kCUs && p.Ktot >= 32 * kRun) b128_tiles_of<B128, kOp, 4>(p, smem);
   else b128_tiles_of<B256N, kOp, 2>(p, smem);
 }
 

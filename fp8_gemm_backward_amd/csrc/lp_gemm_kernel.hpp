@@ -1016,9 +1016,10 @@ hipError_t b128_fwd_skinny(const Params& prm, hipStream_t s);
 hipError_t b128_fwd_fused(const Params& prm, const void* x, hipStream_t s);
 hipError_t b128_dx(const Params& prm, int tile, hipStream_t s);
 hipError_t b128_dw(const Params& prm, int tile, hipStream_t s);
-// The last dispatch round of a grouped call in parts of tiles (Params::tail).
+// The last dispatch round in parts of tiles (Params::tail); grad_W: dense.
 hipError_t b128_fwd_tail(const Params& prm, hipStream_t s);
 hipError_t b128_dx_tail(const Params& prm, hipStream_t s);
+hipError_t b128_dw_tail(const Params& prm, hipStream_t s);
 
 }  // namespace gk
 }  // namespace lp

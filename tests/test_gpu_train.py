@@ -174,11 +174,13 @@ def decoded_rows(q, ends=None):
 
 
 # one row to several tiles, sizes off every tile, one long contraction, 256 tiles of 256 x 256, then more of them (ragged
-# at both edges) for each product in turn
+# at both edges) for each product in turn, then long contractions, whose last round is cut into sixteenths (forward and
+# grad_W of the first), quarters (its grad_X) and halves (forward of the second, grad_W of the third)
 DENSE = [(1, 16, 16), (3, 4112, 272), (1, 8208, 272), (2, 16400, 144), (14, 8208, 528), (9, 16400, 272), (24, 4096, 400),
          (31, 2064, 2064), (48, 1040, 528), (64, 2048, 144), (61, 784, 4112), (1, 512, 2048), (2, 144, 128), (5, 272, 1040), (16, 4096, 512), (17, 400, 400), (33, 128, 144),
          (64, 272, 272), (65, 528, 656), (128, 128, 128), (129, 272, 400), (300, 1040, 144), (700, 512, 4112),
-         (4096, 4096, 144), (4112, 4368, 272), (4112, 272, 4368), (272, 4112, 4368)]
+         (4096, 4096, 144), (4112, 4368, 272), (4112, 272, 4368), (272, 4112, 4368),
+         (4112, 4096, 4112), (5000, 4112, 2064), (2064, 4112, 5120)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -199,8 +201,10 @@ def test_dense_products(lp, M, N, K):
 GROUPED = [([5], 16, 16), ([0, 0, 3], 144, 128), ([1] * 9, 272, 272), ([0, 1, 127, 128, 129, 0, 300, 5], 272, 400),
            ([2, 0, 1, 4] * 80, 128, 144), ([900, 30, 0, 600, 257], 1040, 272), ([2500, 1500, 0, 97], 4096, 144),
            ([2500, 1500, 0, 97], 144, 4096),
-           # tiles left after one round of 256, forward: 64 and 32 over 33 stages, 50 over 17; grad_X: 84 over 31, 50 over 32
-           ([2500, 0, 2300, 130], 3856, 4112), ([2500, 1700, 0, 97], 4096, 4112), ([2500, 1700, 0, 97], 4112, 2064)]
+           # tiles left after one round of 256, forward: 64 and 32 over 33 stages, 50 over 17, 16 over 17;
+           # grad_X: 84 over 31, 50 over 32
+           ([2500, 0, 2300, 130], 3856, 4112), ([2500, 1700, 0, 97], 4096, 4112), ([2500, 1700, 0, 97], 4112, 2064),
+           ([2500, 1500, 0, 97], 4096, 2064)]
 
 
 @pytest.mark.parametrize("sizes,N,K", GROUPED)
