@@ -308,7 +308,8 @@ def lp_linear_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor],
     """(grad_X [M,K] or None, grad_W [N,K] or None) of a linear layer.
     `workspace`: a zero-filled uint8 device tensor of at least
     lp_linear_bwd_workspace(...) bytes lets the call split its contraction
-    (lp_linear_bwd_ws); None calls lp_linear_bwd."""
+    (lp_linear_bwd_ws); None calls lp_linear_bwd.  "fp8_r128" gradients need
+    no zeroes, and get a workspace here when the call can use one."""
     M, N = grad_out.rows, grad_out.cols
     K = (w if need_dx else x).cols
     dev = grad_out.codes.device
@@ -327,6 +328,15 @@ def lp_linear_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor],
     wc = w.c() if w is not None else None
     args = (ctypes.byref(g), ctypes.byref(xc) if xc else None, ctypes.byref(wc) if wc else None,
             grad_x.data_ptr() if need_dx else None, grad_w.data_ptr() if need_dw else None)
+    if workspace is None and grad_out.fmt == "fp8_r128" and need_dx != need_dw:
+        out_rows, depth = (M, N) if need_dx else (N, M)
+        if depth > 31 * 128 and -(-out_rows // 128) * -(-K // 128) <= 128:     # else it would not split
+            nbytes = ctypes.c_size_t(0)
+            _check(lib.lp_linear_bwd_workspace(*args, ctypes.byref(nbytes)), "lp_linear_bwd_workspace")
+            if nbytes.value:
+                workspace = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+                if stream is not None:
+                    workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream))
     if workspace is None:
         st = lib.lp_linear_bwd(*args, _stream(stream))
         _check(st, "lp_linear_bwd")

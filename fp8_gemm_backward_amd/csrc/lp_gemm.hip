@@ -206,7 +206,21 @@ SplitPlan split_plan(const GemmCall& call) {
 
 using namespace gk;
 
-size_t gemm_workspace_bytes(const GemmCall& call) { return split_plan(call).bytes; }
+namespace {
+
+struct B128Plan {
+  int tile;            // tile size
+  int splits;          // workgroups that share a tile's contraction
+  int split_len;       // its elements for each
+  size_t bytes;        // workspace, 0 without splits
+};
+B128Plan b128_plan(const GemmCall& call);
+
+}  // namespace
+
+size_t gemm_workspace_bytes(const GemmCall& call) {
+  return native_b128(call) ? b128_plan(call).bytes : split_plan(call).bytes;
+}
 
 namespace {
 
@@ -306,11 +320,57 @@ int b128_tile(const Params& prm, B128Op op) {
   return c64 <= c128 && c64 <= c256 ? 64 : c128 <= c256 ? 128 : 256;
 }
 
+// The first 4 KiB of a workspace hold what other products need zero between calls
+// (their tiles' counters): left alone.
+constexpr size_t kB128WsHead = 4096;
+
+// A dense grad_X or grad_W of few tiles over a long contraction, given a
+// workspace: several workgroups to a tile, an fp32 tile from each, and a
+// second launch that adds them.  By the same estimate as b128_tile, plus 5 us
+// for that launch and the way of the fp32 tiles to memory and back (8 bytes an
+// element at 5 TB/s); at least 16 stages to a workgroup.  grad_W of 240 x 240 over 21648
+// rows 81.9 us without, 19.8 with; 16 x 4096 over 32768 96.4, 35.0; 64 x 4096 over 8192
+// 27.1, 17.2; 1024 x 1024 over 32768 99.5, 52.1, over 8192 (64 stages, 64 tiles of 128 x
+// 128) left whole at 28.2.
+B128Plan b128_plan(const GemmCall& call) {
+  const B128Op op = call.dw ? B128Op::kDw : B128Op::kDx;
+  const Params prm = base_params(call);
+  B128Plan best{b128_tile(prm, op), 1, prm.Ktot, 0};
+  const int64_t runs = (prm.Ktot + 127) / 128;
+  if (call.offsets != nullptr || best.tile == 256 || runs < 32) return best;
+  auto stage = [](int tile, int64_t n) { return tile == 64 ? (n <= kCUs / 2 ? 20 : 28) : (n <= kCUs / 2 ? 50 : 62); };
+  int64_t cost = INT64_MAX;
+  for (int tile : {64, 128}) {
+    Params t = prm;
+    b128_tiles(t, tile, call.dw);
+    if (t.ntiles <= 0 || t.ntiles > kCUs) continue;
+    for (int64_t s = 1; s * t.ntiles <= kCUs && runs / s >= 16; ++s) {
+      const int64_t per = (runs + s - 1) / s;
+      if (s > 1 && (runs + per - 1) / per != s) continue;        // no empty split
+      const int64_t joint = s > 1 ? 500 + t.ntiles * s * tile * tile / 6250 : 0;
+      const int64_t c = stage(tile, t.ntiles * s) * per + joint;
+      if (c >= cost) continue;
+      cost = c;
+      best = B128Plan{tile, (int)s, (int)(per * 128), s > 1 ? kB128WsHead + (size_t)t.ntiles * s * tile * tile * 4 : 0};
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
 hipError_t launch_gemm(const GemmCall& call, hipStream_t stream) {
   if (native_b128(call)) {
     Params prm = base_params(call);
+    const B128Plan plan = b128_plan(call);
+    if (plan.splits > 1 && call.ws != nullptr && call.ws_bytes >= plan.bytes) {
+      b128_tiles(prm, plan.tile, call.dw);
+      prm.splits = plan.splits;
+      prm.split_len = plan.split_len;
+      prm.ws = reinterpret_cast<float*>(static_cast<uint8_t*>(call.ws) + kB128WsHead);
+      const hipError_t e = call.dw ? b128_dw(prm, plan.tile, stream) : b128_dx(prm, plan.tile, stream);
+      return e != hipSuccess ? e : b128_join(prm, plan.tile, stream);
+    }
     const int tile = b128_tile(prm, call.dw ? B128Op::kDw : B128Op::kDx);
     b128_tiles(prm, tile, call.dw);
     const bool split = tile == 256 && !(call.dw && call.offsets != nullptr) && b128_split(prm);

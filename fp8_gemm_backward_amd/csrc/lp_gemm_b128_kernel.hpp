@@ -208,7 +208,7 @@ struct B128Frag {
       const uint32_t at = ((uint32_t)(uintptr_t)(lds_i32x2b*)tile + (uint32_t)a) ^ (16 * f);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const i32x2b x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2b*)(at + (64 * (t / 2) + 8 * (t % 2)) * kMN));
+        const i32x2b x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2b*)(uintptr_t)(at + (64 * (t / 2) + 8 * (t % 2)) * kMN));
         v[2 * t] = x[0];
         v[2 * t + 1] = x[1];
       }
@@ -243,17 +243,34 @@ inline constexpr int kWholeRows = kParts > 1 ? 256 : C::BP;      // of a whole t
 template <class C, int kParts>
 inline constexpr int kPartCols = kParts > 1 ? 256 / C::BQ : 1;   // parts side by side
 
+// Row and column of tile i of a dense product.
+__device__ __forceinline__ int2 dense_order(const Params& p, int rows, int i) {
+  return p.gm > 1 ? grouped_order(i, (p.Ptot + rows - 1) / rows, p.nq, p.gm) : make_int2(i / p.nq, i % p.nq);
+}
+
 // Tiles of a dense product: a contiguous range for each XCD, in blocks that
-// share operand rows and columns.
+// share operand rows and columns.  Params::splits workgroups share a tile's
+// contraction, split_len elements each, and leave fp32 tiles (b128_join).
 template <class C, int kParts>
 __device__ __forceinline__ Tile dense_tile(const Params& p, int hw) {
   constexpr int kRows = kWholeRows<C, kParts>, kCols = kPartCols<C, kParts>;
-  const int2 w = tile_of<kParts>(p, p.ntiles, hw);
-  if (w.x < 0) return Tile{0, 0, 0, 0, 0, 0, 0, 0, false};
-  int2 pq = make_int2(w.x / p.nq, w.x % p.nq);
-  if (p.gm > 1) pq = grouped_order(w.x, (p.Ptot + kRows - 1) / kRows, p.nq, p.gm);
-  Tile t{0, pq.x * kRows + w.y / kCols * C::BP, p.Ptot, (pq.y * kCols + w.y % kCols) * C::BQ, 0, p.Ktot, 0, 0, false};
+  int split = 0;
+  int2 w;
+  if (kParts == 1 && C::KW > 1 && p.splits > 1) {                // the splits of a tile are neighbours
+    const int i = xcd_remap(hw, p.ntiles * p.splits);
+    w = make_int2(i / p.splits, 0);
+    split = i - w.x * p.splits;
+  } else {
+    w = tile_of<kParts>(p, p.ntiles, hw);
+    if (w.x < 0) return Tile{0, 0, 0, 0, 0, 0, 0, 0, false};
+  }
+  const int2 pq = dense_order(p, kRows, w.x);
+  Tile t{0, pq.x * kRows + w.y / kCols * C::BP, p.Ptot, (pq.y * kCols + w.y % kCols) * C::BQ, 0, p.Ktot, w.x, split, false};
   t.valid = t.p0 < p.Ptot && t.q0 < p.Qtot;
+  if (kParts == 1 && C::KW > 1 && p.splits > 1) {
+    t.kbeg = split * p.split_len;
+    t.kend = p.Ktot - t.kbeg < p.split_len ? p.Ktot : t.kbeg + p.split_len;
+  }
   return t;
 }
 
@@ -432,7 +449,7 @@ __device__ __forceinline__ void b128_tiles_of(const Params& p, uint8_t* all_smem
     lq.start(p.Q, kDW ? 0 : t.g, t.q0, p.Qtot, t.kbeg, t.kend);
     lp.advance(kw);
     lq.advance(kw);
-    const int64_t run0 = kDW ? (t.kbeg / kRun + t.g) : 0;        // first scale row of the contraction
+    const int64_t run0 = t.kbeg / kRun + (kDW ? t.g : 0);        // first scale row of the contraction
     if (sp_wave || kDW) {
       const int first = (sp_wave ? t.p0 : t.q0) + 64 * sv, cols = (sp_wave ? p.Ptot : p.Qtot) - first;
       sstep = sp_wave ? p.P.scale_ld : p.Q.scale_ld;
@@ -442,6 +459,7 @@ __device__ __forceinline__ void b128_tiles_of(const Params& p, uint8_t* all_smem
       const int qb = (t.q0 + 64 * sv) / kRun;                    // the 128-column block of these 64 columns
       sbase = p.Q.scales + (int64_t)t.g * p.Q.scale_batch + (kQK ? (int64_t)qb * p.Q.scale_ld : qb * 4);
       sstep = kQK ? 4 : p.Q.scale_ld;
+      sbase += run0 * sstep;
       slen = qb * kRun < p.Qtot ? 4 : 0;
     }
     sbase += (uint64_t)kw * sstep;
@@ -609,6 +627,12 @@ __device__ __forceinline__ void b128_tiles_of(const Params& p, uint8_t* all_smem
             for (int d = 0; d < 4; ++d) e[4 * h + d] = g == 0 ? v[d] : e[4 * h + d] + v[d];
           }
         }
+        if (p.splits > 1) {
+          f32x4* const part = reinterpret_cast<f32x4*>(p.ws + ((size_t)t.tile * p.splits + t.split) * (C::BP * C::BQ) + r * C::BQ + 4 * c);
+          part[0] = f32x4{e[0], e[1], e[2], e[3]};
+          part[1] = f32x4{e[4], e[5], e[6], e[7]};
+          continue;
+        }
         const int row = t.p0 + r, col = t.q0 + 4 * c;
         if (row < t.pend && col < p.Qtot)
           *reinterpret_cast<u32x4*>(out + (int64_t)row * p.ldc + col) =
@@ -764,7 +788,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 template <class C, int kOp>
 inline hipError_t run_b128(const Params& prm, hipStream_t s) {
   if (prm.ntiles <= 0) return hipSuccess;
-  b128_kernel<C, kOp><<<dim3(takes_turns<C, kOp>(prm) ? kCUs : prm.ntiles), dim3(64 * C::NW * C::KW), 0, s>>>(prm);
+  b128_kernel<C, kOp><<<dim3(takes_turns<C, kOp>(prm) ? kCUs : prm.ntiles * prm.splits), dim3(64 * C::NW * C::KW), 0, s>>>(prm);
   return hipGetLastError();
 }
 

@@ -1020,6 +1020,9 @@ hipError_t b128_dw(const Params& prm, int tile, hipStream_t s);
 hipError_t b128_fwd_tail(const Params& prm, hipStream_t s);
 hipError_t b128_dx_tail(const Params& prm, hipStream_t s);
 hipError_t b128_dw_tail(const Params& prm, hipStream_t s);
+// Adds the fp32 tiles (tile x tile) that the splits of a dense product left in
+// Params::ws.
+hipError_t b128_join(const Params& prm, int tile, hipStream_t s);
 
 }  // namespace gk
 }  // namespace lp

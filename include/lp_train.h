@@ -11,6 +11,11 @@
  *   grad_X = lp_linear_bwd / lp_grouped_bwd    grad_out LP_FP8_R128 (axis -1), w LP_FP8_B128
  *   grad_W = lp_linear_bwd / lp_grouped_bwd    grad_out and x LP_FP8_R128 (axis -2)
  *
+ * lp_linear_bwd_workspace reports a size for a dense product of few output tiles
+ * over a long contraction, and lp_linear_bwd_ws then splits it; of these
+ * operands' workspace nothing need be zero before the call, its first 4 KiB
+ * are left alone, the rest is overwritten.
+ *
  * Quantization rule, shared by every function here.  A set of values (a run
  * of 128 along an axis, cut at the tensor's edge, or a 128 x 128 block) with
  * largest magnitude a gets

@@ -244,6 +244,35 @@ def test_grouped_products(lp, sizes, N, K, tail):
         assert_product(dw[k], grv[a:b].T, xrv[a:b], f"dW of group {k}")
 
 
+@pytest.mark.parametrize("M,N,K", [(4100, 16, 16), (9000, 80, 144), (5000, 272, 400), (20, 4240, 400), (130, 8208, 144),
+                                   (1, 4112, 16), (12345, 240, 240)])
+def test_split_contractions(lp, M, N, K):
+    """Few output tiles over a long contraction: split over workgroups when there is a workspace (the binding's own, one
+    of the caller's that holds garbage, or the library's), whole without; the workspace's head stays as it was."""
+    rng = np.random.default_rng(M + N + K)
+    w, wv = weight(lp, rng, 1, N, K)
+    x, g = bf16_dev(bits(rng, (M, K))), bf16_dev(bits(rng, (M, N), 1e-3))
+    gc, gr = lp.lp_r128_quant_dual(g)
+    xr = lp.lp_r128_quant(x, -2)
+    for q, other, ref, kw in ((gc, w, (decoded(gc), wv[0]), dict(need_dw=False)),
+                              (gr, xr, (decoded_rows(gr).T, decoded_rows(xr)), dict(need_dx=False))):
+        args = (q, None, other) if "need_dw" in kw else (q, other, None)
+        n = lp.lp_linear_bwd_workspace(*args, **kw)
+        depth = N if "need_dw" in kw else M
+        assert n > 0 if depth > 8000 else n == 0 if depth < 4000 else True
+        at = 0 if "need_dw" in kw else 1
+        own = lp.lp_linear_bwd(*args, **kw)[at]
+        assert_product(own, *ref, "the binding's workspace")
+        if n == 0:
+            continue
+        assert torch.equal(own, lp.lp_linear_bwd(*args, **kw)[at])
+        ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+        assert torch.equal(own, lp.lp_linear_bwd(*args, workspace=ws, **kw)[at])
+        assert (ws[:4096] == 0xA5).all()
+        assert torch.equal(own, lp.lp_linear_bwd_noalloc(*args, **kw)[at])
+        assert_product(lp.lp_linear_bwd(*args, workspace=ws[:256], **kw)[at], *ref, "too small a workspace: whole")
+
+
 def test_grouped_grad_w_of_many_tiles(lp):
     """More tiles than the workgroups side by side take in eight turns, sizes of empty, short and long groups mixed:
     bit for bit what the groups give in calls of a few groups (checked above)."""

@@ -97,11 +97,17 @@ def test_linear_bwd_rejects(g, x, w, dx, dw, expect):
     assert lin(g, x, w, dx, dw) == expect
 
 
-def test_split_workspace_is_not_asked_for():
-    n = ctypes.c_size_t(7)
-    g, w = q(R, 8, 8192), q(B, 8192, 64)
-    assert lp.lib.lp_linear_bwd_workspace(ctypes.byref(g), None, ctypes.byref(w), FAKE, None, ctypes.byref(n)) == OK
-    assert n.value == 0
+def test_split_workspace():
+    """Asked for only where few tiles meet a long contraction."""
+    def need(g, x, w, dx, dw):
+        n = ctypes.c_size_t(7)
+        args = [None if t is None else ctypes.byref(t) for t in (g, x, w)]
+        assert lp.lib.lp_linear_bwd_workspace(*args, dx, dw, ctypes.byref(n)) == OK
+        return n.value
+    for M, N, K, expect in ((16, 8192, 64, True), (16, 1024, 64, False), (4096, 8192, 4096, False)):
+        assert (need(q(R, M, N), None, q(B, N, K), FAKE, None) > 4096) == expect, "grad_X"
+        assert (need(q(R, N, M, axis=-2), q(R, N, K, axis=-2), None, None, FAKE) > 4096) == expect, "grad_W"
+    assert need(q(R, 8, 1024), None, q(B, 1024, 64), FAKE, None) == 0
 
 
 @pytest.mark.parametrize("x,w,expect", [
