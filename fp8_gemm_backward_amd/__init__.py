@@ -310,17 +310,19 @@ def lp_linear_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor],
     lp_linear_bwd_workspace(...) bytes lets the call split its contraction
     (lp_linear_bwd_ws); None calls lp_linear_bwd.  "fp8_r128" gradients need
     no zeroes, and get a workspace here when the call can use one."""
-    M, N = grad_out.rows, grad_out.cols
+    _, M, N = grad_out.shape
     K = (w if need_dx else x).cols
-    dev = grad_out.codes.device
-    if need_dx and grad_x is None:
-        grad_x = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-    if need_dw and grad_w is None:
-        grad_w = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+    codes = grad_out.codes
     if need_dx:
-        _device(grad_x, "grad_x", 2 * M * K)
+        if grad_x is None:
+            grad_x = codes.new_empty((M, K), dtype=torch.bfloat16)
+        else:
+            _device(grad_x, "grad_x", 2 * M * K)
     if need_dw:
-        _device(grad_w, "grad_w", 2 * N * K)
+        if grad_w is None:
+            grad_w = codes.new_empty((N, K), dtype=torch.bfloat16)
+        else:
+            _device(grad_w, "grad_w", 2 * N * K)
     if workspace is not None:
         _device(workspace, "workspace", 1)
     g = grad_out.c()
@@ -334,7 +336,7 @@ def lp_linear_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor],
             nbytes = ctypes.c_size_t(0)
             _check(lib.lp_linear_bwd_workspace(*args, ctypes.byref(nbytes)), "lp_linear_bwd_workspace")
             if nbytes.value:
-                workspace = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+                workspace = torch.empty(nbytes.value, dtype=torch.uint8, device=codes.device)
                 if stream is not None:
                     workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream))
     if workspace is None:
@@ -424,18 +426,20 @@ def lp_grouped_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor]
                    grad_w: Optional[torch.Tensor] = None, stream=None):
     """(grad_X [M,K] or None, grad_W [G,N,K] or None) of a grouped matmul.
     Rows of grad_X at or past offsets[-1] are left as they were in `grad_x`."""
-    M, N = grad_out.rows, grad_out.cols
+    _, M, N = grad_out.shape
     G = offsets.numel()
     K = (w if need_dx else x).cols
-    dev = grad_out.codes.device
-    if need_dx and grad_x is None:
-        grad_x = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-    if need_dw and grad_w is None:
-        grad_w = torch.empty((G, N, K), dtype=torch.bfloat16, device=dev)
+    codes = grad_out.codes
     if need_dx:
-        _device(grad_x, "grad_x", 2 * M * K)
+        if grad_x is None:
+            grad_x = codes.new_empty((M, K), dtype=torch.bfloat16)
+        else:
+            _device(grad_x, "grad_x", 2 * M * K)
     if need_dw:
-        _device(grad_w, "grad_w", 2 * G * N * K)
+        if grad_w is None:
+            grad_w = codes.new_empty((G, N, K), dtype=torch.bfloat16)
+        else:
+            _device(grad_w, "grad_w", 2 * G * N * K)
     _device(offsets, "offsets", 4 * G, torch.int32)
     g = grad_out.c()
     xc = x.c() if x is not None else None
@@ -499,10 +503,8 @@ def lp_r128_quant(src: torch.Tensor, axis: int = -1, offsets: Optional[torch.Ten
     "fp8_r128" along `axis` (-1 or -2).  offsets (axis -2): int32 cumulative
     group ends; runs restart at every group's first row."""
     b, r, c = shape = _shape3(src)
-    dev = src.device
-    codes = torch.empty(shape, dtype=torch.uint8, device=dev)
-    scales = torch.empty((b, -(-c // 128), r) if axis == -1 else (b, _runs(r, offsets), c), dtype=torch.float32,
-                         device=dev)
+    codes = src.new_empty(shape, dtype=torch.uint8)
+    scales = src.new_empty((b, -(-c // 128), r) if axis == -1 else (b, _runs(r, offsets), c), dtype=torch.float32)
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
     _check(lib.lp_r128_quant(src.data_ptr(), b, r, c, axis, *_offsets(offsets), codes.data_ptr(), scales.data_ptr(),
                              _stream(stream)), "lp_r128_quant")
@@ -514,11 +516,10 @@ def lp_r128_quant_dual(src: torch.Tensor, offsets: Optional[torch.Tensor] = None
     -2); the second one's runs restart at each group of `offsets`.  Rows past
     the last offset are left unwritten in both."""
     b, r, c = shape = _shape3(src)
-    dev = src.device
-    codes_c = torch.empty(shape, dtype=torch.uint8, device=dev)
+    codes_c = src.new_empty(shape, dtype=torch.uint8)
     codes_r = torch.empty_like(codes_c)
-    scales_c = torch.empty((b, -(-c // 128), r), dtype=torch.float32, device=dev)
-    scales_r = torch.empty((b, _runs(r, offsets), c), dtype=torch.float32, device=dev)
+    scales_c = src.new_empty((b, -(-c // 128), r), dtype=torch.float32)
+    scales_r = src.new_empty((b, _runs(r, offsets), c), dtype=torch.float32)
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
     _check(lib.lp_r128_quant_dual(src.data_ptr(), b, r, c, *_offsets(offsets), codes_c.data_ptr(), scales_c.data_ptr(),
                                   codes_r.data_ptr(), scales_r.data_ptr(), _stream(stream)), "lp_r128_quant_dual")
