@@ -375,13 +375,17 @@ __device__ __forceinline__ Tile grouped_dw_tile(const Params& p, const GroupScan
 // 2048 x 7168, 1024 rows 387 -> 335 us, 32768 rows 850 -> 779; their grad_X of
 // 32768 rows 606 -> 585; dense 8192 x 4096 x 4096 forward 121.8 -> 117.4,
 // grad_X 120.2 -> 115.9, grad_W 139.9 -> 134.9.
-// A grouped grad_W's tiles differ in length, and dealt ahead they end less
-// evenly than dispatched one by one; it takes turns from eight rounds on (8
-// uneven experts, four rounds: 164 us against 154).
+// A grouped grad_W's tiles differ in length, and dealt ahead (every other round in
+// reverse) they end less evenly than dispatched one by one: from eight rounds
+// on, or four when no group can have more than 32 stages.  (4096 rows, 5.5 rounds:
+// 16 even groups of 2048 x 2816 72.6 us dispatched, 58.7 in turns, 32 skewed ones of 1024 x
+// 2816 52.3, 48.2; but with 16384 rows 83.4, 100.2.  In reverse: 32 skewed groups of
+// 2048 x 4096, 16384 rows, 226 -> 216.)
 template <class C, int kOp>
 __host__ __device__ __forceinline__ bool takes_turns(const Params& p) {
   if (C::KW > 1 || C::NS > 2 || (p.offsets != nullptr && p.groups > 64)) return false;
-  return p.ntiles > (kOp == kB128Dw && p.offsets != nullptr ? 8 : 1) * kCUs;
+  const bool uneven = kOp == kB128Dw && p.offsets != nullptr;
+  return p.ntiles > (!uneven ? 1 : p.Ktot <= 32 * kRun ? 4 : 8) * kCUs;
 }
 
 // LDS of this wave written and read, and every wave here (loads into the stages
@@ -418,7 +422,7 @@ __device__ __forceinline__ void b128_tiles_of(const Params& p, uint8_t* all_smem
     if (p.offsets == nullptr) return dense_tile<C, kParts>(p, hw);
     return kDW ? grouped_dw_tile<C>(p, sc, rank, hw) : grouped_tile<C, kParts>(p, sc, hw);
   };
-  int hw = blockIdx.x;
+  int hw = blockIdx.x, round = 0;
   Tile t;
   if (kDW && p.offsets != nullptr && p.groups > 64) {
     t = select_tile<C, kDW>(p, ends);
@@ -646,7 +650,9 @@ __device__ __forceinline__ void b128_tiles_of(const Params& p, uint8_t* all_smem
       const Tile done = t;
       bool more = false;
       if (turns) {
-        hw += gridDim.x;
+        const int x = blockIdx.x & 7, j = blockIdx.x >> 3, last = (int)(gridDim.x >> 3) - 1;   // XCD, place in it
+        ++round;
+        hw = round * (int)gridDim.x + 8 * (kDW && p.offsets != nullptr && (round & 1) ? last - j : j) + x;
         more = hw < p.ntiles;
         if (more) {
           t = pick(hw);

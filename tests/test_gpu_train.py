@@ -177,7 +177,8 @@ def decoded_rows(q, ends=None):
 # at both edges) for each product in turn, then long contractions, whose last round is cut into sixteenths (forward and
 # grad_W of the first), quarters (its grad_X) and halves (forward of the second, grad_W of the third)
 DENSE = [(1, 16, 16), (3, 4112, 272), (1, 8208, 272), (2, 16400, 144), (14, 8208, 528), (9, 16400, 272), (24, 4096, 400),
-         (31, 2064, 2064), (48, 1040, 528), (64, 2048, 144), (61, 784, 4112), (1, 512, 2048), (2, 144, 128), (5, 272, 1040), (16, 4096, 512), (17, 400, 400), (33, 128, 144),
+         (31, 2064, 2064), (48, 1040, 528), (64, 2048, 144), (61, 784, 4112), (1, 512, 2048), (2, 144, 128), (5, 272, 1040),
+         (16, 4096, 512), (17, 400, 400), (33, 128, 144),
          (64, 272, 272), (65, 528, 656), (128, 128, 128), (129, 272, 400), (300, 1040, 144), (700, 512, 4112),
          (4096, 4096, 144), (4112, 4368, 272), (4112, 272, 4368), (272, 4112, 4368),
          (4112, 4096, 4112), (5000, 4112, 2064), (2064, 4112, 5120)]
@@ -273,12 +274,13 @@ def test_split_contractions(lp, M, N, K):
         assert_product(lp.lp_linear_bwd(*args, workspace=ws[:256], **kw)[at], *ref, "too small a workspace: whole")
 
 
-def test_grouped_grad_w_of_many_tiles(lp):
-    """More tiles than the workgroups side by side take in eight turns, sizes of empty, short and long groups mixed:
+@pytest.mark.parametrize("G,N,K", [(40, 1792, 1808), (20, 1792, 1920)])
+def test_grouped_grad_w_of_many_tiles(lp, G, N, K):
+    """More tiles than the workgroups side by side take in eight turns (four), sizes of empty, short and long groups mixed:
     bit for bit what the groups give in calls of a few groups (checked above)."""
     rng = np.random.default_rng(21)
-    sizes = [int(v) for v in rng.choice([0, 1, 40, 128, 129, 300], 40)]
-    M, N, K, ends = sum(sizes), 1800 // 16 * 16, 1808, ends_of(sizes)
+    sizes = [int(v) for v in rng.choice([0, 1, 40, 128, 129, 300], G)]
+    M, ends = sum(sizes), ends_of(sizes)
     xb, gb = bits(rng, (M, K)), bits(rng, (M, N), 1e-3)
 
     def grad_w(a, b, off):
@@ -286,7 +288,7 @@ def test_grouped_grad_w_of_many_tiles(lp):
         out = torch.full((off.numel(), N, K), 3.0, dtype=torch.bfloat16, device="cuda")
         return lp.lp_grouped_bwd(gr, xr, None, off, need_dx=False, grad_w=out)[1]
     whole = grad_w(0, M, dev(ends))
-    for k in range(0, 40, 4):
+    for k in range(0, G, 4):
         a = int(ends[k - 1]) if k else 0
         part = grad_w(a, int(ends[k + 3]), dev((ends[k:k + 4] - a).astype(np.int32)))
         assert torch.equal(whole[k:k + 4], part), k
