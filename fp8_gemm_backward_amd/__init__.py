@@ -93,7 +93,8 @@ _CODE_BITS = {"bf16": 16, "mxfp4": 4, "nvfp4": 4, "fp8_b128": 8, "mxfp8": 8, "fp
 _NAMES = {f: (f"{f} codes", f"{f} scales", f"{f} tensor scale") for f in FMT}
 
 
-def _scale_bytes(fmt: str, axis: int, b: int, r: int, c: int) -> int:
+def _scale_bytes(fmt: str, axis: int, b: int, r: int, c: int, groups: int = 0) -> int:
+    """Bytes of scales that a call reads, over `groups` groups of rows (0: a call without offsets)."""
     """Bytes of a tensor's block scales (include/lp.h, formats)."""
     if fmt == "mxfp4" or (fmt == "mxfp8" and axis == -1):
         return b * r * (c // 32)
@@ -104,7 +105,10 @@ def _scale_bytes(fmt: str, axis: int, b: int, r: int, c: int) -> int:
     if fmt == "fp8_b128":
         return b * (-(-r // 128)) * (-(-c // 128)) * 4
     if fmt == "fp8_r128":
-        return 4 * (b * (-(-c // 128)) * r if axis == -1 else b * (-(-r // 128)) * c)
+        if axis == -1:
+            return 4 * b * (-(-c // 128)) * r
+        # Runs that restart at every group: group g's begin at its first row / 128 + g.
+        return 4 * b * (r // 128 + groups if groups > 1 else -(-r // 128)) * c
     return 0
 
 
@@ -169,12 +173,13 @@ class QTensor:
     def cols(self) -> int:
         return self.shape[2]
 
-    def c(self) -> _QTensorC:
+    def c(self, groups: int = 0) -> _QTensorC:
+        """The C descriptor, for a call over `groups` groups of rows (0: without offsets)."""
         b, r, c = self.shape
         n = b * r * c
         fmt, codes, scales, ts = self.fmt, self.codes, self.scales, self.tensor_scale
         _device(codes, _NAMES[fmt][0], n * _CODE_BITS[fmt] // 8)
-        _device(scales, _NAMES[fmt][1], _scale_bytes(fmt, self.axis, b, r, c))
+        _device(scales, _NAMES[fmt][1], _scale_bytes(fmt, self.axis, b, r, c, groups))
         if fmt in ("nvfp4", "fp8t_e4m3", "fp8t_e5m2"):
             _device(ts, _NAMES[fmt][2], 4 if n else 0, torch.float32)
         return _QTensorC(FMT[fmt], self.axis, b, r, c, None if codes is None else codes.data_ptr(),
@@ -425,7 +430,8 @@ def lp_grouped_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor]
                    need_dx: bool = True, need_dw: bool = True, grad_x: Optional[torch.Tensor] = None,
                    grad_w: Optional[torch.Tensor] = None, stream=None):
     """(grad_X [M,K] or None, grad_W [G,N,K] or None) of a grouped matmul.
-    Rows of grad_X at or past offsets[-1] are left as they were in `grad_x`."""
+    Rows of grad_X at or past offsets[-1] are left as they were in `grad_x`.  "fp8_r128" operands along -2: as
+    lp_r128_quant with these offsets makes them."""
     _, M, N = grad_out.shape
     G = offsets.numel()
     K = (w if need_dx else x).cols
@@ -441,8 +447,8 @@ def lp_grouped_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor]
         else:
             _device(grad_w, "grad_w", 2 * G * N * K)
     _device(offsets, "offsets", 4 * G, torch.int32)
-    g = grad_out.c()
-    xc = x.c() if x is not None else None
+    g = grad_out.c(G)
+    xc = x.c(G) if x is not None else None
     wc = w.c() if w is not None else None
     st = lib.lp_grouped_bwd(ctypes.byref(g), ctypes.byref(xc) if xc else None, ctypes.byref(wc) if wc else None,
                             offsets.data_ptr(), G, grad_x.data_ptr() if need_dx else None,
