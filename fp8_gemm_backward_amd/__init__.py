@@ -148,7 +148,10 @@ class QTensor:
     codes: bf16 values (fmt "bf16"), uint8 E4M3 codes, or uint8 packed E2M1
     pairs; scales: uint8 E8M0 / E4M3 bytes or float32 block scales; for
     NVFP4 and the per-tensor FP8 formats `tensor_scale` is a one-element
-    float32 device tensor.
+    float32 device tensor.  run_groups: for "fp8_r128" along -2, the number of
+    groups at whose first rows the runs restart (0: none do), as the
+    quantizers set it; calls that would look for the runs elsewhere refuse the
+    tensor.  None: not known, and not checked.
     """
     fmt: str
     codes: torch.Tensor
@@ -156,6 +159,7 @@ class QTensor:
     tensor_scale: Optional[torch.Tensor] = None
     shape: tuple = ()
     axis: int = -1
+    run_groups: Optional[int] = None
 
     def __post_init__(self):
         if not self.shape:
@@ -178,6 +182,9 @@ class QTensor:
         b, r, c = self.shape
         n = b * r * c
         fmt, codes, scales, ts = self.fmt, self.codes, self.scales, self.tensor_scale
+        made = self.run_groups                               # (one group: the layout without offsets)
+        if made is not None and made != groups and (made > 1 or groups > 1):
+            raise ValueError(f"{fmt} runs made for {made} groups, the call has {groups} (0: no offsets)")
         _device(codes, _NAMES[fmt][0], n * _CODE_BITS[fmt] // 8)
         _device(scales, _NAMES[fmt][1], _scale_bytes(fmt, self.axis, b, r, c, groups))
         if fmt in ("nvfp4", "fp8t_e4m3", "fp8t_e5m2"):
@@ -199,7 +206,8 @@ def _check(st: int, where: str):
 
 
 def lp_dequant(src: QTensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Decode `src` to bf16 [batch, rows, cols] (bit-exact)."""
+    """Decode `src` to bf16 [batch, rows, cols] (bit-exact); not "fp8_r128"
+    whose runs restart at groups."""
     if out is None:
         out = torch.empty(src.shape, dtype=torch.bfloat16, device=src.codes.device)
     q = src.c()
@@ -515,7 +523,7 @@ def lp_r128_quant(src: torch.Tensor, axis: int = -1, offsets: Optional[torch.Ten
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
     _check(lib.lp_r128_quant(src.data_ptr(), b, r, c, axis, *_offsets(offsets), codes.data_ptr(), scales.data_ptr(),
                              _stream(stream)), "lp_r128_quant")
-    return QTensor("fp8_r128", codes, scales, None, shape, axis)
+    return QTensor("fp8_r128", codes, scales, None, shape, axis, _offsets(offsets)[1] if axis == -2 else None)
 
 
 def lp_r128_quant_dual(src: torch.Tensor, offsets: Optional[torch.Tensor] = None, stream=None) -> tuple:
@@ -524,13 +532,14 @@ def lp_r128_quant_dual(src: torch.Tensor, offsets: Optional[torch.Tensor] = None
     the last offset are left unwritten in both."""
     b, r, c = shape = _shape3(src)
     codes_c = src.new_empty(shape, dtype=torch.uint8)
-    codes_r = torch.empty_like(codes_c)
+    codes_r = src.new_empty(shape, dtype=torch.uint8)
     scales_c = src.new_empty((b, -(-c // 128), r), dtype=torch.float32)
     scales_r = src.new_empty((b, _runs(r, offsets), c), dtype=torch.float32)
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
     _check(lib.lp_r128_quant_dual(src.data_ptr(), b, r, c, *_offsets(offsets), codes_c.data_ptr(), scales_c.data_ptr(),
                                   codes_r.data_ptr(), scales_r.data_ptr(), _stream(stream)), "lp_r128_quant_dual")
-    return QTensor("fp8_r128", codes_c, scales_c, None, shape, -1), QTensor("fp8_r128", codes_r, scales_r, None, shape, -2)
+    return (QTensor("fp8_r128", codes_c, scales_c, None, shape, -1),
+            QTensor("fp8_r128", codes_r, scales_r, None, shape, -2, _offsets(offsets)[1]))
 
 
 def lp_b128_quant(src: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,

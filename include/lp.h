@@ -77,6 +77,10 @@
  *                -1 -> scales[batch][ceil(cols/128)][rows],
  *                -2 -> scales[batch][ceil(rows/128)][cols]
  *                (the product reads one run's scales of many rows at a time).
+ *                Calls with group offsets take an axis -2 tensor whose runs
+ *                restart at the groups, in a longer array (lp_r128_quant);
+ *                lp_dequant and calls without offsets take it in the layout
+ *                above only, and a descriptor does not say which one it is.
  *                rows < 2^29.
  *                The activations and gradients that go with an LP_FP8_B128
  *                weight in FP8 products (lp_train.h has the quantizers).

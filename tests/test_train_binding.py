@@ -83,3 +83,48 @@ def test_grouped_grad_w_needs_scales_of_every_run(calls, rows, groups, runs, ok,
         with pytest.raises(ValueError, match="scales"):
             call()
         assert not calls
+
+
+# ---------------------------------------------------------------- which groups a token-run tensor was made for
+
+def test_quantizers_note_the_groups(calls):
+    src = DeviceTensor((300, 256), torch.bfloat16)
+    assert lp.lp_r128_quant(src, -2).run_groups == 0 and lp.lp_r128_quant(src, -2, offsets(5)).run_groups == 5
+    assert lp.lp_r128_quant(src, -1).run_groups is None
+    for off, n in ((None, 0), (offsets(7), 7)):
+        cols, rows = lp.lp_r128_quant_dual(src, off)
+        assert cols.run_groups is None and rows.run_groups == n
+
+
+@pytest.mark.parametrize("made_for,ok", [(None, True), (0, True), (1, True), (2, False), (5, False)])
+def test_calls_without_offsets_refuse_runs_of_groups(calls, made_for, ok):
+    """The dense calls find a row's run at row / 128; runs that restart at a group's first row are elsewhere."""
+    def q():
+        return runs_tensor(300, 256, 3 + 5, run_groups=made_for)
+    out = DeviceTensor((300, 256), torch.bfloat16)
+    for call in (lambda: lp.lp_dequant(q(), out), lambda: lp.lp_linear_bwd(q(), runs_tensor(300, 256, 3), None, need_dx=False),
+                 lambda: lp.lp_linear_bwd(runs_tensor(300, 256, 3), q(), None, need_dx=False)):
+        calls.clear()
+        if ok:
+            call()
+            assert len(calls) == 1
+        else:
+            with pytest.raises(ValueError, match="groups"):
+                call()
+            assert not calls
+
+
+@pytest.mark.parametrize("made_for,groups,ok", [(None, 4, True), (4, 4, True), (3, 4, False), (5, 4, False), (0, 4, False),
+                                                (1, 4, False), (0, 1, True), (1, 1, True), (None, 1, True), (2, 1, False)])
+def test_grouped_grad_w_refuses_runs_of_other_groups(calls, made_for, groups, ok):
+    for k in range(2):
+        ops = [runs_tensor(300, 256, 9), runs_tensor(300, 256, 9)]
+        ops[k].run_groups = made_for
+        calls.clear()
+        if ok:
+            lp.lp_grouped_bwd(*ops, None, offsets(groups), need_dx=False)
+            assert len(calls) == 1
+        else:
+            with pytest.raises(ValueError, match="groups"):
+                lp.lp_grouped_bwd(*ops, None, offsets(groups), need_dx=False)
+            assert not calls
