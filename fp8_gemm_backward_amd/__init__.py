@@ -510,7 +510,11 @@ def _runs(rows: int, offsets: Optional[torch.Tensor]) -> int:
 
 
 def _offsets(offsets: Optional[torch.Tensor]) -> tuple:
-    return (None, 0) if offsets is None else (offsets.data_ptr(), offsets.numel())
+    if offsets is None:
+        return None, 0
+    if offsets.numel() == 0:                                 # its null address would mean no offsets
+        raise LpError(2, "offsets of no group")
+    return offsets.data_ptr(), offsets.numel()
 
 
 def lp_r128_quant(src: torch.Tensor, axis: int = -1, offsets: Optional[torch.Tensor] = None, stream=None) -> QTensor:

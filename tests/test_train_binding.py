@@ -128,3 +128,21 @@ def test_grouped_grad_w_refuses_runs_of_other_groups(calls, made_for, groups, ok
             with pytest.raises(ValueError, match="groups"):
                 lp.lp_grouped_bwd(*ops, None, offsets(groups), need_dx=False)
             assert not calls
+
+
+@pytest.mark.parametrize("ptr", [0, FAKE])
+def test_quantizers_refuse_offsets_of_no_group(monkeypatch, ptr):
+    """An empty offsets tensor has a null address, with which the C call would quantize without groups: into scales of
+    rows // 128 runs, one too few."""
+    made = []
+    for name in ("lp_r128_quant", "lp_r128_quant_dual"):
+        monkeypatch.setattr(lp.lib, name, lambda *a: made.append(a) or 0)
+    monkeypatch.setattr(lp, "_stream", lambda s: 0)
+    none = offsets(0)
+    monkeypatch.setattr(none, "data_ptr", lambda: ptr, raising=False)
+    src = DeviceTensor((300, 256), torch.bfloat16)
+    for call in (lambda: lp.lp_r128_quant(src, -2, none), lambda: lp.lp_r128_quant_dual(src, none)):
+        with pytest.raises(lp.LpError) as e:
+            call()
+        assert e.value.status == 2
+    assert not made
