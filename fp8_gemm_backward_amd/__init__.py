@@ -684,7 +684,8 @@ class AdamWPlan:
         if self._chunks:
             table = torch.empty(-(-nbytes.value // 8), dtype=torch.int64)
             _check(lib.lp_adamw_plan(*args, table.data_ptr(), ctypes.byref(nbytes), ctypes.byref(chunks)), "lp_adamw_plan")
-            self._table, self._home = table.to(self._kept[0][0].device), _stream(None)
+            device = next(p.device for p, n in zip(self._kept[0], self._n) if n)
+            self._table, self._home = table.to(device), _stream(None)
 
 
 _ADAMW_DTYPE = {torch.float32: 0, torch.bfloat16: 1}

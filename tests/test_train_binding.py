@@ -146,3 +146,17 @@ def test_quantizers_refuse_offsets_of_no_group(monkeypatch, ptr):
             call()
         assert e.value.status == 2
     assert not made
+
+
+# ---------------------------------------------------------------- AdamW
+
+def adamw_lists(*params):
+    return [list(params)] + [[DeviceTensor(p.shape, torch.float32) for p in params] for _ in range(3)]
+
+
+def test_adamw_table_goes_where_the_parameters_are(calls):
+    """An empty parameter may be anywhere (it is not touched); the table may not."""
+    p = DeviceTensor((300,), torch.float32)
+    for params in ([p], [torch.zeros(0), p], [p, torch.zeros(0)]):
+        assert lp.AdamWPlan(*adamw_lists(*params))._table.device == p.device
+    assert lp.AdamWPlan(*adamw_lists(torch.zeros(0)))._table is None
