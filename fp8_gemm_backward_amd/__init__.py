@@ -200,6 +200,19 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
+def _torch_stream(stream):
+    """The torch stream of a stream argument (a torch stream, or a raw handle)."""
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+
+
+def _capturing(stream) -> bool:
+    """Whether what is enqueued on the stream goes into a graph."""
+    if stream is None or _stream(stream) == _stream(None):
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(_torch_stream(stream)):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _check(st: int, where: str):
     if st != 0:
         raise LpError(st, where)
@@ -622,8 +635,12 @@ class AdamWPlan:
     the new float32 parameters.  weight_decay, lr_scale: one number or one
     per tensor.  The plan keeps the tensors alive and holds the device table
     that the step reads; set_grads makes a new one, so gradients that stay
-    where they are from step to step are the cheaper way, and set_grads
-    cannot be captured into a graph (the step can)."""
+    where they are from step to step are the cheaper way.
+
+    A step can be captured into a graph, set_grads cannot.  The graph steps
+    with the gradients, and the step number, of its capture whatever set_grads
+    does later; the plan keeps the table and the gradients of captured steps,
+    and has to live as long as the graph."""
 
     def __init__(self, params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales=None, exp_avg_sq_scales=None, copies=None,
                  weight_decay=0.0, lr_scale=1.0):
@@ -639,6 +656,7 @@ class AdamWPlan:
         self.param_dtype = params[0].dtype if k else torch.float32
         self._n = [p.numel() for p in params]
         self._c = (_AdamWTensorC * max(k, 1))()
+        self._table, self._in_graph, self._of_graphs = None, False, []
         self._kept = [list(params), list(exp_avgs), list(exp_avg_sqs)] + [list(v) for v in (exp_avg_scales, exp_avg_sq_scales, copies) if v is not None]
         if self.param_dtype not in _ADAMW_DTYPE:
             raise ValueError(f"parameters must be float32 or bfloat16, not {self.param_dtype}")
@@ -676,6 +694,9 @@ class AdamWPlan:
         if dtype not in _ADAMW_DTYPE:
             raise ValueError(f"gradients must be float32 or bfloat16, not {dtype}")
         self._pointers("grad", grads, "grads", self._n, dtype)
+        if self._in_graph:
+            self._of_graphs.append((self._table, self._grads))
+            self._in_graph = False
         self.grad_dtype, self._grads = dtype, list(grads)
         nbytes, chunks = ctypes.c_size_t(0), ctypes.c_int64(0)
         args = (self._c, len(self._n), _ADAMW_DTYPE[self.param_dtype], _ADAMW_DTYPE[dtype], int(self.bits8))
@@ -698,6 +719,8 @@ def lp_adamw(plan: AdamWPlan, lr: float, beta1: float = 0.9, beta2: float = 0.99
     if grad_scale is not None:
         _device(grad_scale, "grad_scale", 4, torch.float32)
     t, s = plan._table, _stream(stream)
+    if t is not None and not plan._in_graph:
+        plan._in_graph = _capturing(stream)
     if t is not None and s != plan._home:        # not to be reused before that stream is done with it
         t.record_stream(torch.cuda.ExternalStream(s))
     _check(lib.lp_adamw(None if t is None else t.data_ptr(), len(plan._n), plan._chunks, _ADAMW_DTYPE[plan.param_dtype],

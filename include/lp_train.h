@@ -116,7 +116,8 @@ lp_status lp_grouped_fwd_dyn(const void* x_bf16, int64_t M, const lp_qtensor* w,
  * lp_adamw_plan writes the table that lp_adamw reads: which tensors, and which
  * part of them each workgroup takes.  It runs on the host and touches no GPU.
  * The caller copies the table to device memory once and keeps it (and the
- * tensors) as long as it steps with it; a plan is made anew when a tensor moves.
+ * tensors) as long as it steps with it, or replays a graph that captured a step
+ * with it; a plan is made anew when a tensor moves.
  *
  * tensors      HOST array of `count`, not kept.  Pointers need the alignment of
  *              their element only; tensors whose pointers are all aligned to

@@ -1,7 +1,8 @@
 """The binding's own checks of the block-scaled FP8 training calls, with
 stand-ins for device tensors and for the C functions (CPU only; no kernel is
 launched)."""
-import ctypes
+import gc
+import weakref
 
 import pytest
 import torch
@@ -160,3 +161,23 @@ def test_adamw_table_goes_where_the_parameters_are(calls):
     for params in ([p], [torch.zeros(0), p], [p, torch.zeros(0)]):
         assert lp.AdamWPlan(*adamw_lists(*params))._table.device == p.device
     assert lp.AdamWPlan(*adamw_lists(torch.zeros(0)))._table is None
+
+
+@pytest.mark.parametrize("captured", [True, False])
+def test_adamw_keeps_what_a_captured_step_reads(calls, monkeypatch, captured):
+    """A graph that holds a step reads that step's table, and through it the gradients, at every replay: set_grads must
+    not free them."""
+    capturing = captured
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    lists = adamw_lists(DeviceTensor((300,), torch.float32))
+    first = weakref.ref(lists[1][0])
+    plan = lp.AdamWPlan(*lists)
+    lists[1] = None
+    table = weakref.ref(plan._table)
+    lp.lp_adamw(plan, lr=0.1)
+    capturing = False
+    for _ in range(3):
+        plan.set_grads([DeviceTensor((300,), torch.float32)])
+        lp.lp_adamw(plan, lr=0.1)
+    gc.collect()
+    assert (table() is not None) == (first() is not None) == captured
