@@ -202,7 +202,11 @@ def _stream(stream) -> Optional[int]:
 
 def _torch_stream(stream):
     """The torch stream of a stream argument (a torch stream, or a raw handle)."""
-    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream(stream)
+    # (ExternalStream(0) is a stream of torch's pool)
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
 
 
 def _capturing(stream) -> bool:
@@ -364,7 +368,7 @@ def lp_linear_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor],
             if nbytes.value:
                 workspace = torch.empty(nbytes.value, dtype=torch.uint8, device=codes.device)
                 if stream is not None:
-                    workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream))
+                    workspace.record_stream(_torch_stream(stream))
     if workspace is None:
         st = lib.lp_linear_bwd(*args, _stream(stream))
         _check(st, "lp_linear_bwd")
@@ -592,7 +596,7 @@ def _fwd_dyn(x: torch.Tensor, w: QTensor, offsets: Optional[torch.Tensor], y: Op
         at = -(-4 * nb * M // 16) * 16                       # scratch: scales, then (16-byte aligned) codes
         scratch = torch.empty(at + M * K, dtype=torch.uint8, device=x.device)
         if stream is not None:                               # not to be reused before that stream is done with it
-            scratch.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream))
+            scratch.record_stream(_torch_stream(stream))
         scales = scratch.data_ptr()
         codes = scales + at
     args = (codes, scales, y.data_ptr(), _stream(stream))
@@ -722,7 +726,7 @@ def lp_adamw(plan: AdamWPlan, lr: float, beta1: float = 0.9, beta2: float = 0.99
     if t is not None and not plan._in_graph:
         plan._in_graph = _capturing(stream)
     if t is not None and s != plan._home:        # not to be reused before that stream is done with it
-        t.record_stream(torch.cuda.ExternalStream(s))
+        t.record_stream(_torch_stream(s))
     _check(lib.lp_adamw(None if t is None else t.data_ptr(), len(plan._n), plan._chunks, _ADAMW_DTYPE[plan.param_dtype],
                         _ADAMW_DTYPE[plan.grad_dtype], int(plan.bits8), lr, beta1, beta2, eps, step,
                         None if grad_scale is None else grad_scale.data_ptr(), s), "lp_adamw")
