@@ -3,6 +3,9 @@
 A thin Python binding over the C-ABI library `liblp.so` (declared in
 `include/lp.h`).  The functions below keep the C names; they only marshal
 torch tensors (device memory) and the current HIP stream into the C calls.
+With stream= (a torch stream or a raw handle) a call runs on that stream, and
+what it allocates comes from that stream's memory; the caller orders his own
+tensors, the results among them, between the streams.
 Every step of the computation runs in the library's HIP kernels; there is no
 fallback, and importing this package fails if the library is not built
 (`python fp8_gemm_backward_amd/build.py`).
@@ -209,6 +212,21 @@ def _torch_stream(stream):
     return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
 
 
+def _new(like: torch.Tensor, shape, dtype, stream, result: bool = True) -> torch.Tensor:
+    """A tensor on like's device for a call on `stream` to write.  On another
+    stream than the current one it is taken from that stream's memory: a block
+    of the current stream's may still be used by work enqueued there before
+    it was freed, which the call does not wait for.  result: returned to the
+    caller, who uses it on the current stream."""
+    if stream is None or not like.is_cuda or _stream(stream) == _stream(None):
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(_torch_stream(stream)):
+        t = like.new_empty(shape, dtype=dtype)
+    if result:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _capturing(stream) -> bool:
     """Whether what is enqueued on the stream goes into a graph."""
     if stream is None or _stream(stream) == _stream(None):
@@ -226,7 +244,7 @@ def lp_dequant(src: QTensor, out: Optional[torch.Tensor] = None, stream=None) ->
     """Decode `src` to bf16 [batch, rows, cols] (bit-exact); not "fp8_r128"
     whose runs restart at groups."""
     if out is None:
-        out = torch.empty(src.shape, dtype=torch.bfloat16, device=src.codes.device)
+        out = _new(src.codes, src.shape, torch.bfloat16, stream)
     q = src.c()
     _device(out, "out", 2 * src.shape[0] * src.shape[1] * src.shape[2])
     _check(lib.lp_dequant(ctypes.byref(q), out.data_ptr(), _stream(stream)), "lp_dequant")
@@ -239,12 +257,11 @@ def lp_mx_quant(src: torch.Tensor, axis: int, fmt: str = "mxfp8", codes: Optiona
     `axis` (-1 or -2) to "mxfp8" or "mxfp4"."""
     shape = tuple(src.shape) if src.dim() == 3 else (1,) + tuple(src.shape)
     b, r, c = shape
-    dev = src.device
     if codes is None:
-        codes = torch.empty((b, r, c if fmt == "mxfp8" else c // 2), dtype=torch.uint8, device=dev)
+        codes = _new(src, (b, r, c if fmt == "mxfp8" else c // 2), torch.uint8, stream)
     if scales is None:
         sshape = (b, r, c // 32) if axis == -1 else (b, r // 32, c)
-        scales = torch.empty(sshape, dtype=torch.uint8, device=dev)
+        scales = _new(src, sshape, torch.uint8, stream)
     n = b * r * c
     _device(src, "src", 2 * n, torch.bfloat16)
     _device(codes, "codes", n if fmt == "mxfp8" else n // 2)
@@ -259,13 +276,12 @@ def lp_mx_quant_dual(src: torch.Tensor, fmt: str = "mxfp8", stream=None) -> tupl
     both axes in one pass: (copy scaled along -1, copy scaled along -2)."""
     shape = tuple(src.shape) if src.dim() == 3 else (1,) + tuple(src.shape)
     b, r, c = shape
-    dev = src.device
     cb = c if fmt == "mxfp8" else c // 2
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
-    codes_c = torch.empty((b, r, cb), dtype=torch.uint8, device=dev)
-    scales_c = torch.empty((b, r, c // 32), dtype=torch.uint8, device=dev)
-    codes_r = torch.empty((b, r, cb), dtype=torch.uint8, device=dev)
-    scales_r = torch.empty((b, r // 32, c), dtype=torch.uint8, device=dev)
+    codes_c = _new(src, (b, r, cb), torch.uint8, stream)
+    scales_c = _new(src, (b, r, c // 32), torch.uint8, stream)
+    codes_r = _new(src, (b, r, cb), torch.uint8, stream)
+    scales_r = _new(src, (b, r // 32, c), torch.uint8, stream)
     _check(lib.lp_mx_quant_dual(src.data_ptr(), b, r, c, FMT[fmt], codes_c.data_ptr(), scales_c.data_ptr(),
                                 codes_r.data_ptr(), scales_r.data_ptr(), _stream(stream)), "lp_mx_quant_dual")
     return QTensor(fmt, codes_c, scales_c, None, shape, -1), QTensor(fmt, codes_r, scales_r, None, shape, -2)
@@ -275,7 +291,7 @@ def lp_tensor_amax(src: torch.Tensor, amax: Optional[torch.Tensor] = None, strea
     """max |x| of a bf16 tensor into a float32 device scalar (`amax` may be a
     one-element view into an amax history)."""
     if amax is None:
-        amax = torch.empty(1, dtype=torch.float32, device=src.device)
+        amax = _new(src, 1, torch.float32, stream)
     _device(src, "src", 2 * src.numel(), torch.bfloat16)
     _device(amax, "amax", 4, torch.float32)
     _check(lib.lp_tensor_amax(src.data_ptr(), src.numel(), amax.data_ptr(), _stream(stream)), "lp_tensor_amax")
@@ -289,7 +305,7 @@ def lp_tensor_quant(src: torch.Tensor, fmt: str, scale: torch.Tensor, amax: Opti
     scalar `scale`; the input's amax goes to `amax` when given."""
     shape = tuple(src.shape) if src.dim() == 3 else (1,) + tuple(src.shape)
     if codes is None:
-        codes = torch.empty(shape, dtype=torch.uint8, device=src.device)
+        codes = _new(src, shape, torch.uint8, stream)
     _device(src, "src", 2 * src.numel(), torch.bfloat16)
     _device(codes, "codes", src.numel())
     _device(scale, "scale", 4, torch.float32)
@@ -307,9 +323,9 @@ def lp_tensor_quant_delayed(src: torch.Tensor, fmt: str, history: torch.Tensor, 
     ring), quantization with it, the input's amax into history[slot]."""
     shape = tuple(src.shape) if src.dim() == 3 else (1,) + tuple(src.shape)
     if codes is None:
-        codes = torch.empty(shape, dtype=torch.uint8, device=src.device)
+        codes = _new(src, shape, torch.uint8, stream)
     if scale is None:
-        scale = torch.empty(1, dtype=torch.float32, device=src.device)
+        scale = _new(src, 1, torch.float32, stream)
     _device(src, "src", 2 * src.numel(), torch.bfloat16)
     _device(codes, "codes", src.numel())
     _device(history, "history", 4 * max(history.numel(), 1), torch.float32)
@@ -324,7 +340,7 @@ def lp_scale_from_history(history: torch.Tensor, fmt: str, margin: int = 0, scal
                           stream=None) -> torch.Tensor:
     """Per-tensor scale (float32 device scalar) from a float32 amax history."""
     if scale is None:
-        scale = torch.empty(1, dtype=torch.float32, device=history.device)
+        scale = _new(history, 1, torch.float32, stream)
     _device(history, "history", 4 * max(history.numel(), 1), torch.float32)
     _device(scale, "scale", 4, torch.float32)
     _check(lib.lp_scale_from_history(history.data_ptr(), history.numel(), FMT[fmt], margin, scale.data_ptr(),
@@ -345,12 +361,12 @@ def lp_linear_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor],
     codes = grad_out.codes
     if need_dx:
         if grad_x is None:
-            grad_x = codes.new_empty((M, K), dtype=torch.bfloat16)
+            grad_x = _new(codes, (M, K), torch.bfloat16, stream)
         else:
             _device(grad_x, "grad_x", 2 * M * K)
     if need_dw:
         if grad_w is None:
-            grad_w = codes.new_empty((N, K), dtype=torch.bfloat16)
+            grad_w = _new(codes, (N, K), torch.bfloat16, stream)
         else:
             _device(grad_w, "grad_w", 2 * N * K)
     if workspace is not None:
@@ -366,9 +382,7 @@ def lp_linear_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor],
             nbytes = ctypes.c_size_t(0)
             _check(lib.lp_linear_bwd_workspace(*args, ctypes.byref(nbytes)), "lp_linear_bwd_workspace")
             if nbytes.value:
-                workspace = torch.empty(nbytes.value, dtype=torch.uint8, device=codes.device)
-                if stream is not None:
-                    workspace.record_stream(_torch_stream(stream))
+                workspace = _new(codes, nbytes.value, torch.uint8, stream, result=False)
     if workspace is None:
         st = lib.lp_linear_bwd(*args, _stream(stream))
         _check(st, "lp_linear_bwd")
@@ -387,11 +401,10 @@ def lp_linear_bwd_noalloc(grad_out: QTensor, x: Optional[QTensor], w: Optional[Q
     given)."""
     M, N = grad_out.rows, grad_out.cols
     K = (w if need_dx else x).cols
-    dev = grad_out.codes.device
     if need_dx and grad_x is None:
-        grad_x = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        grad_x = _new(grad_out.codes, (M, K), torch.bfloat16, stream)
     if need_dw and grad_w is None:
-        grad_w = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+        grad_w = _new(grad_out.codes, (N, K), torch.bfloat16, stream)
     if need_dx:
         _device(grad_x, "grad_x", 2 * M * K)
     if need_dw:
@@ -416,14 +429,13 @@ def lp_grouped_dx_deferred(grad_out: QTensor, w: torch.Tensor, offsets: torch.Te
     here when not given and fuse_rows < M."""
     G, N, K = w.shape
     M = grad_out.rows
-    dev = grad_out.codes.device
     if grad_x is None:
-        grad_x = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        grad_x = _new(grad_out.codes, (M, K), torch.bfloat16, stream)
     if fuse_rows < M or N % 512 or K % 32:
         if w_codes is None:
-            w_codes = torch.empty((G, N, K), dtype=torch.uint8, device=dev)
+            w_codes = _new(w, (G, N, K), torch.uint8, stream, result=False)
         if w_scales is None:
-            w_scales = torch.empty((G, N // 32, K), dtype=torch.uint8, device=dev)
+            w_scales = _new(w, (G, N // 32, K), torch.uint8, stream, result=False)
         _device(w_codes, "w_codes", G * N * K)
         _device(w_scales, "w_scales", G * (N // 32) * K)
     _device(w, "w", 2 * G * N * K, torch.bfloat16)
@@ -463,12 +475,12 @@ def lp_grouped_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor]
     codes = grad_out.codes
     if need_dx:
         if grad_x is None:
-            grad_x = codes.new_empty((M, K), dtype=torch.bfloat16)
+            grad_x = _new(codes, (M, K), torch.bfloat16, stream)
         else:
             _device(grad_x, "grad_x", 2 * M * K)
     if need_dw:
         if grad_w is None:
-            grad_w = codes.new_empty((G, N, K), dtype=torch.bfloat16)
+            grad_w = _new(codes, (G, N, K), torch.bfloat16, stream)
         else:
             _device(grad_w, "grad_w", 2 * G * N * K)
     _device(offsets, "offsets", 4 * G, torch.int32)
@@ -487,7 +499,7 @@ def lp_linear_fwd(x: QTensor, w: QTensor, y: Optional[torch.Tensor] = None, stre
     both "nvfp4", a "bf16" x with a "bf16", "fp8_b128" or "nvfp4" weight, or
     an "fp8_r128" x (along -1) with an "fp8_b128" weight."""
     if y is None:
-        y = torch.empty((x.rows, w.rows), dtype=torch.bfloat16, device=x.codes.device)
+        y = _new(x.codes, (x.rows, w.rows), torch.bfloat16, stream)
     _device(y, "y", 2 * x.rows * w.rows)
     xc, wc = x.c(), w.c()
     _check(lib.lp_linear_fwd(ctypes.byref(xc), ctypes.byref(wc), y.data_ptr(), _stream(stream)), "lp_linear_fwd")
@@ -499,7 +511,7 @@ def lp_grouped_fwd(x: QTensor, w: QTensor, offsets: torch.Tensor, y: Optional[to
     """y [M, N]: rows of group g are x[rows] @ w[g]^T; rows at or past
     offsets[-1] are left as they were in `y`."""
     if y is None:
-        y = torch.empty((x.rows, w.rows), dtype=torch.bfloat16, device=x.codes.device)
+        y = _new(x.codes, (x.rows, w.rows), torch.bfloat16, stream)
     _device(y, "y", 2 * x.rows * w.rows)
     _device(offsets, "offsets", 4 * offsets.numel(), torch.int32)
     xc, wc = x.c(), w.c()
@@ -539,8 +551,8 @@ def lp_r128_quant(src: torch.Tensor, axis: int = -1, offsets: Optional[torch.Ten
     "fp8_r128" along `axis` (-1 or -2).  offsets (axis -2): int32 cumulative
     group ends; runs restart at every group's first row."""
     b, r, c = shape = _shape3(src)
-    codes = src.new_empty(shape, dtype=torch.uint8)
-    scales = src.new_empty((b, -(-c // 128), r) if axis == -1 else (b, _runs(r, offsets), c), dtype=torch.float32)
+    codes = _new(src, shape, torch.uint8, stream)
+    scales = _new(src, (b, -(-c // 128), r) if axis == -1 else (b, _runs(r, offsets), c), torch.float32, stream)
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
     _check(lib.lp_r128_quant(src.data_ptr(), b, r, c, axis, *_offsets(offsets), codes.data_ptr(), scales.data_ptr(),
                              _stream(stream)), "lp_r128_quant")
@@ -552,10 +564,10 @@ def lp_r128_quant_dual(src: torch.Tensor, offsets: Optional[torch.Tensor] = None
     -2); the second one's runs restart at each group of `offsets`.  Rows past
     the last offset are left unwritten in both."""
     b, r, c = shape = _shape3(src)
-    codes_c = src.new_empty(shape, dtype=torch.uint8)
-    codes_r = src.new_empty(shape, dtype=torch.uint8)
-    scales_c = src.new_empty((b, -(-c // 128), r), dtype=torch.float32)
-    scales_r = src.new_empty((b, _runs(r, offsets), c), dtype=torch.float32)
+    codes_c = _new(src, shape, torch.uint8, stream)
+    codes_r = _new(src, shape, torch.uint8, stream)
+    scales_c = _new(src, (b, -(-c // 128), r), torch.float32, stream)
+    scales_r = _new(src, (b, _runs(r, offsets), c), torch.float32, stream)
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
     _check(lib.lp_r128_quant_dual(src.data_ptr(), b, r, c, *_offsets(offsets), codes_c.data_ptr(), scales_c.data_ptr(),
                                   codes_r.data_ptr(), scales_r.data_ptr(), _stream(stream)), "lp_r128_quant_dual")
@@ -569,9 +581,9 @@ def lp_b128_quant(src: torch.Tensor, codes: Optional[torch.Tensor] = None, scale
     "fp8_b128" (into `codes` and `scales` when given)."""
     b, r, c = shape = _shape3(src)
     if codes is None:
-        codes = torch.empty(shape, dtype=torch.uint8, device=src.device)
+        codes = _new(src, shape, torch.uint8, stream)
     if scales is None:
-        scales = torch.empty((b, -(-r // 128), -(-c // 128)), dtype=torch.float32, device=src.device)
+        scales = _new(src, (b, -(-r // 128), -(-c // 128)), torch.float32, stream)
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
     _device(codes, "codes", b * r * c)
     _device(scales, "scales", _scale_bytes("fp8_b128", -1, b, r, c), torch.float32)
@@ -586,7 +598,7 @@ def _fwd_dyn(x: torch.Tensor, w: QTensor, offsets: Optional[torch.Tensor], y: Op
         raise ValueError(f"x has {K} columns, the weight {w.cols}")
     _device(x, "x", 2 * M * K, torch.bfloat16)
     if y is None:
-        y = x.new_empty((M, w.rows), dtype=torch.bfloat16)
+        y = _new(x, (M, w.rows), torch.bfloat16, stream)
     else:
         _device(y, "y", 2 * M * w.rows)
     nb = -(-K // 128)
@@ -594,9 +606,7 @@ def _fwd_dyn(x: torch.Tensor, w: QTensor, offsets: Optional[torch.Tensor], y: Op
         codes = scales = None
     else:
         at = -(-4 * nb * M // 16) * 16                       # scratch: scales, then (16-byte aligned) codes
-        scratch = torch.empty(at + M * K, dtype=torch.uint8, device=x.device)
-        if stream is not None:                               # not to be reused before that stream is done with it
-            scratch.record_stream(_torch_stream(stream))
+        scratch = _new(x, at + M * K, torch.uint8, stream, result=False)
         scales = scratch.data_ptr()
         codes = scales + at
     args = (codes, scales, y.data_ptr(), _stream(stream))
