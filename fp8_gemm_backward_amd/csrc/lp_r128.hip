@@ -27,7 +27,7 @@ __global__ __launch_bounds__(kThreads) void r128_cols(const uint16_t* __restrict
   if (row >= total_rows) return;
   const int lane = threadIdx.x & 15;
   const uint32_t b = fdiv((uint32_t)row, rows), r = (uint32_t)row - b * rows.d;
-  const int nrun = (cols + kRunLen - 1) / kRunLen;
+  const int nrun = (cols - 1) / kRunLen + 1;               // (cols may be the largest int less 15)
   u32x4 v[kRunCols];
 #pragma unroll
   for (int j = 0; j < kRunCols; ++j) {
