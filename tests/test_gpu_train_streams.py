@@ -57,6 +57,35 @@ def test_adamw_table_of_another_stream_outlives_a_step_on_the_default_one(lp, bu
     assert torch.equal(run(torch.cuda.Stream()), want)
 
 
+def test_a_captured_adamw_step_outlives_set_grads(lp):
+    """Replays after set_grads, with memory given out in between, step with the gradients of the capture."""
+    n = 5000
+    p0, g1, g2 = np.random.default_rng(18).standard_normal((3, n), dtype=np.float32)
+
+    def fresh(g):
+        t = [dev(p0), torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")]
+        return t, lp.AdamWPlan(t[:1], [dev(g)], t[1:2], t[2:])
+    want_t, want_plan = fresh(g1)
+    t, plan = fresh(g1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lp.lp_adamw(plan, lr=0.1, step=1)
+    for _ in range(3):
+        plan.set_grads([dev(g2)])
+        junk = [torch.full((k,), -1, dtype=torch.int64, device="cuda") for k in (16, 64, 2500) for _ in range(4)]
+        graph.replay()
+        torch.cuda.synchronize()
+        del junk
+        lp.lp_adamw(want_plan, lr=0.1, step=1)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(t, want_t))
+    lp.lp_adamw(plan, lr=0.1, step=2)                    # an eager step takes the new gradients
+    want_plan.set_grads([dev(g2)])
+    lp.lp_adamw(want_plan, lr=0.1, step=2)
+    assert all(torch.equal(a, b) for a, b in zip(t, want_t))
+
+
 # ---------------------------------------------------------------- what a call allocates
 
 def products(lp):
