@@ -196,10 +196,14 @@ class QTensor:
                          None if scales is None else scales.data_ptr(), None if ts is None else ts.data_ptr())
 
 
+# torch.cuda.current_stream().cuda_stream without the Stream object (2.7 us a
+# call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        # torch.cuda.current_stream().cuda_stream without the Stream object (2.8 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 

@@ -181,3 +181,15 @@ def test_adamw_keeps_what_a_captured_step_reads(calls, monkeypatch, captured):
         lp.lp_adamw(plan, lr=0.1)
     gc.collect()
     assert (table() is not None) == (first() is not None) == captured
+
+
+@pytest.mark.parametrize("private", [True, False])
+def test_current_stream_without_torch_s_private_lookup(monkeypatch, private):
+    """The handle comes from a private call of torch's where there is one, from the public stream object otherwise."""
+    class Stream:
+        cuda_stream = 77
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    monkeypatch.setattr(lp, "_raw_stream", (lambda device: 1000 + device) if private else None)
+    assert lp._stream(None) == (1003 if private else 77)
+    assert lp._stream(Stream) == 77 and lp._stream(5) == 5
