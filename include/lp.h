@@ -300,9 +300,13 @@ lp_status lp_tensor_quant_delayed(const void* src_bf16, int64_t n, int32_t dst_f
  *           Or LP_FP8_R128 with scale_axis -1 (needs grad_w == NULL and w
  *           LP_FP8_B128) or -2 (needs grad_x == NULL and x LP_FP8_R128 with
  *           scale_axis -2), as produced by lp_r128_quant_dual: the product
- *           runs on the FP8 MFMA, in fp32 within each 128 of the contraction;
- *           each such sum is multiplied by the two scales' fp32 product and
- *           added in fp32.  LP_FP8_R128 pairs with nothing else.
+ *           runs on the FP8 MFMA.  Each 128 of the contraction is summed by
+ *           one instruction into an fp32 result; inside it the matrix core
+ *           aligns the (exact) products and drops low bits, less than 2^-10 of
+ *           the sum of their magnitudes in all (the largest measured: 2^-11.8
+ *           for one large product among small ones, 2^-12.6 for random codes).
+ *           The result is multiplied by the two scales' fp32 product and added
+ *           in fp32.  LP_FP8_R128 pairs with nothing else.
  * x         [M][K] saved input, or NULL when grad_w == NULL.
  * w         [N][K] saved weight, or NULL when grad_x == NULL.
  *           x and w: LP_BF16, LP_MXFP4, LP_NVFP4 (scale_axis -1), LP_FP8_B128,
@@ -490,8 +494,8 @@ lp_status lp_grouped_dx_deferred(const lp_qtensor* grad_out, const void* w, int6
  *      (scale_axis -1, K % 32 == 0): an NVFP4 x decoded first with
  *      lp_dequant, which saves the per-tile decode of x;
  *    - x LP_FP8_R128 (scale_axis -1) and w LP_FP8_B128 (K % 16 == 0), on the
- *      FP8 MFMA: fp32 sums within each 128 of K, times the two scales'
- *      fp32 product, added in fp32.
+ *      FP8 MFMA: sums of each 128 of K, times the two scales' fp32 product,
+ *      added in fp32, as lp_linear_bwd says of these operands.
  *    N % 16 == 0; M >= 0 arbitrary.
  * y  device bf16 [M][N].
  * MX operands: y[m][n] = sum_k dec(x)[m][k] * dec(w)[n][k] on the

@@ -8,6 +8,7 @@ import torch
 
 from gpu_util import assert_bits_equal, bf16_dev, bits_host, dev
 from oracle import train as O
+from oracle.formats import E4M3_TABLE
 from test_gpu_train import assert_product, bits, decoded, decoded_rows, weight
 
 pytestmark = pytest.mark.gpu
@@ -90,3 +91,19 @@ def test_sizes_of_zero(lp, M, N, K):
     torch.cuda.synchronize()
     for t in outs:
         assert not t.any()
+
+
+@pytest.mark.parametrize("M", [3, 40])
+@pytest.mark.parametrize("small", [1, 9, 24, 57, 65])
+def test_bits_dropped_inside_an_instruction_stay_within_the_bound(lp, M, small):
+    """Two products of 448 x 448 that cancel, among equal small ones: the matrix core aligns all of them to the large
+    ones, and what it drops is less than 2^-10 of the magnitudes' sum."""
+    N, K = 16, 128
+    for big, other in ((0, 1), (0, 64), (5, 100)):
+        x, w = np.full((M, K), small, np.uint8), np.full((N, K), 57, np.uint8)
+        x[:, big], x[:, other], w[:, big], w[:, other] = 0x7E, 0xFE, 0x7E, 0x7E
+        ones = torch.ones(1, 1, 1, device="cuda")
+        y = lp.lp_linear_fwd(lp.QTensor("fp8_r128", dev(x), ones.expand(1, 1, M).contiguous()), lp.QTensor("fp8_b128", dev(w), ones))
+        a, b = E4M3_TABLE[x], E4M3_TABLE[w].T
+        bound = 2.0 ** -8 * np.abs(a @ b) + 2.0 ** -10 * (np.abs(a) @ np.abs(b))
+        assert (np.abs(y.float().cpu().numpy() - a @ b) <= bound).all(), (big, other)
