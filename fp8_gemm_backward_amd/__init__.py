@@ -216,27 +216,38 @@ def _torch_stream(stream):
     return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
 
 
-def _new(like: torch.Tensor, shape, dtype, stream, result: bool = True) -> torch.Tensor:
-    """A tensor on like's device for a call on `stream` to write.  On another
-    stream than the current one it is taken from that stream's memory: a block
+def _new(like: torch.Tensor, stream, result: bool = True):
+    """new_empty(shape, dtype=) of like's device for a call on `stream` to write.
+    On another stream than the current one the memory is that stream's: a block
     of the current stream's may still be used by work enqueued there before
     it was freed, which the call does not wait for.  result: returned to the
     caller, who uses it on the current stream."""
     if stream is None or not like.is_cuda or _stream(stream) == _stream(None):
-        return like.new_empty(shape, dtype=dtype)
-    with torch.cuda.stream(_torch_stream(stream)):
-        t = like.new_empty(shape, dtype=dtype)
-    if result:
-        t.record_stream(torch.cuda.current_stream())
-    return t
+        return like.new_empty
+
+    def new(shape, dtype):
+        current = torch.cuda.current_stream()
+        torch.cuda.set_stream(_torch_stream(stream))         # (half the cost of the context manager)
+        try:
+            t = like.new_empty(shape, dtype=dtype)
+        finally:
+            torch.cuda.set_stream(current)
+        if result:
+            t.record_stream(current)
+        return t
+    return new
 
 
 def _capturing(stream) -> bool:
     """Whether what is enqueued on the stream goes into a graph."""
     if stream is None or _stream(stream) == _stream(None):
         return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.stream(_torch_stream(stream)):
+    current = torch.cuda.current_stream()
+    torch.cuda.set_stream(_torch_stream(stream))
+    try:
         return torch.cuda.is_current_stream_capturing()
+    finally:
+        torch.cuda.set_stream(current)
 
 
 def _check(st: int, where: str):
@@ -248,7 +259,7 @@ def lp_dequant(src: QTensor, out: Optional[torch.Tensor] = None, stream=None) ->
     """Decode `src` to bf16 [batch, rows, cols] (bit-exact); not "fp8_r128"
     whose runs restart at groups."""
     if out is None:
-        out = _new(src.codes, src.shape, torch.bfloat16, stream)
+        out = _new(src.codes, stream)(src.shape, dtype=torch.bfloat16)
     q = src.c()
     _device(out, "out", 2 * src.shape[0] * src.shape[1] * src.shape[2])
     _check(lib.lp_dequant(ctypes.byref(q), out.data_ptr(), _stream(stream)), "lp_dequant")
@@ -262,10 +273,10 @@ def lp_mx_quant(src: torch.Tensor, axis: int, fmt: str = "mxfp8", codes: Optiona
     shape = tuple(src.shape) if src.dim() == 3 else (1,) + tuple(src.shape)
     b, r, c = shape
     if codes is None:
-        codes = _new(src, (b, r, c if fmt == "mxfp8" else c // 2), torch.uint8, stream)
+        codes = _new(src, stream)((b, r, c if fmt == "mxfp8" else c // 2), dtype=torch.uint8)
     if scales is None:
         sshape = (b, r, c // 32) if axis == -1 else (b, r // 32, c)
-        scales = _new(src, sshape, torch.uint8, stream)
+        scales = _new(src, stream)(sshape, dtype=torch.uint8)
     n = b * r * c
     _device(src, "src", 2 * n, torch.bfloat16)
     _device(codes, "codes", n if fmt == "mxfp8" else n // 2)
@@ -282,10 +293,10 @@ def lp_mx_quant_dual(src: torch.Tensor, fmt: str = "mxfp8", stream=None) -> tupl
     b, r, c = shape
     cb = c if fmt == "mxfp8" else c // 2
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
-    codes_c = _new(src, (b, r, cb), torch.uint8, stream)
-    scales_c = _new(src, (b, r, c // 32), torch.uint8, stream)
-    codes_r = _new(src, (b, r, cb), torch.uint8, stream)
-    scales_r = _new(src, (b, r // 32, c), torch.uint8, stream)
+    codes_c = _new(src, stream)((b, r, cb), dtype=torch.uint8)
+    scales_c = _new(src, stream)((b, r, c // 32), dtype=torch.uint8)
+    codes_r = _new(src, stream)((b, r, cb), dtype=torch.uint8)
+    scales_r = _new(src, stream)((b, r // 32, c), dtype=torch.uint8)
     _check(lib.lp_mx_quant_dual(src.data_ptr(), b, r, c, FMT[fmt], codes_c.data_ptr(), scales_c.data_ptr(),
                                 codes_r.data_ptr(), scales_r.data_ptr(), _stream(stream)), "lp_mx_quant_dual")
     return QTensor(fmt, codes_c, scales_c, None, shape, -1), QTensor(fmt, codes_r, scales_r, None, shape, -2)
@@ -295,7 +306,7 @@ def lp_tensor_amax(src: torch.Tensor, amax: Optional[torch.Tensor] = None, strea
     """max |x| of a bf16 tensor into a float32 device scalar (`amax` may be a
     one-element view into an amax history)."""
     if amax is None:
-        amax = _new(src, 1, torch.float32, stream)
+        amax = _new(src, stream)(1, dtype=torch.float32)
     _device(src, "src", 2 * src.numel(), torch.bfloat16)
     _device(amax, "amax", 4, torch.float32)
     _check(lib.lp_tensor_amax(src.data_ptr(), src.numel(), amax.data_ptr(), _stream(stream)), "lp_tensor_amax")
@@ -309,7 +320,7 @@ def lp_tensor_quant(src: torch.Tensor, fmt: str, scale: torch.Tensor, amax: Opti
     scalar `scale`; the input's amax goes to `amax` when given."""
     shape = tuple(src.shape) if src.dim() == 3 else (1,) + tuple(src.shape)
     if codes is None:
-        codes = _new(src, shape, torch.uint8, stream)
+        codes = _new(src, stream)(shape, dtype=torch.uint8)
     _device(src, "src", 2 * src.numel(), torch.bfloat16)
     _device(codes, "codes", src.numel())
     _device(scale, "scale", 4, torch.float32)
@@ -327,9 +338,9 @@ def lp_tensor_quant_delayed(src: torch.Tensor, fmt: str, history: torch.Tensor, 
     ring), quantization with it, the input's amax into history[slot]."""
     shape = tuple(src.shape) if src.dim() == 3 else (1,) + tuple(src.shape)
     if codes is None:
-        codes = _new(src, shape, torch.uint8, stream)
+        codes = _new(src, stream)(shape, dtype=torch.uint8)
     if scale is None:
-        scale = _new(src, 1, torch.float32, stream)
+        scale = _new(src, stream)(1, dtype=torch.float32)
     _device(src, "src", 2 * src.numel(), torch.bfloat16)
     _device(codes, "codes", src.numel())
     _device(history, "history", 4 * max(history.numel(), 1), torch.float32)
@@ -344,7 +355,7 @@ def lp_scale_from_history(history: torch.Tensor, fmt: str, margin: int = 0, scal
                           stream=None) -> torch.Tensor:
     """Per-tensor scale (float32 device scalar) from a float32 amax history."""
     if scale is None:
-        scale = _new(history, 1, torch.float32, stream)
+        scale = _new(history, stream)(1, dtype=torch.float32)
     _device(history, "history", 4 * max(history.numel(), 1), torch.float32)
     _device(scale, "scale", 4, torch.float32)
     _check(lib.lp_scale_from_history(history.data_ptr(), history.numel(), FMT[fmt], margin, scale.data_ptr(),
@@ -365,12 +376,12 @@ def lp_linear_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor],
     codes = grad_out.codes
     if need_dx:
         if grad_x is None:
-            grad_x = _new(codes, (M, K), torch.bfloat16, stream)
+            grad_x = _new(codes, stream)((M, K), dtype=torch.bfloat16)
         else:
             _device(grad_x, "grad_x", 2 * M * K)
     if need_dw:
         if grad_w is None:
-            grad_w = _new(codes, (N, K), torch.bfloat16, stream)
+            grad_w = _new(codes, stream)((N, K), dtype=torch.bfloat16)
         else:
             _device(grad_w, "grad_w", 2 * N * K)
     if workspace is not None:
@@ -386,7 +397,7 @@ def lp_linear_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor],
             nbytes = ctypes.c_size_t(0)
             _check(lib.lp_linear_bwd_workspace(*args, ctypes.byref(nbytes)), "lp_linear_bwd_workspace")
             if nbytes.value:
-                workspace = _new(codes, nbytes.value, torch.uint8, stream, result=False)
+                workspace = _new(codes, stream, result=False)(nbytes.value, dtype=torch.uint8)
     if workspace is None:
         st = lib.lp_linear_bwd(*args, _stream(stream))
         _check(st, "lp_linear_bwd")
@@ -406,9 +417,9 @@ def lp_linear_bwd_noalloc(grad_out: QTensor, x: Optional[QTensor], w: Optional[Q
     M, N = grad_out.rows, grad_out.cols
     K = (w if need_dx else x).cols
     if need_dx and grad_x is None:
-        grad_x = _new(grad_out.codes, (M, K), torch.bfloat16, stream)
+        grad_x = _new(grad_out.codes, stream)((M, K), dtype=torch.bfloat16)
     if need_dw and grad_w is None:
-        grad_w = _new(grad_out.codes, (N, K), torch.bfloat16, stream)
+        grad_w = _new(grad_out.codes, stream)((N, K), dtype=torch.bfloat16)
     if need_dx:
         _device(grad_x, "grad_x", 2 * M * K)
     if need_dw:
@@ -434,12 +445,12 @@ def lp_grouped_dx_deferred(grad_out: QTensor, w: torch.Tensor, offsets: torch.Te
     G, N, K = w.shape
     M = grad_out.rows
     if grad_x is None:
-        grad_x = _new(grad_out.codes, (M, K), torch.bfloat16, stream)
+        grad_x = _new(grad_out.codes, stream)((M, K), dtype=torch.bfloat16)
     if fuse_rows < M or N % 512 or K % 32:
         if w_codes is None:
-            w_codes = _new(w, (G, N, K), torch.uint8, stream, result=False)
+            w_codes = _new(w, stream, result=False)((G, N, K), dtype=torch.uint8)
         if w_scales is None:
-            w_scales = _new(w, (G, N // 32, K), torch.uint8, stream, result=False)
+            w_scales = _new(w, stream, result=False)((G, N // 32, K), dtype=torch.uint8)
         _device(w_codes, "w_codes", G * N * K)
         _device(w_scales, "w_scales", G * (N // 32) * K)
     _device(w, "w", 2 * G * N * K, torch.bfloat16)
@@ -479,12 +490,12 @@ def lp_grouped_bwd(grad_out: QTensor, x: Optional[QTensor], w: Optional[QTensor]
     codes = grad_out.codes
     if need_dx:
         if grad_x is None:
-            grad_x = _new(codes, (M, K), torch.bfloat16, stream)
+            grad_x = _new(codes, stream)((M, K), dtype=torch.bfloat16)
         else:
             _device(grad_x, "grad_x", 2 * M * K)
     if need_dw:
         if grad_w is None:
-            grad_w = _new(codes, (G, N, K), torch.bfloat16, stream)
+            grad_w = _new(codes, stream)((G, N, K), dtype=torch.bfloat16)
         else:
             _device(grad_w, "grad_w", 2 * G * N * K)
     _device(offsets, "offsets", 4 * G, torch.int32)
@@ -503,7 +514,7 @@ def lp_linear_fwd(x: QTensor, w: QTensor, y: Optional[torch.Tensor] = None, stre
     both "nvfp4", a "bf16" x with a "bf16", "fp8_b128" or "nvfp4" weight, or
     an "fp8_r128" x (along -1) with an "fp8_b128" weight."""
     if y is None:
-        y = _new(x.codes, (x.rows, w.rows), torch.bfloat16, stream)
+        y = _new(x.codes, stream)((x.rows, w.rows), dtype=torch.bfloat16)
     _device(y, "y", 2 * x.rows * w.rows)
     xc, wc = x.c(), w.c()
     _check(lib.lp_linear_fwd(ctypes.byref(xc), ctypes.byref(wc), y.data_ptr(), _stream(stream)), "lp_linear_fwd")
@@ -515,7 +526,7 @@ def lp_grouped_fwd(x: QTensor, w: QTensor, offsets: torch.Tensor, y: Optional[to
     """y [M, N]: rows of group g are x[rows] @ w[g]^T; rows at or past
     offsets[-1] are left as they were in `y`."""
     if y is None:
-        y = _new(x.codes, (x.rows, w.rows), torch.bfloat16, stream)
+        y = _new(x.codes, stream)((x.rows, w.rows), dtype=torch.bfloat16)
     _device(y, "y", 2 * x.rows * w.rows)
     _device(offsets, "offsets", 4 * offsets.numel(), torch.int32)
     xc, wc = x.c(), w.c()
@@ -555,12 +566,13 @@ def lp_r128_quant(src: torch.Tensor, axis: int = -1, offsets: Optional[torch.Ten
     "fp8_r128" along `axis` (-1 or -2).  offsets (axis -2): int32 cumulative
     group ends; runs restart at every group's first row."""
     b, r, c = shape = _shape3(src)
-    codes = _new(src, shape, torch.uint8, stream)
-    scales = _new(src, (b, -(-c // 128), r) if axis == -1 else (b, _runs(r, offsets), c), torch.float32, stream)
+    new, off = _new(src, stream), _offsets(offsets)
+    codes = new(shape, dtype=torch.uint8)
+    scales = new((b, -(-c // 128), r) if axis == -1 else (b, _runs(r, offsets), c), dtype=torch.float32)
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
-    _check(lib.lp_r128_quant(src.data_ptr(), b, r, c, axis, *_offsets(offsets), codes.data_ptr(), scales.data_ptr(),
+    _check(lib.lp_r128_quant(src.data_ptr(), b, r, c, axis, *off, codes.data_ptr(), scales.data_ptr(),
                              _stream(stream)), "lp_r128_quant")
-    return QTensor("fp8_r128", codes, scales, None, shape, axis, _offsets(offsets)[1] if axis == -2 else None)
+    return QTensor("fp8_r128", codes, scales, None, shape, axis, off[1] if axis == -2 else None)
 
 
 def lp_r128_quant_dual(src: torch.Tensor, offsets: Optional[torch.Tensor] = None, stream=None) -> tuple:
@@ -568,15 +580,15 @@ def lp_r128_quant_dual(src: torch.Tensor, offsets: Optional[torch.Tensor] = None
     -2); the second one's runs restart at each group of `offsets`.  Rows past
     the last offset are left unwritten in both."""
     b, r, c = shape = _shape3(src)
-    codes_c = _new(src, shape, torch.uint8, stream)
-    codes_r = _new(src, shape, torch.uint8, stream)
-    scales_c = _new(src, (b, -(-c // 128), r), torch.float32, stream)
-    scales_r = _new(src, (b, _runs(r, offsets), c), torch.float32, stream)
+    new, off = _new(src, stream), _offsets(offsets)
+    codes_c, codes_r = new(shape, dtype=torch.uint8), new(shape, dtype=torch.uint8)
+    scales_c = new((b, -(-c // 128), r), dtype=torch.float32)
+    scales_r = new((b, _runs(r, offsets), c), dtype=torch.float32)
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
-    _check(lib.lp_r128_quant_dual(src.data_ptr(), b, r, c, *_offsets(offsets), codes_c.data_ptr(), scales_c.data_ptr(),
+    _check(lib.lp_r128_quant_dual(src.data_ptr(), b, r, c, *off, codes_c.data_ptr(), scales_c.data_ptr(),
                                   codes_r.data_ptr(), scales_r.data_ptr(), _stream(stream)), "lp_r128_quant_dual")
     return (QTensor("fp8_r128", codes_c, scales_c, None, shape, -1),
-            QTensor("fp8_r128", codes_r, scales_r, None, shape, -2, _offsets(offsets)[1]))
+            QTensor("fp8_r128", codes_r, scales_r, None, shape, -2, off[1]))
 
 
 def lp_b128_quant(src: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
@@ -585,9 +597,9 @@ def lp_b128_quant(src: torch.Tensor, codes: Optional[torch.Tensor] = None, scale
     "fp8_b128" (into `codes` and `scales` when given)."""
     b, r, c = shape = _shape3(src)
     if codes is None:
-        codes = _new(src, shape, torch.uint8, stream)
+        codes = _new(src, stream)(shape, dtype=torch.uint8)
     if scales is None:
-        scales = _new(src, (b, -(-r // 128), -(-c // 128)), torch.float32, stream)
+        scales = _new(src, stream)((b, -(-r // 128), -(-c // 128)), dtype=torch.float32)
     _device(src, "src", 2 * b * r * c, torch.bfloat16)
     _device(codes, "codes", b * r * c)
     _device(scales, "scales", _scale_bytes("fp8_b128", -1, b, r, c), torch.float32)
@@ -602,7 +614,7 @@ def _fwd_dyn(x: torch.Tensor, w: QTensor, offsets: Optional[torch.Tensor], y: Op
         raise ValueError(f"x has {K} columns, the weight {w.cols}")
     _device(x, "x", 2 * M * K, torch.bfloat16)
     if y is None:
-        y = _new(x, (M, w.rows), torch.bfloat16, stream)
+        y = _new(x, stream)((M, w.rows), dtype=torch.bfloat16)
     else:
         _device(y, "y", 2 * M * w.rows)
     nb = -(-K // 128)
@@ -610,7 +622,7 @@ def _fwd_dyn(x: torch.Tensor, w: QTensor, offsets: Optional[torch.Tensor], y: Op
         codes = scales = None
     else:
         at = -(-4 * nb * M // 16) * 16                       # scratch: scales, then (16-byte aligned) codes
-        scratch = _new(x, at + M * K, torch.uint8, stream, result=False)
+        scratch = _new(x, stream, result=False)(at + M * K, dtype=torch.uint8)
         scales = scratch.data_ptr()
         codes = scales + at
     args = (codes, scales, y.data_ptr(), _stream(stream))
