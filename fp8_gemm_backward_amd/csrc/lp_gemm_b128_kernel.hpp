@@ -30,10 +30,12 @@
 // 8192 x 4096 outputs: 1.59 us (forward, grad_X) and 1.86 us (grad_W) per 128 deep
 // stage and round of 256 tiles, 2.69 and 2.31 PFLOP/s asymptotically; with a contraction of 4096
 // 117, 116 and 135 us (2.35, 2.37, 2.04 PFLOP/s).  A plain FP8 product of the vendor's
-// library without block scales reaches 2.83 PFLOP/s at 8192^3.  Bound by power
-// and instruction issue: the clock falls to 1.9 GHz, the matrix cores are busy
-// 55% of the time, LDS 27%; leaving out grad_W's 128 multiplies per wave and stage takes
-// 272 us to 228 over a contraction of 8192.
+// library without block scales reaches 2.83 PFLOP/s at 8192^3.  Bound by the
+// stages' loads, instruction issue and power: without the loads 3.6 PFLOP/s, about half
+// of the difference by the clock (2.2 GHz, 1.9 with them), half by waiting.  The matrix
+// cores are busy 46 to 55% of the time, LDS 27%, and the waves wait for a quarter of
+// it.  Leaving out grad_W's 128 multiplies per wave and stage takes 272 us to 228 over
+// a contraction of 8192.
 //
 // A 128-deep stage of both operands and its scales goes from global memory
 // straight into LDS, two stages deep; one barrier per stage.  LDS layouts:
