@@ -103,6 +103,7 @@ def products(lp):
     long_g, long_x = (lp.lp_r128_quant(randn(12000, 16), -2) for _ in range(2))     # split: a workspace
     sq = randn(96, 128)
     hist, scale = torch.ones(4, device="cuda"), torch.ones(1, device="cuda")
+    rings = [hist.clone() for _ in range(4)]             # (the call writes its own)
     mx, t8 = lp.lp_mx_quant(sq, -1), lp.lp_tensor_quant(sq, "fp8t_e4m3", scale)
     b16 = lp.QTensor("bf16", g, shape=(1, M, N))
     wm = randn(2, 64, 64)
@@ -114,7 +115,7 @@ def products(lp):
         "mx_quant_dual": lambda s: parts(*lp.lp_mx_quant_dual(sq, stream=s)),
         "tensor_amax": lambda s: [lp.lp_tensor_amax(sq, stream=s)],
         "tensor_quant": lambda s: [lp.lp_tensor_quant(sq, "fp8t_e5m2", scale, stream=s).codes],
-        "tensor_quant_delayed": lambda s: [lp.lp_tensor_quant_delayed(sq, "fp8t_e4m3", hist.clone(), 0, stream=s).codes],
+        "tensor_quant_delayed": lambda s: [lp.lp_tensor_quant_delayed(sq, "fp8t_e4m3", rings.pop(), 0, stream=s).codes],
         "scale_from_history": lambda s: [lp.lp_scale_from_history(hist, "fp8t_e4m3", stream=s)],
         "r128_quant": lambda s: parts(lp.lp_r128_quant(x, -1, stream=s)),
         "r128_quant rows": lambda s: parts(lp.lp_r128_quant(x, -2, stream=s)),
@@ -154,7 +155,7 @@ def test_what_a_call_allocates_is_memory_of_its_stream(lp, monkeypatch, raw):
     """Results and hidden scratch: no address that a C call is given, but the inputs', is the current stream's memory."""
     calls, keep = products(lp)
     inputs = set()
-    for v in keep.values():
+    for v in [*keep.values(), *keep["rings"]]:
         for t in parts(v) + [v.tensor_scale] if isinstance(v, lp.QTensor) else [v]:
             if isinstance(t, torch.Tensor):
                 inputs.add(t.data_ptr())
@@ -171,8 +172,6 @@ def test_what_a_call_allocates_is_memory_of_its_stream(lp, monkeypatch, raw):
         seen.clear()
         out = call(s.cuda_stream if raw else s)
         streams = {segment_stream(p) for p in seen if segment_stream(p) is not None}
-        if name == "tensor_quant_delayed":
-            streams.discard(0)                           # (the copy of the history)
         assert streams == {s.cuda_stream}, name
         assert {segment_stream(t.data_ptr()) for t in out} == {s.cuda_stream}, name
     torch.cuda.synchronize()
