@@ -663,7 +663,7 @@ class AdamWPlan:
     uint8 E4M3 codes with float32 scales per 128 elements
     (exp_avg_sq_scales: of sqrt(v)).  copies: bfloat16 tensors that receive
     the new float32 parameters.  weight_decay, lr_scale: one number or one
-    per tensor.  The plan keeps the tensors alive and holds the device table
+    per tensor.  Tensors must not overlap (a tied weight is listed once).  The plan keeps the tensors alive and holds the device table
     that the step reads; set_grads makes a new one, so gradients that stay
     where they are from step to step are the cheaper way.
 
