@@ -83,7 +83,7 @@ def breaches(code) -> list:
     return found
 
 
-def test_checker_sees_planted_breaches():
+def test_planted_breaches_are_seen():
     def check(*lines):
         return bool(breaches([("f", line) for line in lines]))
     load = "buffer_load_dwordx4 v1, s[4:7], s9 offen lds"
