@@ -14,7 +14,9 @@ Formats (see include/lp.h): "bf16", "mxfp4", "nvfp4", "fp8_b128", "mxfp8",
 the per-tensor scaled "fp8t_e4m3", "fp8t_e5m2", and "fp8_r128" (E4M3 with an
 fp32 scale per run of 128, the counterpart of an "fp8_b128" weight in FP8
 products).  include/lp_train.h declares the quantizers of the last two, the
-forwards that quantize their own input, and the AdamW step.
+forwards that quantize their own input, and the AdamW step; include/lp_moe.h
+what a mixture-of-experts layer has around its grouped products, and the
+forwards of few rows by a 4-bit weight.
 """
 from __future__ import annotations
 
@@ -77,13 +79,25 @@ def _load() -> ctypes.CDLL:
     f64 = ctypes.c_double
     lib.lp_adamw_plan.argtypes = [v, i64, i32, i32, i32, v, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(i64)]
     lib.lp_adamw.argtypes = [v, i64, i64, i32, i32, i32, f64, f64, f64, f64, i64, v, v]
+    lib.lp_moe_gate.argtypes = [v, i32, i64, i64, i64, i32, v, v, v]
+    lib.lp_moe_gate_bwd.argtypes = [v, v, i32, i64, i64, i64, i32, v, v, v, v]
+    lib.lp_moe_sort_workspace.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_size_t)]
+    lib.lp_moe_sort.argtypes = [v, i64, i64, v, v, v, v, ctypes.c_size_t, v]
+    lib.lp_moe_gather.argtypes = [v, i64, i64, i64, v, v, v]
+    lib.lp_moe_gather_quant.argtypes = [v, i64, i64, i64, v, v, v, i64, v, v, v, v, v]
+    lib.lp_moe_combine.argtypes = [v, i64, i64, i64, v, v, v, v]
+    lib.lp_moe_combine_bwd.argtypes = [v, v, i64, i64, i64, v, v, v, v, v]
+    lib.lp_linear_fwd_w4.argtypes = [v, i64, P, v, v]
+    lib.lp_grouped_fwd_w4.argtypes = [v, i64, P, v, i64, v, v]
     lib.lp_status_string.argtypes = [i32]
     lib.lp_status_string.restype = ctypes.c_char_p
     for f in ("lp_dequant", "lp_mx_quant", "lp_mx_quant_dual", "lp_linear_bwd", "lp_grouped_bwd",
               "lp_linear_bwd_workspace", "lp_linear_bwd_ws", "lp_linear_bwd_noalloc", "lp_grouped_dx_deferred", "lp_tensor_amax", "lp_tensor_quant",
               "lp_scale_from_history", "lp_linear_fwd", "lp_grouped_fwd", "lp_tensor_quant_delayed",
               "lp_r128_quant", "lp_r128_quant_dual", "lp_b128_quant", "lp_linear_fwd_dyn", "lp_grouped_fwd_dyn",
-              "lp_adamw_plan", "lp_adamw"):
+              "lp_adamw_plan", "lp_adamw", "lp_moe_gate", "lp_moe_gate_bwd", "lp_moe_sort_workspace", "lp_moe_sort",
+              "lp_moe_gather", "lp_moe_gather_quant", "lp_moe_combine", "lp_moe_combine_bwd", "lp_linear_fwd_w4",
+              "lp_grouped_fwd_w4"):
         getattr(lib, f).restype = ctypes.c_int32
     return lib
 
@@ -756,3 +770,219 @@ def lp_adamw(plan: AdamWPlan, lr: float, beta1: float = 0.9, beta2: float = 0.99
     _check(lib.lp_adamw(None if t is None else t.data_ptr(), len(plan._n), plan._chunks, _ADAMW_DTYPE[plan.param_dtype],
                         _ADAMW_DTYPE[plan.grad_dtype], int(plan.bits8), lr, beta1, beta2, eps, step,
                         None if grad_scale is None else grad_scale.data_ptr(), s), "lp_adamw")
+
+
+# ---------------------------------------------------------------- include/lp_moe.h
+
+_GATE_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _gate_dtype(logits: torch.Tensor) -> int:
+    if logits.dtype not in _GATE_DTYPE:
+        raise ValueError(f"logits must be float32 or bfloat16, not {logits.dtype}")
+    return _GATE_DTYPE[logits.dtype]
+
+
+def lp_moe_gate(logits: torch.Tensor, topk: int, renorm: bool = True, weights: Optional[torch.Tensor] = None,
+                chosen: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """(weights float32 [T, topk], chosen int32 [T, topk]) of logits [T, E]
+    (float32 or bfloat16): every token's topk largest, largest first, ties to
+    the lowest expert, -inf never (-1 and weight 0 where nothing is left), with
+    their softmax probabilities, divided by their sum with renorm."""
+    T, E = logits.shape
+    dtype = _gate_dtype(logits)
+    if weights is None or chosen is None:
+        new = _new(logits, stream)
+        weights = new((T, topk), dtype=torch.float32) if weights is None else weights
+        chosen = new((T, topk), dtype=torch.int32) if chosen is None else chosen
+    _device(logits, "logits", T * E * logits.element_size())
+    _device(weights, "weights", 4 * T * topk, torch.float32)
+    _device(chosen, "chosen", 4 * T * topk, torch.int32)
+    _check(lib.lp_moe_gate(logits.data_ptr(), dtype, T, E, topk, int(renorm), weights.data_ptr(), chosen.data_ptr(),
+                           _stream(stream)), "lp_moe_gate")
+    return weights, chosen
+
+
+def lp_moe_gate_bwd(grad_weights: torch.Tensor, logits: torch.Tensor, weights: torch.Tensor, chosen: torch.Tensor,
+                    renorm: bool = True, grad_logits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of lp_moe_gate's logits, in their dtype, from that of its
+    weights; weights, chosen and renorm are the forward's."""
+    T, E = logits.shape
+    k = chosen.shape[-1]
+    dtype = _gate_dtype(logits)
+    if grad_logits is None:
+        grad_logits = _new(logits, stream)((T, E), dtype=logits.dtype)
+    _device(logits, "logits", T * E * logits.element_size())
+    _device(grad_logits, "grad_logits", T * E * logits.element_size(), logits.dtype)
+    _device(grad_weights, "grad_weights", 4 * T * k, torch.float32)
+    _device(weights, "weights", 4 * T * k, torch.float32)
+    _device(chosen, "chosen", 4 * T * k, torch.int32)
+    _check(lib.lp_moe_gate_bwd(grad_weights.data_ptr(), logits.data_ptr(), dtype, T, E, k, int(renorm),
+                               weights.data_ptr(), chosen.data_ptr(), grad_logits.data_ptr(), _stream(stream)),
+           "lp_moe_gate_bwd")
+    return grad_logits
+
+
+def lp_moe_sort(experts: torch.Tensor, groups: int, stream=None) -> tuple:
+    """(offsets int32 [groups], rows int32 like experts, order int32 [pairs]) of
+    int32 experts [T, k]: the pairs stably sorted by expert.  offsets: the
+    grouped products' cumulative ends; rows: every pair's row (-1: an expert
+    outside 0 .. groups-1); order: every row's pair t * k + j (unwritten past
+    the last offset)."""
+    n = experts.numel()
+    new = _new(experts, stream)
+    offsets, order = new((groups,), dtype=torch.int32), new((n,), dtype=torch.int32)
+    rows = new(experts.shape, dtype=torch.int32)
+    _device(experts, "experts", 4 * n, torch.int32)
+    ws, nbytes = None, ctypes.c_size_t(0)
+    _check(lib.lp_moe_sort_workspace(n, groups, ctypes.byref(nbytes)), "lp_moe_sort_workspace")
+    if nbytes.value:
+        ws = _new(experts, stream, result=False)((nbytes.value,), dtype=torch.uint8)
+    _check(lib.lp_moe_sort(experts.data_ptr(), n, groups, offsets.data_ptr(), rows.data_ptr(), order.data_ptr(),
+                           None if ws is None else ws.data_ptr(), nbytes.value, _stream(stream)), "lp_moe_sort")
+    return offsets, rows, order
+
+
+def _tokens(rows: torch.Tensor) -> tuple:
+    if rows.dim() != 2:
+        raise ValueError(f"rows must be [tokens, slots], not {tuple(rows.shape)}")
+    T, k = rows.shape
+    _device(rows, "rows", 4 * T * k, torch.int32)
+    return T, k
+
+
+def _matrix(t: torch.Tensor, name: str, rows: int) -> int:
+    """Columns of a bf16 matrix [rows, columns]."""
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must be [{rows}, columns], not {tuple(t.shape)}")
+    _device(t, name, 2 * rows * t.shape[1], torch.bfloat16)
+    return t.shape[1]
+
+
+def lp_moe_gather(x: torch.Tensor, rows: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """bf16 rows [T * k, H]: out[rows[t, j]] = x[t] (rows as lp_moe_sort makes
+    them).  Rows of no pair are left as they were in `out`."""
+    T, k = _tokens(rows)
+    H = _matrix(x, "x", T)
+    if out is None:
+        out = _new(x, stream)((T * k, H), dtype=torch.bfloat16)
+    else:
+        _matrix(out, "out", T * k)
+        _device(out, "out", 2 * T * k * H)
+    _check(lib.lp_moe_gather(x.data_ptr(), T, k, H, rows.data_ptr(), out.data_ptr(), _stream(stream)), "lp_moe_gather")
+    return out
+
+
+def lp_moe_gather_quant(x: torch.Tensor, order: torch.Tensor, offsets: torch.Tensor, topk: int,
+                        weights: Optional[torch.Tensor] = None, out: Optional[tuple] = None, stream=None) -> tuple:
+    """lp_r128_quant_dual of lp_moe_gather's rows (with weights: each row times
+    its pair's weight), bit for bit, without the bf16 rows: x [T, H], order
+    and offsets as lp_moe_sort makes them.  out: the two "fp8_r128" tensors
+    to write, as this call returns them."""
+    T = x.shape[0]
+    M, G = T * topk, offsets.numel()
+    H = _matrix(x, "x", T)
+    if G == 0:
+        raise LpError(2, "offsets of no group")
+    _device(order, "order", 4 * M, torch.int32)
+    _device(offsets, "offsets", 4 * G, torch.int32)
+    if weights is not None:
+        _device(weights, "weights", 4 * M, torch.float32)
+    runs, nb = M // 128 + G, -(-H // 128)
+    if out is None:
+        new = _new(x, stream)
+        out = (QTensor("fp8_r128", new((1, M, H), dtype=torch.uint8), new((1, nb, M), dtype=torch.float32), None,
+                       (1, M, H), -1),
+               QTensor("fp8_r128", new((1, M, H), dtype=torch.uint8), new((1, runs, H), dtype=torch.float32), None,
+                       (1, M, H), -2, G))
+    else:
+        for q, n, name in zip(out, (nb * M, runs * H), ("out[0]", "out[1]")):
+            if q.fmt != "fp8_r128" or tuple(q.shape) != (1, M, H) or q.axis != (-1 if q is out[0] else -2):
+                raise ValueError(f"{name}: not the tensor this call writes")
+            _device(q.codes, f"{name} codes", M * H, torch.uint8)
+            _device(q.scales, f"{name} scales", 4 * n, torch.float32)
+        out[1].run_groups = G
+    cols, toks = out
+    _check(lib.lp_moe_gather_quant(x.data_ptr(), T, topk, H, order.data_ptr(), None if weights is None else weights.data_ptr(),
+                                   offsets.data_ptr(), G, cols.codes.data_ptr(), cols.scales.data_ptr(),
+                                   toks.codes.data_ptr(), toks.scales.data_ptr(), _stream(stream)), "lp_moe_gather_quant")
+    return out
+
+
+def lp_moe_combine(y: torch.Tensor, rows: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """bf16 [T, H]: out[t] = sum_j weights[t, j] * y[rows[t, j]], summed in
+    fp32 (weights None: 1, which is the gradient of lp_moe_gather); zeros for a
+    token without a row."""
+    T, k = _tokens(rows)
+    H = _matrix(y, "y", T * k)
+    if weights is not None:
+        _device(weights, "weights", 4 * T * k, torch.float32)
+    if out is None:
+        out = _new(y, stream)((T, H), dtype=torch.bfloat16)
+    else:
+        _matrix(out, "out", T)
+        _device(out, "out", 2 * T * H)
+    _check(lib.lp_moe_combine(y.data_ptr(), T, k, H, rows.data_ptr(), None if weights is None else weights.data_ptr(),
+                              out.data_ptr(), _stream(stream)), "lp_moe_combine")
+    return out
+
+
+def lp_moe_combine_bwd(grad: torch.Tensor, y: Optional[torch.Tensor], rows: torch.Tensor,
+                       weights: Optional[torch.Tensor] = None, need_dy: bool = True, need_dw: bool = True,
+                       grad_y: Optional[torch.Tensor] = None, grad_weights: Optional[torch.Tensor] = None,
+                       stream=None) -> tuple:
+    """(grad_y bf16 [T * k, H] or None, grad_weights float32 [T, k] or None) of
+    lp_moe_combine from grad [T, H].  Rows of no pair are left as they were in
+    `grad_y`; y is read for grad_weights only."""
+    T, k = _tokens(rows)
+    H = _matrix(grad, "grad", T)
+    if weights is not None:
+        _device(weights, "weights", 4 * T * k, torch.float32)
+    if need_dy:
+        if grad_y is None:
+            grad_y = _new(grad, stream)((T * k, H), dtype=torch.bfloat16)
+        else:
+            _device(grad_y, "grad_y", 2 * T * k * H, torch.bfloat16)
+    if need_dw:
+        _device(y, "y", 2 * T * k * H, torch.bfloat16)
+        if grad_weights is None:
+            grad_weights = _new(grad, stream)((T, k), dtype=torch.float32)
+        else:
+            _device(grad_weights, "grad_weights", 4 * T * k, torch.float32)
+    _check(lib.lp_moe_combine_bwd(grad.data_ptr(), y.data_ptr() if need_dw else None, T, k, H, rows.data_ptr(),
+                                  None if weights is None else weights.data_ptr(), grad_y.data_ptr() if need_dy else None,
+                                  grad_weights.data_ptr() if need_dw else None, _stream(stream)), "lp_moe_combine_bwd")
+    return (grad_y if need_dy else None), (grad_weights if need_dw else None)
+
+
+def _fwd_w4(x: torch.Tensor, w: QTensor, offsets: Optional[torch.Tensor], y: Optional[torch.Tensor], stream):
+    M, K = x.shape
+    if K != w.cols:
+        raise ValueError(f"x has {K} columns, the weight {w.cols}")
+    _device(x, "x", 2 * M * K, torch.bfloat16)
+    if y is None:
+        y = _new(x, stream)((M, w.rows), dtype=torch.bfloat16)
+    else:
+        _device(y, "y", 2 * M * w.rows)
+    wc = w.c()
+    if offsets is None:
+        _check(lib.lp_linear_fwd_w4(x.data_ptr(), M, ctypes.byref(wc), y.data_ptr(), _stream(stream)), "lp_linear_fwd_w4")
+    else:
+        _device(offsets, "offsets", 4 * offsets.numel(), torch.int32)
+        _check(lib.lp_grouped_fwd_w4(x.data_ptr(), M, ctypes.byref(wc), offsets.data_ptr(), offsets.numel(), y.data_ptr(),
+                                     _stream(stream)), "lp_grouped_fwd_w4")
+    return y
+
+
+def lp_linear_fwd_w4(x: torch.Tensor, w: QTensor, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y [M, N] = x @ w^T: a bf16 x [M, K] (made for few rows) times an "mxfp4"
+    or "nvfp4" weight."""
+    return _fwd_w4(x, w, None, y, stream)
+
+
+def lp_grouped_fwd_w4(x: torch.Tensor, w: QTensor, offsets: torch.Tensor, y: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """y [M, N]: rows of group g are x[rows] @ w[g]^T; rows at or past
+    offsets[-1] are left as they were in `y`."""
+    return _fwd_w4(x, w, offsets, y, stream)

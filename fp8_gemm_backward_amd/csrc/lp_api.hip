@@ -352,7 +352,8 @@ extern "C" {
 // scaled along k (K % 128 for MXFP4, K % 64 for MXFP8), both NVFP4 (K % 32),
 // a bf16 x with a bf16 or block-FP8 weight, or an LP_FP8_R128 x (along k) with
 // a block-FP8 weight (K % 16); N % 16.
-static lp_status check_fwd(const lp_qtensor* x, const lp_qtensor* w, void* y, int64_t groups) {
+// w4: a bf16 x with an MXFP4 or NVFP4 weight (K % 32) instead.
+static lp_status check_fwd(const lp_qtensor* x, const lp_qtensor* w, void* y, int64_t groups, bool w4 = false) {
   lp_status st = check_tensor(x);
   if (st != LP_OK) return st;
   if ((st = check_tensor(w)) != LP_OK) return st;
@@ -360,11 +361,11 @@ static lp_status check_fwd(const lp_qtensor* x, const lp_qtensor* w, void* y, in
   const bool nv = x->fmt == LP_NVFP4 && w->fmt == LP_NVFP4;
   const bool b16 = x->fmt == LP_BF16 && (w->fmt == LP_BF16 || w->fmt == LP_FP8_B128 || w->fmt == LP_NVFP4);
   const bool r128 = x->fmt == LP_FP8_R128 && x->scale_axis == -1 && w->fmt == LP_FP8_B128;
-  if (!mx && !nv && !b16 && !r128) return LP_ERR_FORMAT;
+  if (w4 ? x->fmt != LP_BF16 || !is_fp4(w->fmt) : !mx && !nv && !b16 && !r128) return LP_ERR_FORMAT;
   if ((mx || nv) && (x->scale_axis != -1 || w->scale_axis != -1)) return LP_ERR_FORMAT;
-  if (w->fmt == LP_NVFP4 && w->scale_axis != -1) return LP_ERR_FORMAT;
+  if (is_fp4(w->fmt) && w->scale_axis != -1) return LP_ERR_FORMAT;
   if (x->batch != 1 || w->batch != (groups ? groups : 1) || w->cols != x->cols) return LP_ERR_SHAPE;
-  const int64_t kmul = x->fmt == LP_MXFP4 ? 128 : x->fmt == LP_MXFP8 ? 64 : w->fmt == LP_NVFP4 ? 32 : 16;
+  const int64_t kmul = x->fmt == LP_MXFP4 ? 128 : x->fmt == LP_MXFP8 ? 64 : is_fp4(w->fmt) ? 32 : 16;
   if (x->cols % kmul || w->rows % 16) return LP_ERR_SHAPE;
   if (x->rows >= kMaxProductRows || x->cols >= kMaxProductCols || w->rows >= kMaxProductCols) return LP_ERR_SHAPE;
   if (!tiles_ok(x->rows / 128 + (groups ? groups : 1) + 1, w->rows)) return LP_ERR_SHAPE;
@@ -375,8 +376,8 @@ static lp_status check_fwd(const lp_qtensor* x, const lp_qtensor* w, void* y, in
 
 }  // extern "C"
 
-lp_status lp::check_forward(const lp_qtensor* x, const lp_qtensor* w, void* y, int64_t groups) {
-  return check_fwd(x, w, y, groups);
+lp_status lp::check_forward(const lp_qtensor* x, const lp_qtensor* w, void* y, int64_t groups, bool w4) {
+  return check_fwd(x, w, y, groups, w4);
 }
 
 extern "C" {

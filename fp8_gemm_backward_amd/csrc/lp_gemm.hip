@@ -449,6 +449,12 @@ hipError_t launch_fwd(const lp_qtensor& x, const lp_qtensor& w, const int32_t* o
   return fwd_dec(tail_params(prm), x.fmt, w.fmt, true, stream);
 }
 
+hipError_t launch_fwd_w4(const lp_qtensor& x, const lp_qtensor& w, const int32_t* offsets, int32_t groups, void* y,
+                         hipStream_t stream) {
+  const Params prm = fwd_params(x, w, offsets, groups, y);
+  return w4_fits(prm) ? w4_fwd(prm, w.fmt, stream) : launch_fwd(x, w, offsets, groups, y, stream);
+}
+
 hipError_t launch_fwd_dyn(const void* x, const lp_qtensor& xq, const lp_qtensor& w, const int32_t* offsets,
                           int32_t groups, void* x_codes, void* x_scales, void* y, hipStream_t stream) {
   const Params prm = fwd_params(xq, w, offsets, groups, y);

@@ -11,7 +11,8 @@
 // quantized operand is decoded to bf16 inside the contraction, as the
 // backward decodes it, and contracted on the bf16 MFMA with fp32 sums.  A
 // bf16 x with an NVFP4 weight is the same product with x decoded
-// beforehand (lp_dequant), once rather than in every tile that reads it.
+// beforehand (lp_dequant), once rather than in every tile that reads it; an
+// MXFP4 weight takes the same way in the 4-bit forward of many rows.
 #include "lp_gemm_kernel.hpp"
 
 namespace lp {
@@ -24,6 +25,9 @@ hipError_t fwd_dec(const Params& prm, int fmt_x, int fmt_w, bool narrow, hipStre
   if (fmt_x == LP_BF16 && fmt_w == LP_FP8_B128)
     return narrow ? run<Narrow, BF16, -1, FP8_B128, -1, false, true>(prm, s)
                   : run<Big, BF16, -1, FP8_B128, -1, false, true>(prm, s);
+  if (fmt_x == LP_BF16 && fmt_w == LP_MXFP4)
+    return narrow ? run<Narrow, BF16, -1, MXFP4, -1, false, true>(prm, s)
+                  : run<Big, BF16, -1, MXFP4, -1, false, true>(prm, s);
   if (fmt_x == LP_BF16 && fmt_w == LP_NVFP4)
     return narrow ? run<Narrow, BF16, -1, NVFP4, -1, false, true>(prm, s)
                   : run<Big, BF16, -1, NVFP4, -1, false, true>(prm, s);

@@ -284,7 +284,7 @@ struct Decoded {
   static constexpr int VMEM = PER * (kScale ? 2 : 1);                // vector-memory loads per slab
   static constexpr int QUARTERS = F == BF16 ? 1 : 4;                 // decode items per piece
   static constexpr int DECODES = PER * PIECES * QUARTERS;            // decode items per slab
-  static_assert(kKMajor ? ((F == MXFP8 && A == -1) || F == NVFP4 || F == FP8_B128) : true,
+  static_assert(kKMajor ? ((F == MXFP8 && A == -1) || F == MXFP4 || F == NVFP4 || F == FP8_B128) : true,
                 "k-major decode needs scales along the contraction");
 
   using Stage = Raw<F, A>[PER];
@@ -997,7 +997,7 @@ hipError_t dw_pt(const Params& prm, int fmt_p, int fmt_q, hipStream_t s);
 // both MXFP8.
 hipError_t fwd_mx(const Params& prm, bool fp4, hipStream_t s);
 // Forward y = x @ w^T through bf16 tiles (fused decode): bf16 x with a bf16
-// weight (256 x 128 tiles) or a block-FP8 or NVFP4 weight, NVFP4 x with an
+// weight (256 x 128 tiles) or a block-FP8, MXFP4 or NVFP4 weight, NVFP4 x with an
 // NVFP4 weight (256 x 256 tiles; 256 x 128 when narrow, the last round of a
 // split grouped call).
 hipError_t fwd_dec(const Params& prm, int fmt_x, int fmt_w, bool narrow, hipStream_t s);
@@ -1016,6 +1016,9 @@ constexpr int kFuseRows = 4;
 bool b128_skinny_fits(const Params& prm);
 hipError_t b128_fwd_skinny(const Params& prm, hipStream_t s);
 hipError_t b128_fwd_fused(const Params& prm, const void* x, hipStream_t s);
+// The forward of few rows of a bf16 x by an MXFP4 or NVFP4 weight.
+bool w4_fits(const Params& prm);
+hipError_t w4_fwd(const Params& prm, int fmt_w, hipStream_t s);
 hipError_t b128_dx(const Params& prm, int tile, hipStream_t s);
 hipError_t b128_dw(const Params& prm, int tile, hipStream_t s);
 // The last dispatch round in parts of tiles (Params::tail); grad_W: dense.

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "lp.h"
+#include "lp_moe.h"
 #include "lp_train.h"
 
 namespace lp {
@@ -134,7 +135,32 @@ struct AdamwCall {
 };
 hipError_t launch_adamw(const AdamwCall& c, hipStream_t stream);
 
-// The checks of lp_linear_fwd (groups 0) and lp_grouped_fwd (lp_api.hip).
-lp_status check_forward(const lp_qtensor* x, const lp_qtensor* w, void* y, int64_t groups);
+// The checks of lp_linear_fwd (groups 0) and lp_grouped_fwd (lp_api.hip); w4:
+// those of a bf16 x by a 4-bit weight instead.
+lp_status check_forward(const lp_qtensor* x, const lp_qtensor* w, void* y, int64_t groups, bool w4 = false);
+
+// Mixture of experts (lp_moe_gate.hip, lp_moe_sort.hip, lp_moe_rows.hip,
+// lp_r128.hip).
+hipError_t launch_moe_gate(const void* logits, bool bf16, int64_t tokens, int32_t experts, int32_t topk, bool renorm,
+                           float* weights, int32_t* chosen, hipStream_t s);
+hipError_t launch_moe_gate_bwd(const float* grad_w, const void* logits, bool bf16, int64_t tokens, int32_t experts,
+                               int32_t topk, bool renorm, const float* weights, const int32_t* chosen, void* grad_l,
+                               hipStream_t s);
+size_t moe_sort_workspace(int64_t pairs, int64_t groups);
+hipError_t launch_moe_sort(const int32_t* experts, int64_t pairs, int32_t groups, int32_t* offsets, int32_t* rows,
+                           int32_t* order, void* ws, hipStream_t s);
+hipError_t launch_moe_gather(const void* x, int64_t tokens, int64_t topk, int64_t cols, const int32_t* rows, void* y,
+                             hipStream_t s);
+hipError_t launch_moe_gather_quant(const void* x, int64_t tokens, int64_t topk, int64_t cols, const int32_t* order,
+                                   const float* weights, const int32_t* offsets, int64_t groups, void* codes_c,
+                                   void* scales_c, void* codes_r, void* scales_r, hipStream_t s);
+hipError_t launch_moe_combine(const void* y, int64_t tokens, int64_t topk, int64_t cols, const int32_t* rows,
+                              const float* weights, void* out, hipStream_t s);
+hipError_t launch_moe_combine_bwd(const void* grad, const void* y, int64_t tokens, int64_t topk, int64_t cols,
+                                  const int32_t* rows, const float* weights, void* grad_y, float* grad_w,
+                                  hipStream_t s);
+// The forward of a bf16 x by an MXFP4 or NVFP4 weight (lp_gemm.hip).
+hipError_t launch_fwd_w4(const lp_qtensor& x, const lp_qtensor& w, const int32_t* offsets, int32_t groups, void* y,
+                         hipStream_t s);
 
 }  // namespace lp

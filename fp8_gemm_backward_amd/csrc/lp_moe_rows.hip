@@ -1,0 +1,187 @@
+// Rows of tokens to their experts and back (HBM-bound).
+//
+//   gather:   y[rows[t][j]] = x[t]
+//   combine:  out[t] = sum_j w[t][j] y[rows[t][j]]
+//   backward: grad_y[rows[t][j]] = w[t][j] grad[t],  grad_w[t][j] = grad[t] . y[rows[t][j]]
+//
+// All of them by token: a token's row is read (or written) once and its k rows
+// written (read) from there, whichever way the indices point.
+#include "lp_device.hpp"
+#include "lp_internal.hpp"
+#include "lp_mxq.hpp"
+
+namespace lp {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int64_t kMaxBlocks = 1 << 20;
+constexpr int kSlots = 8;                      // rows in flight per thread
+
+struct RowArgs {
+  const uint16_t* x;
+  const uint16_t* y;
+  uint16_t* out;
+  float* grad_w;
+  const int32_t* rows;
+  const float* weights;
+  int64_t tokens;
+  int32_t k, pieces;                           // pieces of 8 columns in a row; tokens * pieces < 2^31
+  uint32_t M;
+  FastDiv per_row;                             // by pieces
+};
+
+__device__ __forceinline__ u32x4 load16(const uint16_t* base, int64_t row, int pieces, int c) {
+  return reinterpret_cast<const u32x4*>(base)[row * pieces + c];
+}
+
+__global__ __launch_bounds__(kThreads) void gather_kernel(RowArgs a) {
+  const uint32_t units = (uint32_t)a.tokens * a.pieces;
+  for (uint32_t u = blockIdx.x * kThreads + threadIdx.x; u < units; u += gridDim.x * kThreads) {
+    const uint32_t token = fdiv(u, a.per_row);
+    const int c = (int)(u - token * a.pieces);
+    const int64_t t = token;
+    const u32x4 v = load16(a.x, t, a.pieces, c);
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t r = (uint32_t)a.rows[t * a.k + j];
+      if (r < a.M) reinterpret_cast<u32x4*>(a.out)[(int64_t)r * a.pieces + c] = v;
+    }
+  }
+}
+
+template <bool kWeighted>
+__global__ __launch_bounds__(kThreads) void combine_kernel(RowArgs a) {
+  const uint32_t units = (uint32_t)a.tokens * a.pieces;
+  for (uint32_t u = blockIdx.x * kThreads + threadIdx.x; u < units; u += gridDim.x * kThreads) {
+    const uint32_t token = fdiv(u, a.per_row);
+    const int c = (int)(u - token * a.pieces);
+    const int64_t t = token;
+    float s[8] = {};
+    for (int j0 = 0; j0 < a.k; j0 += kSlots) {
+      u32x4 v[kSlots];
+      float w[kSlots];
+      uint32_t r[kSlots];
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        r[i] = j0 + i < a.k ? (uint32_t)a.rows[t * a.k + j0 + i] : ~0u;
+        w[i] = 1.0f;
+        if (r[i] >= a.M) continue;
+        v[i] = load16(a.y, r[i], a.pieces, c);
+        if constexpr (kWeighted) w[i] = a.weights[t * a.k + j0 + i];
+      }
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        if (r[i] >= a.M) continue;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          s[2 * d] = __builtin_fmaf(w[i], bf16_lo(v[i][d]), s[2 * d]);
+          s[2 * d + 1] = __builtin_fmaf(w[i], bf16_hi(v[i][d]), s[2 * d + 1]);
+        }
+      }
+    }
+    reinterpret_cast<u32x4*>(a.out)[u] =
+        u32x4{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7])};
+  }
+}
+
+// One workgroup per token: x is the token's gradient.
+template <bool kRows, bool kDots>
+__global__ __launch_bounds__(kThreads) void combine_bwd_kernel(RowArgs a) {
+  __shared__ float part[kThreads / 64][kSlots];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    for (int j0 = 0; j0 < a.k; j0 += kSlots) {
+      uint32_t r[kSlots];
+      float w[kSlots], dot[kSlots] = {};
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        r[i] = j0 + i < a.k ? (uint32_t)a.rows[t * a.k + j0 + i] : ~0u;
+        w[i] = kRows && a.weights != nullptr && j0 + i < a.k ? a.weights[t * a.k + j0 + i] : 1.0f;
+      }
+      for (int c = threadIdx.x; c < a.pieces; c += kThreads) {
+        const u32x4 g = load16(a.x, t, a.pieces, c);
+        float f[8];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          f[2 * d] = bf16_lo(g[d]);
+          f[2 * d + 1] = bf16_hi(g[d]);
+        }
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+          if (r[i] >= a.M) continue;
+          if constexpr (kDots) {
+            const u32x4 v = load16(a.y, r[i], a.pieces, c);
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              dot[i] = __builtin_fmaf(f[2 * d], bf16_lo(v[d]), dot[i]);
+              dot[i] = __builtin_fmaf(f[2 * d + 1], bf16_hi(v[d]), dot[i]);
+            }
+          }
+          if constexpr (kRows)
+            reinterpret_cast<u32x4*>(a.out)[(int64_t)r[i] * a.pieces + c] =
+                u32x4{pack_bf16x2(w[i] * f[0], w[i] * f[1]), pack_bf16x2(w[i] * f[2], w[i] * f[3]),
+                      pack_bf16x2(w[i] * f[4], w[i] * f[5]), pack_bf16x2(w[i] * f[6], w[i] * f[7])};
+        }
+      }
+      if constexpr (kDots) {
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+#pragma unroll
+          for (int d = 1; d < 64; d *= 2) dot[i] += __shfl_xor(dot[i], d);
+          if (lane == 0) part[wave][i] = dot[i];
+        }
+        __syncthreads();
+        if (threadIdx.x < kSlots && j0 + (int)threadIdx.x < a.k) {
+          float s = 0.0f;
+          for (int v = 0; v < kThreads / 64; ++v) s += part[v][threadIdx.x];
+          a.grad_w[t * a.k + j0 + threadIdx.x] = s;
+        }
+        __syncthreads();
+      }
+    }
+  }
+}
+
+RowArgs args(const void* x, const void* y, void* out, float* grad_w, const int32_t* rows, const float* weights,
+             int64_t tokens, int64_t topk, int64_t cols) {
+  return RowArgs{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(y), static_cast<uint16_t*>(out), grad_w,
+                 rows, weights, tokens, (int32_t)topk, (int32_t)(cols / 8), (uint32_t)(tokens * topk),
+                 make_fastdiv((uint32_t)(cols >= 8 ? cols / 8 : 1))};
+}
+dim3 grid_of(int64_t blocks) { return dim3((uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks)); }
+
+}  // namespace
+
+hipError_t launch_moe_gather(const void* x, int64_t tokens, int64_t topk, int64_t cols, const int32_t* rows, void* y,
+                             hipStream_t s) {
+  const RowArgs a = args(x, nullptr, y, nullptr, rows, nullptr, tokens, topk, cols);
+  gather_kernel<<<grid_of((tokens * a.pieces + kThreads - 1) / kThreads), dim3(kThreads), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const void* y, int64_t tokens, int64_t topk, int64_t cols, const int32_t* rows,
+                              const float* weights, void* out, hipStream_t s) {
+  const RowArgs a = args(nullptr, y, out, nullptr, rows, weights, tokens, topk, cols);
+  const dim3 grid = grid_of((tokens * a.pieces + kThreads - 1) / kThreads);
+  if (weights != nullptr)
+    combine_kernel<true><<<grid, dim3(kThreads), 0, s>>>(a);
+  else
+    combine_kernel<false><<<grid, dim3(kThreads), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_bwd(const void* grad, const void* y, int64_t tokens, int64_t topk, int64_t cols,
+                                  const int32_t* rows, const float* weights, void* grad_y, float* grad_w,
+                                  hipStream_t s) {
+  const RowArgs a = args(grad, y, grad_y, grad_w, rows, weights, tokens, topk, cols);
+  const dim3 grid = grid_of(tokens), block(kThreads);
+  if (grad_y != nullptr && grad_w != nullptr)
+    combine_bwd_kernel<true, true><<<grid, block, 0, s>>>(a);
+  else if (grad_y != nullptr)
+    combine_bwd_kernel<true, false><<<grid, block, 0, s>>>(a);
+  else
+    combine_bwd_kernel<false, true><<<grid, block, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace lp

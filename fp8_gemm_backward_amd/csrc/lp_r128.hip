@@ -72,6 +72,16 @@ __device__ __forceinline__ void run_rows(const int32_t* __restrict__ offsets, in
   }
 }
 
+// Rows that come from elsewhere: row r is row order[r] / k of src, times
+// weights[order[r]] when there are weights, rounded to bf16; zeros when order[r]
+// is no pair.
+struct RowMap {
+  const int32_t* order;
+  const float* weights;
+  FastDiv k;
+  uint32_t pairs;
+};
+
 // One 128 x 128 tile per workgroup, for runs along the rows (kRows), along
 // both axes (kRows and kCols) or one scale for the tile (neither).  Thread
 // 16 i + c holds rows i + 32 k (k = 0..3) of columns 8 c .. 8 c + 7, so that
@@ -93,8 +103,8 @@ struct TileArgs {
 
 constexpr int kTileThreads = 512, kTileWaves = kTileThreads / 64, kStep = kTileThreads / 16, kTileRows = kRunLen / kStep;
 
-template <bool kCols, bool kRows>
-__global__ __launch_bounds__(kTileThreads) void r128_tile(TileArgs a) {
+template <bool kCols, bool kRows, bool kMap = false>
+__global__ __launch_bounds__(kTileThreads) void r128_tile(TileArgs a, RowMap map) {
   __shared__ alignas(16) uint16_t s_max[kTileWaves][kRunLen];
   __shared__ alignas(16) float s_scale[kRunLen], s_recip[kRunLen];
   const uint32_t rtile = fdiv(blockIdx.x, a.col_tiles);
@@ -114,8 +124,19 @@ __global__ __launch_bounds__(kTileThreads) void r128_tile(TileArgs a) {
 #pragma unroll
   for (int k = 0; k < kTileRows; ++k) {
     const int r = ri + kStep * k;
-    v[k] = col_ok && r0 + r < r1 ? *reinterpret_cast<const u32x4*>(a.src + base + (int64_t)r * a.cols)
-                                 : u32x4{0u, 0u, 0u, 0u};
+    if constexpr (kMap) {
+      const uint32_t pair = r0 + r < r1 ? (uint32_t)map.order[r0 + r] : ~0u;
+      v[k] = u32x4{0u, 0u, 0u, 0u};
+      if (!col_ok || pair >= map.pairs) continue;
+      v[k] = *reinterpret_cast<const u32x4*>(a.src + (int64_t)fdiv(pair, map.k) * a.cols + c);
+      if (map.weights == nullptr) continue;
+      const float w = map.weights[pair];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) v[k][d] = pack_bf16x2(w * bf16_lo(v[k][d]), w * bf16_hi(v[k][d]));
+    } else {
+      v[k] = col_ok && r0 + r < r1 ? *reinterpret_cast<const u32x4*>(a.src + base + (int64_t)r * a.cols)
+                                   : u32x4{0u, 0u, 0u, 0u};
+    }
   }
   // Column maxima (bf16 magnitude pairs).
   u32x4 cm = {0u, 0u, 0u, 0u};
@@ -225,11 +246,23 @@ hipError_t launch_r128_tiles(const void* src, int64_t batch, int64_t rows, int64
                    (int32_t)rows, (int32_t)cols, make_fastdiv((uint32_t)ct), make_fastdiv((uint32_t)rt)};
   const dim3 grid((uint32_t)(batch * rt * ct)), block(kTileThreads);
   if (codes_r == nullptr)
-    r128_tile<false, false><<<grid, block, 0, stream>>>(a);
+    r128_tile<false, false><<<grid, block, 0, stream>>>(a, RowMap{});
   else if (codes_c == nullptr)
-    r128_tile<false, true><<<grid, block, 0, stream>>>(a);
+    r128_tile<false, true><<<grid, block, 0, stream>>>(a, RowMap{});
   else
-    r128_tile<true, true><<<grid, block, 0, stream>>>(a);
+    r128_tile<true, true><<<grid, block, 0, stream>>>(a, RowMap{});
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_gather_quant(const void* x, int64_t tokens, int64_t topk, int64_t cols, const int32_t* order,
+                                   const float* weights, const int32_t* offsets, int64_t groups, void* codes_c,
+                                   void* scales_c, void* codes_r, void* scales_r, hipStream_t stream) {
+  const int64_t rows = tokens * topk, ct = (cols + kRunLen - 1) / kRunLen, rt = rows / kRunLen + groups;
+  const TileArgs a{static_cast<const uint16_t*>(x), static_cast<uint8_t*>(codes_c), static_cast<uint8_t*>(codes_r),
+                   static_cast<float*>(scales_c), static_cast<float*>(scales_r), offsets, (int32_t)groups,
+                   (int32_t)rows, (int32_t)cols, make_fastdiv((uint32_t)ct), make_fastdiv((uint32_t)rt)};
+  r128_tile<true, true, true><<<dim3((uint32_t)(rt * ct)), dim3(kTileThreads), 0, stream>>>(
+      a, RowMap{order, weights, make_fastdiv((uint32_t)topk), (uint32_t)rows});
   return hipGetLastError();
 }
 

@@ -28,8 +28,10 @@ Pins (tests/test_oracle_*.py, all CPU):
   AstrAI page, triple-loop GEMMs with the scales applied to the sums.
 * training (train.py): hand-made runs and blocks of the quantization rule,
   run indices of groups written out, the AdamW formula in scalars.
+* mixture of experts (moe.py): the gate's gradient against differences, the
+  sort against its definition, gather and combine as adjoints.
 
 Parity unpinned by the source documents: the E2M1 nibble order and the NVFP4
 tensor-scale reading (see formats.py).
 """
-from . import formats, gemm, pertensor, train  # noqa: F401
+from . import formats, gemm, moe, pertensor, train  # noqa: F401
