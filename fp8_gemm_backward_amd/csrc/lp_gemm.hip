@@ -452,7 +452,9 @@ hipError_t launch_fwd(const lp_qtensor& x, const lp_qtensor& w, const int32_t* o
 hipError_t launch_fwd_w4(const lp_qtensor& x, const lp_qtensor& w, const int32_t* offsets, int32_t groups, void* y,
                          hipStream_t stream) {
   const Params prm = fwd_params(x, w, offsets, groups, y);
-  return w4_fits(prm) ? w4_fwd(prm, w.fmt, stream) : launch_fwd(x, w, offsets, groups, y, stream);
+  bool done = false;
+  const hipError_t e = w4_fwd(prm, w.fmt, &done, stream);
+  return done ? e : launch_fwd(x, w, offsets, groups, y, stream);
 }
 
 hipError_t launch_fwd_dyn(const void* x, const lp_qtensor& xq, const lp_qtensor& w, const int32_t* offsets,

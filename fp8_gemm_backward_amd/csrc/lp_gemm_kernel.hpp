@@ -1016,9 +1016,9 @@ constexpr int kFuseRows = 4;
 bool b128_skinny_fits(const Params& prm);
 hipError_t b128_fwd_skinny(const Params& prm, hipStream_t s);
 hipError_t b128_fwd_fused(const Params& prm, const void* x, hipStream_t s);
-// The forward of few rows of a bf16 x by an MXFP4 or NVFP4 weight.
-bool w4_fits(const Params& prm);
-hipError_t w4_fwd(const Params& prm, int fmt_w, hipStream_t s);
+// The forward of few rows of a bf16 x by an MXFP4 or NVFP4 weight; done: false when
+// fwd_dec is estimated to be faster (nothing is launched then).
+hipError_t w4_fwd(const Params& prm, int fmt_w, bool* done, hipStream_t s);
 hipError_t b128_dx(const Params& prm, int tile, hipStream_t s);
 hipError_t b128_dw(const Params& prm, int tile, hipStream_t s);
 // The last dispatch round in parts of tiles (Params::tail); grad_W: dense.
