@@ -38,53 +38,61 @@ constexpr int kPitch = 80;                      // LDS bytes of a row's scales: 
 
 struct W4Args {
   Params p;
-  int32_t row_tiles, col_tiles;                 // of the grid; col_tiles: in eighths
+  int32_t row_tiles, col_tiles;                 // row_tiles: dense calls
 };
 
-// The j-th entry of the list of (column, row tile) pairs in which the row tiles
-// of a column follow each other: its row tile is number j % live of the live row
-// tiles (kRows rows of one group).  Every wave looks at 64 groups at a time, one a lane.
-struct RowTile {
-  int g, start, end, live;
+// Row tiles (kRows rows of one group) of a grouped call.  Every wave looks at 64
+// groups at a time, one a lane: their ends, starts and row tiles, and the row tiles
+// up to each.
+struct Groups64 {
+  int end, start, tiles, upto;
 };
 template <int kRows>
-__device__ __forceinline__ RowTile row_tile(const int32_t* offsets, int groups, int M, int j) {
+__device__ __forceinline__ Groups64 groups64(const int32_t* offsets, int groups, int M, int base, int end0, int seen) {
   const int lane = threadIdx.x & 63;
-  auto scan64 = [&](int base, int end0, int seen0, int& e, int& start, int& n, int& upto) __attribute__((always_inline)) {
-    e = base + lane < groups ? offsets[base + lane] : 0;
-    e = e > M ? M : e;
-    e = e < end0 ? end0 : e;
-    e = wave_scan(e, [](int a, int b) { return a > b ? a : b; });
-    start = __shfl_up(e, 1);
-    start = lane == 0 ? end0 : start;
-    n = (e - start + kRows - 1) / kRows;
-    upto = seen0 + wave_scan(n, [](int a, int b) { return a + b; });
-  };
-  RowTile t{0, 0, 0, 0};
-  int e, start, n, upto, end0 = 0, seen = 0;
+  Groups64 s;
+  int e = base + lane < groups ? offsets[base + lane] : 0;
+  e = e > M ? M : e;
+  e = e < end0 ? end0 : e;
+  s.end = wave_scan(e, [](int a, int b) { return a > b ? a : b; });
+  s.start = __shfl_up(s.end, 1);
+  s.start = lane == 0 ? end0 : s.start;
+  s.tiles = (s.end - s.start + kRows - 1) / kRows;
+  s.upto = seen + wave_scan(s.tiles, [](int a, int b) { return a + b; });
+  return s;
+}
+
+// How many there are.
+template <int kRows>
+__device__ __forceinline__ int live_tiles(const int32_t* offsets, int groups, int M) {
+  int end0 = 0, seen = 0;
   for (int base = 0; base < groups; base += 64) {
-    scan64(base, end0, seen, e, start, n, upto);
-    end0 = __builtin_amdgcn_readlane(e, 63);
-    seen = __builtin_amdgcn_readlane(upto, 63);
+    const Groups64 s = groups64<kRows>(offsets, groups, M, base, end0, seen);
+    end0 = __builtin_amdgcn_readlane(s.end, 63);
+    seen = __builtin_amdgcn_readlane(s.upto, 63);
   }
-  t.live = seen;
-  if (seen == 0) return t;
-  const int rt = j % seen;
-  end0 = seen = 0;
+  return seen;
+}
+
+// The rt-th of them (rt below their number).
+struct RowTile {
+  int g, start, end;
+};
+template <int kRows>
+__device__ __forceinline__ RowTile row_tile(const int32_t* offsets, int groups, int M, int rt) {
+  int end0 = 0, seen = 0;
   for (int base = 0; base < groups; base += 64) {
-    if (groups > 64) scan64(base, end0, seen, e, start, n, upto);
-    const uint64_t own = __ballot(upto > rt);
+    const Groups64 s = groups64<kRows>(offsets, groups, M, base, end0, seen);
+    const uint64_t own = __ballot(s.upto > rt);
     if (own != 0) {
       const int l = __builtin_ctzll(own);
-      t.g = base + l;
-      t.end = __builtin_amdgcn_readlane(e, l);
-      t.start = __builtin_amdgcn_readlane(start, l) + (rt - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l))) * kRows;
-      return t;
+      const int before = __builtin_amdgcn_readlane(s.upto, l) - __builtin_amdgcn_readlane(s.tiles, l);
+      return RowTile{base + l, __builtin_amdgcn_readlane(s.start, l) + (rt - before) * kRows, __builtin_amdgcn_readlane(s.end, l)};
     }
-    end0 = __builtin_amdgcn_readlane(e, 63);
-    seen = __builtin_amdgcn_readlane(upto, 63);
+    end0 = __builtin_amdgcn_readlane(s.end, 63);
+    seen = __builtin_amdgcn_readlane(s.upto, 63);
   }
-  return t;
+  return RowTile{0, 0, 0};
 }
 
 // Where the 16-byte chunk 4 h + q (of the 16 of a step) of row r lies in LDS:
@@ -117,22 +125,22 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kEu)))
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wk = wave % kWK, wn = wave / kWK;
-  // Workgroups are dealt to the 8 XCDs in turn: the row tiles of one column
-  // tile share an XCD, whose L2 then serves the weight's second reads.
-  const int xcd = blockIdx.x % 8, j = blockIdx.x / 8;
-  const int rt = j % a.row_tiles;
-  int n0 = (((j / a.row_tiles) * 8 + xcd) * WN + wn) * 16 * kNC;
+  // Tiles in the order of columns, then row tiles.  Workgroups are dealt to the 8
+  // XCDs in turn; XCD x takes the x-th eighth of the tiles, so that the row tiles
+  // of a column share its L2, which then serves the weight's second reads.
+  const int xcd = blockIdx.x % 8, at = blockIdx.x / 8;
+  int live = a.row_tiles;
+  if (p.offsets != nullptr) live = live_tiles<kRows>(p.offsets, p.groups, p.Ptot);
+  const int tiles = live * a.col_tiles, eighth = (tiles + 7) / 8, tile = xcd * eighth + at;
+  if (at >= eighth || tile >= tiles) return;
+  const int col = tile / live, rt = tile - col * live, n0 = (col * WN + wn) * 16 * kNC;
   int g = 0, p0 = rt * kRows, pend = p.Ptot;
   if (p.offsets != nullptr) {
-    const RowTile t = row_tile<kRows>(p.offsets, p.groups, p.Ptot, j);
-    const int col = t.live > 0 ? j / t.live : 0;
+    const RowTile t = row_tile<kRows>(p.offsets, p.groups, p.Ptot, rt);
     g = t.g;
     p0 = t.start;
     pend = t.end;
-    n0 = ((col * 8 + xcd) * WN + wn) * 16 * kNC;
-    if (col >= a.col_tiles) return;
   }
-  if (p0 >= pend) return;
 
   const int K = p.Ktot, N = p.Qtot;
   const int r = lane & 15, h = lane >> 4;
@@ -297,23 +305,25 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kEu)))
 }
 
 // The instantiated shapes of a workgroup, and their times in units of 10 ns:
-// fixed, a step (128 of a wave's part of the contraction) of the first 256
-// workgroups and of every further 256, measured at 2048 and 4096 deep contractions,
-// 64 to 1536 workgroups, weights from HBM.
+// fixed, and for every round of 256 workgroups (the first one, each further one) a
+// step of a wave's part of the contraction and, each further one, a fixed time too.
+// Fitted to 260 measured problems (1 to 4096 rows, dense and up to 64 groups,
+// weights from HBM, both formats) with 7 to 19% of scatter: the shape they choose
+// is within 4% of the fastest of 20 on average, 1.75 times at worst.
 struct Shape {
   int8_t wk, nc, rt;
-  int16_t fixed, step, more;
+  int16_t fixed, step, more, round;
 };
 constexpr Shape kShapes[] = {
-    {8, 1, 1, 390, 115, 138},  {4, 2, 1, 390, 118, 131}, {1, 2, 1, 460, 84, 94},    {4, 1, 2, 480, 68, 110},
-    {2, 2, 2, 610, 99, 123},   {1, 2, 2, 530, 93, 107},  {4, 2, 4, 470, 190, 200},  {2, 2, 4, 910, 115, 160},
-    {1, 2, 4, 840, 110, 130},  {1, 1, 6, 880, 91, 93},   {1, 2, 7, 880, 164, 190},  {1, 2, 8, 1060, 175, 210},
-    {2, 2, 8, 970, 195, 240},
+    {8, 1, 1, 308, 54, 83, 60},    {4, 1, 1, 403, 41, 54, 263},   {2, 1, 1, 412, 36, 43, 300},   {1, 2, 1, 338, 57, 70, 145},
+    {4, 1, 2, 430, 65, 83, 259},   {2, 1, 2, 428, 50, 59, 286},   {1, 2, 2, 376, 68, 82, 150},   {4, 2, 3, 461, 111, 137, 313},
+    {2, 2, 4, 515, 106, 130, 451}, {1, 2, 4, 404, 94, 92, 317},   {1, 1, 6, 380, 88, 63, 224},   {1, 2, 7, 504, 137, 144, 587},
+    {1, 2, 8, 465, 151, 163, 548},
 };
 constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
 // The same of the 256 x 256 tiles that decode into LDS; their matrix cores, busier,
 // run at a lower clock when every CU has a tile.
-constexpr int kTileFixed = 800, kTileStep = 300, kTileStepFull = 410;
+constexpr int kTileFixed = 800, kTileStep = 280, kTileStepFull = 410;
 
 // Row tiles of a call: an upper bound; expected: about what grouped rows make (a
 // group with rows has one tile at least, and half of one to spare on average).
@@ -337,9 +347,9 @@ int choose(const Params& p) {
   for (int i = 0; i < kShapeCount; ++i) {
     const Shape& s = kShapes[i];
     // (a launch has fewer than 2^32 threads)
-    if (row_tiles(p, 16 * s.rt) * (col_tiles(p, s) + 7) >= (int64_t)1 << 23) continue;
+    if (row_tiles(p, 16 * s.rt) * col_tiles(p, s) + 8 > (int64_t)1 << 23) continue;
     const int64_t rounds = (row_tiles(p, 16 * s.rt, true) * col_tiles(p, s) + kCUs - 1) / kCUs;
-    const int64_t t = s.fixed + (steps + s.wk - 1) / s.wk * (s.step + (rounds - 1) * s.more);
+    const int64_t t = s.fixed + (rounds - 1) * s.round + (steps + s.wk - 1) / s.wk * (s.step + (rounds - 1) * s.more);
     if (t < least) {
       least = t;
       best = i;
@@ -347,35 +357,36 @@ int choose(const Params& p) {
   }
   const int64_t tiles = row_tiles(p, 256, true) * ((p.Qtot + 255) / 256);
   const int64_t t = kTileFixed + steps * (tiles <= kCUs / 2 ? kTileStep : kTileStepFull * ((tiles + kCUs - 1) / kCUs));
-  return best >= 0 && least <= t ? best : -1;
+  // (the fit is low by about a quarter where there are many rounds of many rows)
+  return best >= 0 && least + least / 4 <= t ? best : -1;
 }
 
-template <int F, int kWK, int kNC, int kRT, int kDepth, int kXS, int kEu = 2>
-hipError_t launch(W4Args a, int shape, hipStream_t s) {
-  const int64_t rt = row_tiles(a.p, 16 * kRT), nt = (col_tiles(a.p, kShapes[shape]) + 7) / 8;
+template <int F, int kIndex, int kDepth, int kXS, int kEu = 2>
+hipError_t launch(W4Args a, hipStream_t s) {
+  constexpr Shape kS = kShapes[kIndex];
+  const int64_t rt = row_tiles(a.p, 16 * kS.rt), nt = col_tiles(a.p, kS);
   a.row_tiles = (int32_t)rt;
   a.col_tiles = (int32_t)nt;
-  w4_kernel<F, kWK, kNC, kRT, kDepth, kXS, kEu><<<dim3((uint32_t)(rt * nt * 8)), dim3(kThreads), 0, s>>>(a);
+  w4_kernel<F, kS.wk, kS.nc, kS.rt, kDepth, kXS, kEu><<<dim3((uint32_t)((rt * nt + 7) / 8 * 8)), dim3(kThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 
-// (in the order of kShapes)
 template <int F>
 hipError_t launch_shape(const W4Args& a, int shape, hipStream_t s) {
   switch (shape) {
-    case 0: return launch<F, 8, 1, 1, 2, 0>(a, shape, s);
-    case 1: return launch<F, 4, 2, 1, 2, 3>(a, shape, s);
-    case 2: return launch<F, 1, 2, 1, 2, 6>(a, shape, s);
-    case 3: return launch<F, 4, 1, 2, 2, 2>(a, shape, s);
-    case 4: return launch<F, 2, 2, 2, 2, 3>(a, shape, s);
-    case 5: return launch<F, 1, 2, 2, 2, 3>(a, shape, s);
-    case 6: return launch<F, 4, 2, 4, 2, 1>(a, shape, s);
-    case 7: return launch<F, 2, 2, 4, 2, 2>(a, shape, s);
-    case 8: return launch<F, 1, 2, 4, 2, 1, 4>(a, shape, s);
-    case 9: return launch<F, 1, 1, 6, 3, 1, 4>(a, shape, s);
-    case 10: return launch<F, 1, 2, 7, 2, 2>(a, shape, s);
-    case 11: return launch<F, 1, 2, 8, 2, 1>(a, shape, s);
-    default: return launch<F, 2, 2, 8, 2, 1>(a, shape, s);
+    case 0: return launch<F, 0, 2, 0>(a, s);
+    case 1: return launch<F, 1, 2, 3>(a, s);
+    case 2: return launch<F, 2, 3, 6>(a, s);
+    case 3: return launch<F, 3, 2, 6>(a, s);
+    case 4: return launch<F, 4, 2, 2>(a, s);
+    case 5: return launch<F, 5, 3, 3>(a, s);
+    case 6: return launch<F, 6, 3, 3>(a, s);
+    case 7: return launch<F, 7, 2, 1>(a, s);
+    case 8: return launch<F, 8, 2, 2>(a, s);
+    case 9: return launch<F, 9, 2, 1, 4>(a, s);
+    case 10: return launch<F, 10, 3, 1, 4>(a, s);
+    case 11: return launch<F, 11, 2, 2>(a, s);
+    default: return launch<F, 12, 2, 1>(a, s);
   }
 }
 

@@ -57,6 +57,26 @@ def test_linear(lp, fmt, M, N, K):
     assert torch.equal(y, lp.lp_linear_fwd_w4(x, w))                 # the same bits again
 
 
+# Sizes that take each of the workgroup shapes in turn, then the large tiles.
+DENSE = [(16, 16, 32), (101, 608, 160), (175, 768, 160), (853, 80, 32), (1394, 144, 320), (2207, 112, 416), (2634, 288, 32),
+         (2329, 288, 480), (3214, 528, 448), (306, 8832, 32), (289, 6464, 32), (388, 9472, 288), (517, 7216, 32), (1106, 7200, 32)]
+GROUPED = [(3, 16, 32, 2), (34, 128, 160, 33), (282, 496, 160, 2), (109, 592, 32, 2), (2269, 96, 320, 9), (2222, 128, 416, 5),
+           (4076, 80, 64, 33), (3927, 80, 288, 70), (2960, 528, 480, 5), (456, 3904, 32, 9), (3396, 304, 32, 70), (836, 4640, 288, 2),
+           (1390, 1616, 32, 33), (3223, 2336, 32, 5)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K", DENSE)
+def test_every_shape_of_a_workgroup(lp, fmt, M, N, K):
+    test_linear(lp, fmt, M, N, K)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K,G", GROUPED)
+def test_every_shape_of_a_workgroup_grouped(lp, fmt, M, N, K, G):
+    test_grouped(lp, fmt, M, N, K, G, "uneven")
+
+
 def spread(rng, M, G, kind):
     if kind == "empty":
         return np.zeros(G, np.int64)
