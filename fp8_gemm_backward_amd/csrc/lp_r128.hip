@@ -1,6 +1,8 @@
 // Quantization of bf16 to E4M3 with an fp32 scale per run of 128 (along the
 // columns, along the rows, or both from one read) or per 128 x 128 block
 // (HBM-bound, bit-exact; the arithmetic is in lp_r128.hpp).
+#include <type_traits>
+
 #include "lp_internal.hpp"
 #include "lp_r128.hpp"
 
@@ -11,11 +13,20 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRunLen = 128;
 
+// f(0), f(1), f(2), f(3), each with a constant.
+template <class F>
+__device__ __forceinline__ void static_for4(F&& f) {
+  f(std::integral_constant<int, 0>{});
+  f(std::integral_constant<int, 1>{});
+  f(std::integral_constant<int, 2>{});
+  f(std::integral_constant<int, 3>{});
+}
+
 // Runs along the columns.  Sixteen lanes hold a run, eight values each, and
 // take its largest magnitude with lane-row rotations.  A workgroup takes 16
 // rows x 4 runs: a row's four runs are 1 KiB in a line, and the 16 rows'
 // scales of one run index are 64 bytes in a line ([run][row]).  8192 x 4096 in
-// 17.6 us (5.7 TB/s), 24 x 2048 in 3.2 us (a launch).
+// 17.1 us (5.9 TB/s), 24 x 2048 in 2.7 us (a launch).
 constexpr int kRunRows = 16, kRunCols = 4;
 
 __global__ __launch_bounds__(kThreads) void r128_cols(const uint16_t* __restrict__ src, uint8_t* __restrict__ codes,
@@ -47,7 +58,7 @@ __global__ __launch_bounds__(kThreads) void r128_cols(const uint16_t* __restrict
 // start_g / 128 + g onwards, 128 rows each, the last one cut at the group's
 // end.  Run indices between two groups' ranges have no rows.  Every wave
 // looks at 64 groups at a time, one a lane (walking them one by one cost
-// 32768 x 2048 in 64 groups 79 us along both axes, this 54).
+// 32768 x 2048 in 64 groups 79 us along both axes, this 54 then and 45 now).
 __device__ __forceinline__ void run_rows(const int32_t* __restrict__ offsets, int groups, int M, int run, int& r0,
                                          int& r1) {
   const int lane = threadIdx.x & 63;
@@ -72,16 +83,6 @@ __device__ __forceinline__ void run_rows(const int32_t* __restrict__ offsets, in
   }
 }
 
-// Rows that come from elsewhere: row r is row order[r] / k of src, times
-// weights[order[r]] when there are weights, rounded to bf16; zeros when order[r]
-// is no pair.
-struct RowMap {
-  const int32_t* order;
-  const float* weights;
-  FastDiv k;
-  uint32_t pairs;
-};
-
 // One 128 x 128 tile per workgroup, for runs along the rows (kRows), along
 // both axes (kRows and kCols) or one scale for the tile (neither).  Thread
 // 16 i + c holds rows i + 32 k (k = 0..3) of columns 8 c .. 8 c + 7, so that
@@ -89,9 +90,10 @@ struct RowMap {
 // taken over its 16 lanes, a column's over the thread's four rows, the four
 // lane rows of the wave and, through LDS, the eight waves.  One thread per
 // column then makes its scale while the others go on with the runs along the
-// columns.  512 threads a tile: both axes of 1000 x 2064 in 5.8 us, 8192 x
-// 4096 in 26.9 (5.0 TB/s); 256 threads 7.0 and 27.4, 1024 threads 5.7 and 29.0.
-// With every thread making the scales of its eight columns: 6.2 and 27.7.
+// columns.  Both axes of 1000 x 2064 in 4.6 us, of 8192 x 4096 in 23.0 (5.8 TB/s).
+// Before the two-instruction quotients, 5.4 and 26.5, 256 threads took 1.2 and 0.5
+// more, 1024 threads 0.1 less and 2.1 more, and every thread making the scales of
+// its eight columns 0.4 and 0.8 more.
 struct TileArgs {
   const uint16_t* src;
   uint8_t *codes_c, *codes_r;
@@ -103,42 +105,68 @@ struct TileArgs {
 
 constexpr int kTileThreads = 512, kTileWaves = kTileThreads / 64, kStep = kTileThreads / 16, kTileRows = kRunLen / kStep;
 
-template <bool kCols, bool kRows, bool kMap = false>
-__global__ __launch_bounds__(kTileThreads) void r128_tile(TileArgs a, RowMap map) {
-  __shared__ alignas(16) uint16_t s_max[kTileWaves][kRunLen];
-  __shared__ alignas(16) float s_scale[kRunLen], s_recip[kRunLen];
-  const uint32_t rtile = fdiv(blockIdx.x, a.col_tiles);
-  const int ct = blockIdx.x - rtile * a.col_tiles.d;
-  const uint32_t b = fdiv(rtile, a.row_tiles);
-  const int rb = rtile - b * a.row_tiles.d;
-  int r0 = rb * kRunLen, r1 = r0 + kRunLen < a.rows ? r0 + kRunLen : a.rows;
-  if (a.offsets != nullptr) {
-    run_rows(a.offsets, a.groups, a.rows, rb, r0, r1);
-    if (r1 == r0) return;
-  }
+// kStream: past the caches, where the next kernel would not find them anyway.
+template <bool kStream>
+__device__ __forceinline__ void store_codes(uint8_t* to, u32x2 o) {
+  if constexpr (kStream) __builtin_nontemporal_store(o, reinterpret_cast<u32x2*>(to));
+  else *reinterpret_cast<u32x2*>(to) = o;
+}
+
+// 128 rows and columns, offsets inside which take 32 bits.
+__device__ __forceinline__ bool is_full(const TileArgs& a, int rows, int ct) {
+  return rows == kRunLen && ct < a.cols / kRunLen && a.cols < 1 << 25;
+}
+
+// What a tile's threads share.
+struct TileLds {
+  alignas(16) uint16_t max[kTileWaves][kRunLen];
+  alignas(16) float r[kRunLen], l[kRunLen];                // of the runs along the rows (RunRecip)
+  uint32_t bad[kRunLen / 64];                              // whether one of 64 columns has a bad run
+};
+
+__device__ __forceinline__ float bf16_at(u32x4 v, int e) { return e % 2 ? bf16_hi(v[e / 2]) : bf16_lo(v[e / 2]); }
+
+// The values of lane k of each 16, in all of them.
+template <int k>
+__device__ __forceinline__ float row16_lane(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x150 + k, 0xF, 0xF, true));   // row_newbcast:k
+}
+__device__ __forceinline__ uint32_t quad_xor1(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true);      // quad_perm:[1,0,3,2]
+}
+__device__ __forceinline__ uint32_t quad_xor2(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true);      // quad_perm:[2,3,0,1]
+}
+
+// Four maxima over 16 lanes: lane i gets the one of m[i % 4].
+__device__ __forceinline__ uint32_t row16_max4(const uint32_t (&m)[4], int i) {
+  const bool b0 = i & 1, b1 = i & 2;
+  const uint32_t p = umax(b0 ? m[1] : m[0], quad_xor1(b0 ? m[0] : m[1]));
+  const uint32_t q = umax(b0 ? m[3] : m[2], quad_xor1(b0 ? m[2] : m[3]));
+  uint32_t t = umax(b1 ? q : p, quad_xor2(b1 ? p : q));
+  t = umax(t, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)t, 0x128, 0xF, 0xF, true));   // row_ror:8
+  return umax(t, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)t, 0x124, 0xF, 0xF, true));   // row_ror:4
+}
+
+// The tile of rows r0 .. r1 (at most 128; kFull, see is_full: 128 rows and columns) and column
+// tile ct of batch entry b, whose run (block) along the rows is number rb; v: the
+// thread's values.  The two ways of quantizing take 340 vector instructions for a
+// thread's 32 values, which bounds tiles that come out of a cache; hence the
+// four rows' scales made side by side in four lanes, a column's
+// by one thread, and bad runs patched in a branch of their own.
+template <bool kCols, bool kRows, bool kFull, bool kStream = false>
+__device__ __forceinline__ void quant_tile(const TileArgs& a, TileLds& sh, u32x4 (&v)[kTileRows], int64_t b, int rb, int ct,
+                                           int r0, int r1) {
+  static_assert(kTileRows == 4, "a lane of four for each row");
   const int tid = threadIdx.x, ci = tid & 15, ri = tid >> 4, wave = tid >> 6;
-  const int c = ct * kRunLen + 8 * ci;
-  const bool col_ok = c < a.cols;
-  const int64_t base = ((int64_t)b * a.rows + r0) * a.cols + c;
-  u32x4 v[kTileRows];
-#pragma unroll
-  for (int k = 0; k < kTileRows; ++k) {
-    const int r = ri + kStep * k;
-    if constexpr (kMap) {
-      const uint32_t pair = r0 + r < r1 ? (uint32_t)map.order[r0 + r] : ~0u;
-      v[k] = u32x4{0u, 0u, 0u, 0u};
-      if (!col_ok || pair >= map.pairs) continue;
-      v[k] = *reinterpret_cast<const u32x4*>(a.src + (int64_t)fdiv(pair, map.k) * a.cols + c);
-      if (map.weights == nullptr) continue;
-      const float w = map.weights[pair];
-#pragma unroll
-      for (int d = 0; d < 4; ++d) v[k][d] = pack_bf16x2(w * bf16_lo(v[k][d]), w * bf16_hi(v[k][d]));
-    } else {
-      v[k] = col_ok && r0 + r < r1 ? *reinterpret_cast<const u32x4*>(a.src + base + (int64_t)r * a.cols)
-                                   : u32x4{0u, 0u, 0u, 0u};
-    }
-  }
-  // Column maxima (bf16 magnitude pairs).
+  const bool col_ok = kFull || ct * kRunLen + 8 * ci < a.cols;
+  const int n = kFull ? kRunLen : r1 - r0;
+  const int64_t corner = (b * a.rows + r0) * a.cols + ct * kRunLen;       // (uniform)
+  using Off = std::conditional_t<kFull, uint32_t, uint64_t>;
+  const Off off = (Off)ri * (Off)a.cols + 8 * ci, step = (Off)kStep * (Off)a.cols;
+  auto stored = [&](int k) { return kFull || (col_ok && ri + kStep * k < n); };
+  auto empty = [&](int k) { return !kFull && kStep * k >= n; };           // no row of the tile (uniform): groups of few rows
+  // Magnitudes' maxima per column (bf16 pairs).
   u32x4 cm = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int k = 0; k < kTileRows; ++k)
@@ -149,64 +177,85 @@ __global__ __launch_bounds__(kTileThreads) void r128_tile(TileArgs a, RowMap map
     cm[d] = pk_umax16(cm[d], (uint32_t)__shfl_xor((int)cm[d], 16));
     cm[d] = pk_umax16(cm[d], (uint32_t)__shfl_xor((int)cm[d], 32));
   }
-  if ((tid & 63) < 16) *reinterpret_cast<u32x4*>(&s_max[wave][8 * ci]) = cm;
+  if ((tid & 63) < 16) *reinterpret_cast<u32x4*>(&sh.max[wave][8 * ci]) = cm;
   __syncthreads();
   if constexpr (kRows) {
     if (tid < kRunLen) {                                   // one column's scale per thread
       uint32_t m = 0;
 #pragma unroll
-      for (int w = 0; w < kTileWaves; ++w) m = umax(m, s_max[w][tid]);
+      for (int w = 0; w < kTileWaves; ++w) m = umax(m, sh.max[w][tid]);
       const RunScale q = run_scale(m << 16);
-      s_scale[tid] = q.s;
-      s_recip[tid] = q.r;
-      if (ct * kRunLen + tid < a.cols)
+      const RunRecip p = run_recip(q.s, q.r);
+      sh.r[tid] = p.r;
+      sh.l[tid] = q.bad ? __builtin_nanf("") : p.l;
+      const bool any = __ballot(q.bad) != 0;
+      if ((tid & 63) == 0) sh.bad[wave] = any;
+      if (kFull || ct * kRunLen + tid < a.cols)
         a.scales_r[((int64_t)b * a.row_tiles.d + rb) * a.cols + ct * kRunLen + tid] = q.s;
     }
   }
-  if constexpr (kCols) {
+  if constexpr (kCols || kRows) {
+    if constexpr (kCols) {
+      uint32_t m[kTileRows];
 #pragma unroll
-    for (int k = 0; k < kTileRows; ++k) {
-      const int r = ri + kStep * k;
-      const RunScale q = run_scale(row16_max(amax8(v[k])));
-      if (r0 + r >= r1) continue;
-      if (ci == 0) a.scales_c[((int64_t)b * a.col_tiles.d + ct) * a.rows + r0 + r] = q.s;
-      if (col_ok) *reinterpret_cast<u32x2*>(a.codes_c + base + (int64_t)r * a.cols) = run_codes8(v[k], q);
-    }
-  }
-  if constexpr (kRows) {
-    __syncthreads();
-    RunScale q[8];
-    bool bad = false;
+      for (int k = 0; k < kTileRows; ++k) m[k] = amax8(v[k]);
+      const RunScale q = run_scale(row16_max4(m, ci));     // row ri + kStep (ci % 4)
+      const RunRecip p = run_recip(q.s, q.r);
+      if (ci < kTileRows && (kFull || ri + kStep * ci < n))
+        a.scales_c[((int64_t)b * a.col_tiles.d + ct) * a.rows + r0 + ri + kStep * ci] = q.s;
+      const bool any = __ballot(q.bad) != 0;
+      uint8_t* const to = a.codes_c + corner;
+      static_for4([&](auto kk) __attribute__((always_inline)) {
+        constexpr int k = decltype(kk)::value;
+        if (empty(k)) return;
+        const RunRecip pk{row16_lane<k>(p.r), row16_lane<k>(p.l)};
+        float t[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      q[e].s = s_scale[8 * ci + e];
-      q[e].r = s_recip[8 * ci + e];
-      q[e].bad = __builtin_isnan(q[e].s);
-      bad |= q[e].bad;
-    }
-#pragma unroll
-    for (int k = 0; k < kTileRows; ++k) {
-      const int r = ri + kStep * k;
-      uint32_t o[2];
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const uint32_t w0 = v[k][2 * d], w1 = v[k][2 * d + 1];
-        o[d] = to_e4m3x2(run_div(bf16_lo(w0), q[4 * d]), run_div(bf16_hi(w0), q[4 * d + 1])) |
-               (to_e4m3x2(run_div(bf16_lo(w1), q[4 * d + 2]), run_div(bf16_hi(w1), q[4 * d + 3])) << 16);
-        if (__builtin_expect(bad, false)) {
-          const uint32_t nan = nan_e4m3x2(w0) | (nan_e4m3x2(w1) << 16);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (q[4 * d + e].bad) o[d] = (o[d] & ~(0xFFu << (8 * e))) | (nan & (0xFFu << (8 * e)));
+        for (int e = 0; e < 8; ++e) t[e] = run_div_bf16(bf16_at(v[k], e), pk);
+        u32x2 o{codes4_unclamped(t[0], t[1], t[2], t[3]), codes4_unclamped(t[4], t[5], t[6], t[7])};
+        if (__builtin_expect(any, false)) {
+          if (row16_lane<k>(q.bad ? 1.0f : 0.0f) != 0.0f)
+            o = u32x2{nan_e4m3x2(v[k][0]) | (nan_e4m3x2(v[k][1]) << 16), nan_e4m3x2(v[k][2]) | (nan_e4m3x2(v[k][3]) << 16)};
         }
-      }
-      if (col_ok && r0 + r < r1) *reinterpret_cast<u32x2*>(a.codes_r + base + (int64_t)r * a.cols) = u32x2{o[0], o[1]};
+        if (stored(k)) store_codes<kStream>(to + (off + k * step), o);
+        __builtin_amdgcn_sched_barrier(0);                 // (a row at a time: fewer registers)
+      });
     }
-  }
-  if constexpr (!kCols && !kRows) {
+    if constexpr (kRows) {
+      __syncthreads();
+      // (The values are unpacked anew: kept unpacked they took 32 registers more, and
+      // with them a workgroup less per CU.)
+#pragma unroll
+      for (int k = 0; k < kTileRows; ++k) asm volatile("" : "+v"(v[k]));
+      RunRecip q[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = RunRecip{sh.r[8 * ci + e], sh.l[8 * ci + e]};
+      const bool any = (sh.bad[0] | sh.bad[1]) != 0;
+      uint8_t* const to = a.codes_r + corner;
+#pragma unroll
+      for (int k = 0; k < kTileRows; ++k) {
+        if (empty(k)) break;
+        float t[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = run_div_bf16(bf16_at(v[k], e), q[e]);
+        u32x2 o{codes4_unclamped(t[0], t[1], t[2], t[3]), codes4_unclamped(t[4], t[5], t[6], t[7])};
+        if (__builtin_expect(any, false)) {
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            const uint32_t nan = nan_e4m3x2(v[k][2 * d]) | (nan_e4m3x2(v[k][2 * d + 1]) << 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (__builtin_isnan(q[4 * d + e].l)) o[d] = (o[d] & ~(0xFFu << (8 * e))) | (nan & (0xFFu << (8 * e)));
+          }
+        }
+        if (stored(k)) store_codes<kStream>(to + (off + k * step), o);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  } else {
 #pragma unroll
     for (int w = 0; w < kTileWaves; ++w) {
-      const u32x4 o = *reinterpret_cast<const u32x4*>(&s_max[w][8 * ci]);
+      const u32x4 o = *reinterpret_cast<const u32x4*>(&sh.max[w][8 * ci]);
 #pragma unroll
       for (int d = 0; d < 4; ++d) cm[d] = pk_umax16(cm[d], o[d]);
     }
@@ -216,12 +265,84 @@ __global__ __launch_bounds__(kTileThreads) void r128_tile(TileArgs a, RowMap map
     const RunScale q = run_scale(row16_max(m) << 16);
     if (tid == 0) a.scales_c[((int64_t)b * a.row_tiles.d + rb) * a.col_tiles.d + ct] = q.s;
 #pragma unroll
-    for (int k = 0; k < kTileRows; ++k) {
-      const int r = ri + kStep * k;
-      if (col_ok && r0 + r < r1)
-        *reinterpret_cast<u32x2*>(a.codes_c + base + (int64_t)r * a.cols) = run_codes8(v[k], q);
-    }
+    for (int k = 0; k < kTileRows; ++k)
+      if (stored(k)) *reinterpret_cast<u32x2*>(a.codes_c + corner + (off + k * step)) = run_codes8_bf16(v[k], q);
   }
+}
+
+template <bool kCols, bool kRows>
+__global__ __launch_bounds__(kTileThreads) void r128_tile(TileArgs a) {
+  __shared__ TileLds sh;
+  const uint32_t rtile = fdiv(blockIdx.x, a.col_tiles);
+  const int ct = blockIdx.x - rtile * a.col_tiles.d;
+  const uint32_t b = fdiv(rtile, a.row_tiles);
+  const int rb = rtile - b * a.row_tiles.d;
+  int r0 = rb * kRunLen, r1 = r0 + kRunLen < a.rows ? r0 + kRunLen : a.rows;
+  if (a.offsets != nullptr) {
+    run_rows(a.offsets, a.groups, a.rows, rb, r0, r1);
+    if (r1 == r0) return;
+  }
+  const int c = ct * kRunLen + 8 * (threadIdx.x & 15), ri = threadIdx.x >> 4;
+  const int64_t base = ((int64_t)b * a.rows + r0) * a.cols + c;
+  u32x4 v[kTileRows];
+#pragma unroll
+  for (int k = 0; k < kTileRows; ++k) {
+    const int r = ri + kStep * k;
+    v[k] = c < a.cols && r0 + r < r1 ? *reinterpret_cast<const u32x4*>(a.src + base + (int64_t)r * a.cols)
+                                     : u32x4{0u, 0u, 0u, 0u};
+  }
+  if (is_full(a, r1 - r0, ct))
+    quant_tile<kCols, kRows, true>(a, sh, v, b, rb, ct, r0, r1);
+  else
+    quant_tile<kCols, kRows, false>(a, sh, v, b, rb, ct, r0, r1);
+}
+
+// Results larger than a quarter of the 256 MB cache are stored past the caches: 4096
+// tokens to 8 experts each, 7168 wide, read x (59 MB, each row k times) faster from a
+// cache that 470 MB of codes do not wash through, 118 us in all (150).
+constexpr int64_t kCacheBytes = (int64_t)64 << 20;
+
+// Rows that come from elsewhere: row r is row order[r] / k of src, times
+// weights[order[r]] when kWeighted, rounded to bf16; zeros when order[r] is no pair.
+struct RowMap {
+  const int32_t* order;
+  const float* weights;
+  FastDiv k;
+  uint32_t pairs;
+};
+
+template <bool kWeighted, bool kStream>
+__global__ __launch_bounds__(kTileThreads) void r128_mapped(TileArgs a, RowMap map) {
+  __shared__ TileLds sh;
+  const int rb = fdiv(blockIdx.x, a.col_tiles), ct = blockIdx.x - rb * a.col_tiles.d;
+  int r0, r1;
+  run_rows(a.offsets, a.groups, a.rows, rb, r0, r1);
+  if (r1 == r0) return;
+  const int c = ct * kRunLen + 8 * (threadIdx.x & 15), r = r0 + (threadIdx.x >> 4);
+  uint32_t pair[kTileRows];
+#pragma unroll
+  for (int k = 0; k < kTileRows; ++k) {
+    pair[k] = r + kStep * k < r1 ? (uint32_t)map.order[r + kStep * k] : ~0u;
+    if (pair[k] >= map.pairs || c >= a.cols) pair[k] = ~0u;
+  }
+  u32x4 v[kTileRows];
+  float w[kTileRows];
+#pragma unroll
+  for (int k = 0; k < kTileRows; ++k) {
+    v[k] = u32x4{0u, 0u, 0u, 0u};
+    if (pair[k] != ~0u) v[k] = *reinterpret_cast<const u32x4*>(a.src + (int64_t)fdiv(pair[k], map.k) * a.cols + c);
+    if constexpr (kWeighted) w[k] = pair[k] != ~0u ? map.weights[pair[k]] : 0.0f;
+  }
+  if constexpr (kWeighted) {
+#pragma unroll
+    for (int k = 0; k < kTileRows; ++k)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) v[k][d] = pack_bf16x2(w[k] * bf16_lo(v[k][d]), w[k] * bf16_hi(v[k][d]));
+  }
+  if (is_full(a, r1 - r0, ct))
+    quant_tile<true, true, true, kStream>(a, sh, v, 0, rb, ct, r0, r1);
+  else
+    quant_tile<true, true, false, kStream>(a, sh, v, 0, rb, ct, r0, r1);
 }
 
 }  // namespace
@@ -246,11 +367,11 @@ hipError_t launch_r128_tiles(const void* src, int64_t batch, int64_t rows, int64
                    (int32_t)rows, (int32_t)cols, make_fastdiv((uint32_t)ct), make_fastdiv((uint32_t)rt)};
   const dim3 grid((uint32_t)(batch * rt * ct)), block(kTileThreads);
   if (codes_r == nullptr)
-    r128_tile<false, false><<<grid, block, 0, stream>>>(a, RowMap{});
+    r128_tile<false, false><<<grid, block, 0, stream>>>(a);
   else if (codes_c == nullptr)
-    r128_tile<false, true><<<grid, block, 0, stream>>>(a, RowMap{});
+    r128_tile<false, true><<<grid, block, 0, stream>>>(a);
   else
-    r128_tile<true, true><<<grid, block, 0, stream>>>(a, RowMap{});
+    r128_tile<true, true><<<grid, block, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -261,8 +382,13 @@ hipError_t launch_moe_gather_quant(const void* x, int64_t tokens, int64_t topk, 
   const TileArgs a{static_cast<const uint16_t*>(x), static_cast<uint8_t*>(codes_c), static_cast<uint8_t*>(codes_r),
                    static_cast<float*>(scales_c), static_cast<float*>(scales_r), offsets, (int32_t)groups,
                    (int32_t)rows, (int32_t)cols, make_fastdiv((uint32_t)ct), make_fastdiv((uint32_t)rt)};
-  r128_tile<true, true, true><<<dim3((uint32_t)(rt * ct)), dim3(kTileThreads), 0, stream>>>(
-      a, RowMap{order, weights, make_fastdiv((uint32_t)topk), (uint32_t)rows});
+  const RowMap map{order, weights, make_fastdiv((uint32_t)topk), (uint32_t)rows};
+  const dim3 grid((uint32_t)(rt * ct)), block(kTileThreads);
+  const bool past = 2 * rows * cols > kCacheBytes;
+  if (weights != nullptr)
+    past ? r128_mapped<true, true><<<grid, block, 0, stream>>>(a, map) : r128_mapped<true, false><<<grid, block, 0, stream>>>(a, map);
+  else
+    past ? r128_mapped<false, true><<<grid, block, 0, stream>>>(a, map) : r128_mapped<false, false><<<grid, block, 0, stream>>>(a, map);
   return hipGetLastError();
 }
 

@@ -60,6 +60,32 @@ __device__ __forceinline__ uint32_t run_codes4(float a, float b, float c, float 
   return to_e4m3x2(run_div(a, q), run_div(b, q)) | (to_e4m3x2(run_div(c, q), run_div(d, q)) << 16);
 }
 
+// The codes of bf16 values under the scale of a bf16 maximum a take less: the
+// quotient by r + l, the reciprocal rounded down and its residual, in two
+// operations.  v * 448 / a is either a tie between two codes or at least 2^-13 of
+// itself away from one, so that only ties need the quotient's last bits; the codes
+// are those of run_div for every pair of significands at every distance of the
+// exponents (3 million pairs compared, at the ends of the exponents' range too).
+// l >= 0 leaves a negative zero's sign alone.  No quotient of a finite set exceeds 448
+// by more than its last bit, which rounds to 448: nothing to clamp.
+struct RunRecip {
+  float r, l;
+};
+__device__ __forceinline__ RunRecip run_recip(float s, float nearest) {
+  const bool above = __builtin_fmaf(-s, nearest, 1.0f) < 0.0f;
+  const float r = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, nearest) - (above ? 1u : 0u));
+  return RunRecip{r, __builtin_fmaf(-s, r, 1.0f) * r};
+}
+__device__ __forceinline__ float run_div_bf16(float v, const RunRecip& q) { return __builtin_fmaf(v, q.r, v * q.l); }
+
+// Four quotients of at most 448 -> four codes (first in the low byte).
+__device__ __forceinline__ uint32_t codes4_unclamped(float a, float b, float c, float d) {
+  i16x2 o = __builtin_bit_cast(i16x2, __builtin_nondeterministic_value(0u));   // (both halves are written below)
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, a, b, 1.0f, false);
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, c, d, 1.0f, true);
+  return __builtin_bit_cast(uint32_t, o);
+}
+
 // Maximum over the 16 lanes of a lane row.
 __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
   v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false));   // row_ror:8
@@ -82,6 +108,14 @@ __device__ __forceinline__ u32x2 run_codes8(u32x4 v, const RunScale& q) {
   if (q.bad) return u32x2{nan_e4m3x2(v[0]) | (nan_e4m3x2(v[1]) << 16), nan_e4m3x2(v[2]) | (nan_e4m3x2(v[3]) << 16)};
   return u32x2{run_codes4(bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1]), q),
                run_codes4(bf16_lo(v[2]), bf16_hi(v[2]), bf16_lo(v[3]), bf16_hi(v[3]), q)};
+}
+
+// The same of finite values whose largest magnitude, a bf16 too, made the scale.
+__device__ __forceinline__ u32x2 run_codes8_bf16(u32x4 v, const RunScale& q) {
+  if (q.bad) return u32x2{nan_e4m3x2(v[0]) | (nan_e4m3x2(v[1]) << 16), nan_e4m3x2(v[2]) | (nan_e4m3x2(v[3]) << 16)};
+  const RunRecip p = run_recip(q.s, q.r);
+  auto at = [&](int i) { return run_div_bf16(i % 2 ? bf16_hi(v[i / 2]) : bf16_lo(v[i / 2]), p); };
+  return u32x2{codes4_unclamped(at(0), at(1), at(2), at(3)), codes4_unclamped(at(4), at(5), at(6), at(7))};
 }
 
 }  // namespace lp
