@@ -105,6 +105,13 @@ __device__ __forceinline__ uint32_t fix_nan_pair(uint32_t v, uint32_t sign_lo, u
   return lo | (hi << 16);
 }
 
+// Orders the wave's LDS accesses before it ahead of those after it.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Inclusive scan over the wave by DPP shifts inside the lane rows and
 // broadcasts across them.
 template <class F>
