@@ -6,6 +6,8 @@
 //
 // All of them by token: a token's row is read (or written) once and its k rows
 // written (read) from there, whichever way the indices point.
+#include <type_traits>
+
 #include "lp_device.hpp"
 #include "lp_internal.hpp"
 #include "lp_mxq.hpp"
@@ -16,7 +18,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int64_t kMaxBlocks = 1 << 20;
-constexpr int kSlots = 8;                      // rows in flight per thread
 
 struct RowArgs {
   const uint16_t* x;
@@ -31,10 +32,29 @@ struct RowArgs {
   FastDiv per_row;                             // by pieces
 };
 
+// Rows (of all experts) of more than a quarter of the 256 MB cache are read and
+// written past the caches: what runs between their writing and reading, an
+// expert's weights at least, leaves little of them there.  32768 rows of 7168 copied
+// in 91 us (5.8 TB/s; 103 by way of the caches), summed by eights in 93 (104), 16384
+// rows of 4096 in 30 and 35 (39 and 40).
+constexpr int64_t kCacheBytes = (int64_t)64 << 20;
+
 __device__ __forceinline__ u32x4 load16(const uint16_t* base, int64_t row, int pieces, int c) {
   return reinterpret_cast<const u32x4*>(base)[row * pieces + c];
 }
+template <bool kStream>
+__device__ __forceinline__ u32x4 load_row(const uint16_t* base, int64_t row, int pieces, int c) {
+  const u32x4* p = reinterpret_cast<const u32x4*>(base) + row * pieces + c;
+  return kStream ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool kStream>
+__device__ __forceinline__ void store_row(uint16_t* base, int64_t row, int pieces, int c, u32x4 v) {
+  u32x4* p = reinterpret_cast<u32x4*>(base) + row * pieces + c;
+  if constexpr (kStream) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
 
+template <bool kStream>
 __global__ __launch_bounds__(kThreads) void gather_kernel(RowArgs a) {
   const uint32_t units = (uint32_t)a.tokens * a.pieces;
   for (uint32_t u = blockIdx.x * kThreads + threadIdx.x; u < units; u += gridDim.x * kThreads) {
@@ -44,12 +64,12 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(RowArgs a) {
     const u32x4 v = load16(a.x, t, a.pieces, c);
     for (int j = 0; j < a.k; ++j) {
       const uint32_t r = (uint32_t)a.rows[t * a.k + j];
-      if (r < a.M) reinterpret_cast<u32x4*>(a.out)[(int64_t)r * a.pieces + c] = v;
+      if (r < a.M) store_row<kStream>(a.out, r, a.pieces, c, v);
     }
   }
 }
 
-template <bool kWeighted>
+template <bool kWeighted, bool kStream, int kSlots>             // kSlots: rows in flight per thread
 __global__ __launch_bounds__(kThreads) void combine_kernel(RowArgs a) {
   const uint32_t units = (uint32_t)a.tokens * a.pieces;
   for (uint32_t u = blockIdx.x * kThreads + threadIdx.x; u < units; u += gridDim.x * kThreads) {
@@ -66,7 +86,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(RowArgs a) {
         r[i] = j0 + i < a.k ? (uint32_t)a.rows[t * a.k + j0 + i] : ~0u;
         w[i] = 1.0f;
         if (r[i] >= a.M) continue;
-        v[i] = load16(a.y, r[i], a.pieces, c);
+        v[i] = load_row<kStream>(a.y, r[i], a.pieces, c);
         if constexpr (kWeighted) w[i] = a.weights[t * a.k + j0 + i];
       }
 #pragma unroll
@@ -85,7 +105,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(RowArgs a) {
 }
 
 // One workgroup per token: x is the token's gradient.
-template <bool kRows, bool kDots>
+template <bool kRows, bool kDots, bool kStream, int kSlots, int kThreads>
 __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(RowArgs a) {
   __shared__ float part[kThreads / 64][kSlots];
   const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
@@ -110,7 +130,7 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(RowArgs a) {
         for (int i = 0; i < kSlots; ++i) {
           if (r[i] >= a.M) continue;
           if constexpr (kDots) {
-            const u32x4 v = load16(a.y, r[i], a.pieces, c);
+            const u32x4 v = load_row<kStream>(a.y, r[i], a.pieces, c);
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
               dot[i] = __builtin_fmaf(f[2 * d], bf16_lo(v[d]), dot[i]);
@@ -118,9 +138,9 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(RowArgs a) {
             }
           }
           if constexpr (kRows)
-            reinterpret_cast<u32x4*>(a.out)[(int64_t)r[i] * a.pieces + c] =
-                u32x4{pack_bf16x2(w[i] * f[0], w[i] * f[1]), pack_bf16x2(w[i] * f[2], w[i] * f[3]),
-                      pack_bf16x2(w[i] * f[4], w[i] * f[5]), pack_bf16x2(w[i] * f[6], w[i] * f[7])};
+            store_row<kStream>(a.out, r[i], a.pieces, c,
+                               u32x4{pack_bf16x2(w[i] * f[0], w[i] * f[1]), pack_bf16x2(w[i] * f[2], w[i] * f[3]),
+                                     pack_bf16x2(w[i] * f[4], w[i] * f[5]), pack_bf16x2(w[i] * f[6], w[i] * f[7])});
         }
       }
       if constexpr (kDots) {
@@ -148,14 +168,43 @@ RowArgs args(const void* x, const void* y, void* out, float* grad_w, const int32
                  rows, weights, tokens, (int32_t)topk, (int32_t)(cols / 8), (uint32_t)(tokens * topk),
                  make_fastdiv((uint32_t)(cols >= 8 ? cols / 8 : 1))};
 }
+bool streams(const RowArgs& a) { return (int64_t)a.M * a.pieces * 16 > kCacheBytes; }
 dim3 grid_of(int64_t blocks) { return dim3((uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks)); }
+
+// f with the rows in flight for k slots a token: no more than there are, at most 8
+// (2048 tokens of 1040 with 4 rows backwards: 10.1 us by 4, 14.7 by 8).
+template <class F>
+void by_slots(int64_t k, F&& f) {
+  if (k <= 2) f(std::integral_constant<int, 2>{});
+  else if (k <= 4) f(std::integral_constant<int, 4>{});
+  else f(std::integral_constant<int, 8>{});
+}
+
+// Fewer tokens than fill the GPU with workgroups of 256 threads get 1024 threads each
+// (256 tokens of 7168 with 8 rows: 13.6 us, 18.6 by 256 threads).
+constexpr int64_t kFewTokens = 1024;
+
+template <bool kStream, int kThreads>
+void bwd(const RowArgs& a, hipStream_t s) {
+  by_slots(a.k, [&](auto slots) {
+    constexpr int kSlots = decltype(slots)::value;
+    const dim3 grid = grid_of(a.tokens), block(kThreads);
+    if (a.out != nullptr && a.grad_w != nullptr)
+      combine_bwd_kernel<true, true, kStream, kSlots, kThreads><<<grid, block, 0, s>>>(a);
+    else if (a.out != nullptr)
+      combine_bwd_kernel<true, false, kStream, kSlots, kThreads><<<grid, block, 0, s>>>(a);
+    else
+      combine_bwd_kernel<false, true, kStream, kSlots, kThreads><<<grid, block, 0, s>>>(a);
+  });
+}
 
 }  // namespace
 
 hipError_t launch_moe_gather(const void* x, int64_t tokens, int64_t topk, int64_t cols, const int32_t* rows, void* y,
                              hipStream_t s) {
   const RowArgs a = args(x, nullptr, y, nullptr, rows, nullptr, tokens, topk, cols);
-  gather_kernel<<<grid_of((tokens * a.pieces + kThreads - 1) / kThreads), dim3(kThreads), 0, s>>>(a);
+  const dim3 grid = grid_of((tokens * a.pieces + kThreads - 1) / kThreads);
+  streams(a) ? gather_kernel<true><<<grid, dim3(kThreads), 0, s>>>(a) : gather_kernel<false><<<grid, dim3(kThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -163,10 +212,15 @@ hipError_t launch_moe_combine(const void* y, int64_t tokens, int64_t topk, int64
                               const float* weights, void* out, hipStream_t s) {
   const RowArgs a = args(nullptr, y, out, nullptr, rows, weights, tokens, topk, cols);
   const dim3 grid = grid_of((tokens * a.pieces + kThreads - 1) / kThreads);
-  if (weights != nullptr)
-    combine_kernel<true><<<grid, dim3(kThreads), 0, s>>>(a);
-  else
-    combine_kernel<false><<<grid, dim3(kThreads), 0, s>>>(a);
+  const auto run = [&](auto slots) {
+    constexpr int kSlots = decltype(slots)::value;
+    const dim3 block(kThreads);
+    if (weights != nullptr)
+      streams(a) ? combine_kernel<true, true, kSlots><<<grid, block, 0, s>>>(a) : combine_kernel<true, false, kSlots><<<grid, block, 0, s>>>(a);
+    else
+      streams(a) ? combine_kernel<false, true, kSlots><<<grid, block, 0, s>>>(a) : combine_kernel<false, false, kSlots><<<grid, block, 0, s>>>(a);
+  };
+  by_slots(topk, run);
   return hipGetLastError();
 }
 
@@ -174,13 +228,9 @@ hipError_t launch_moe_combine_bwd(const void* grad, const void* y, int64_t token
                                   const int32_t* rows, const float* weights, void* grad_y, float* grad_w,
                                   hipStream_t s) {
   const RowArgs a = args(grad, y, grad_y, grad_w, rows, weights, tokens, topk, cols);
-  const dim3 grid = grid_of(tokens), block(kThreads);
-  if (grad_y != nullptr && grad_w != nullptr)
-    combine_bwd_kernel<true, true><<<grid, block, 0, s>>>(a);
-  else if (grad_y != nullptr)
-    combine_bwd_kernel<true, false><<<grid, block, 0, s>>>(a);
-  else
-    combine_bwd_kernel<false, true><<<grid, block, 0, s>>>(a);
+  if (streams(a)) bwd<true, kThreads>(a, s);
+  else if (tokens < kFewTokens && a.pieces > kThreads) bwd<false, 1024>(a, s);
+  else bwd<false, kThreads>(a, s);
   return hipGetLastError();
 }
 
