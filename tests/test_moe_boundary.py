@@ -59,7 +59,8 @@ def test_sort_workspace():
     for pairs, groups in ((-1, 4), (1 << 30, 4), (8, 0), (8, 1025)):
         assert need(pairs, groups) == (SHAPE, 0)
     assert need(0, 4) == (OK, 0) and need(96, 64) == (OK, 0)
-    big = [need(n, 256)[1] for n in (1 << 16, 1 << 20, (1 << 30) - 1)]
+    assert need(1 << 16, 256) == (OK, 0)                 # (one launch, which needs none)
+    big = [need(n, 256)[1] for n in ((1 << 16) + 1, 1 << 20, (1 << 30) - 1)]
     assert 0 < big[0] < big[1] < big[2]
 
 
