@@ -119,6 +119,30 @@ def test_gate_bwd_ignores_experts_out_of_range(lp):
 
 
 @pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T,E,k", [(6, 40, 5), (9, 256, 8), (3, 700, 20), (2, 5, 3)])
+def test_gate_bwd_of_an_expert_chosen_twice(lp, T, E, k, renorm):
+    """Slots of one expert add up: w_j (g_j - sum w g) each, or p_i times their g and once the inner product."""
+    rng = np.random.default_rng(T)
+    lv, g = rng.standard_normal((T, E)).astype(np.float32), rng.standard_normal((T, k)).astype(np.float32)
+    e, w = rng.integers(0, min(E, 4), (T, k)).astype(np.int32), rng.random((T, k)).astype(np.float32)
+    e[0, 0], w[0, 0] = -1, np.nan
+    got = lp.lp_moe_gate_bwd(dev(g), dev(lv), dev(w), dev(e), renorm=renorm).cpu().numpy().astype(np.float64)
+    w64, g64 = np.where(e >= 0, w, 0).astype(np.float64), g.astype(np.float64)
+    inner = (w64 * g64).sum(1)
+    p = np.exp(lv.astype(np.float64) - lv.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    want = np.zeros((T, E)) if renorm else -p * inner[:, None]
+    size = np.zeros((T, E)) if renorm else p * (w64 * np.abs(g64)).sum(1)[:, None]
+    for t in range(T):
+        for j in range(k):
+            if e[t, j] >= 0:
+                # (without renorm the slots' weights are the softmax's; here any, and each counts as it is)
+                want[t, e[t, j]] += w64[t, j] * (g64[t, j] - inner[t] if renorm else g64[t, j])
+                size[t, e[t, j]] += w64[t, j] * (abs(g64[t, j]) + (w64[t] * np.abs(g64[t])).sum())
+    assert (np.abs(got - want) <= (2 * gate_rtol(lv, E) + (k + 8) * U32) * size + U32 * np.abs(want) + 1e-37).all()
+
+
+@pytest.mark.parametrize("renorm", [False, True])
 def test_gate_gradient_against_differences(lp, renorm):
     """Central differences of fp32 weights with a step of 2^-7: truncation (third derivatives at most 2 of a probability)
     below 2 h^2 / 6, rounding 2 rtol / (2 h)."""
