@@ -327,17 +327,23 @@ __global__ __launch_bounds__(kTileThreads) void r128_mapped(TileArgs a, RowMap m
   }
   u32x4 v[kTileRows];
   float w[kTileRows];
+  // (weights by no branch: one between two rows' loads has the second wait for the first)
+  if constexpr (kWeighted) {
+#pragma unroll
+    for (int k = 0; k < kTileRows; ++k) w[k] = map.weights[pair[k] != ~0u ? pair[k] : 0];
+  }
 #pragma unroll
   for (int k = 0; k < kTileRows; ++k) {
     v[k] = u32x4{0u, 0u, 0u, 0u};
     if (pair[k] != ~0u) v[k] = *reinterpret_cast<const u32x4*>(a.src + (int64_t)fdiv(pair[k], map.k) * a.cols + c);
-    if constexpr (kWeighted) w[k] = pair[k] != ~0u ? map.weights[pair[k]] : 0.0f;
   }
   if constexpr (kWeighted) {
 #pragma unroll
-    for (int k = 0; k < kTileRows; ++k)
+    for (int k = 0; k < kTileRows; ++k) {
+      w[k] = pair[k] != ~0u ? w[k] : 0.0f;
 #pragma unroll
       for (int d = 0; d < 4; ++d) v[k][d] = pack_bf16x2(w[k] * bf16_lo(v[k][d]), w[k] * bf16_hi(v[k][d]));
+    }
   }
   if (is_full(a, r1 - r0, ct))
     quant_tile<true, true, true, kStream>(a, sh, v, 0, rb, ct, r0, r1);

@@ -365,3 +365,22 @@ def test_gather_quant_of_pairs_out_of_range(lp):
     plain = lp.lp_moe_gather(x, dev(rows.reshape(T, k)))
     plain[[0, 31, 79]] = 0
     same_runs(lp, lp.lp_moe_gather_quant(x, dev(bad), off, k), lp.lp_r128_quant_dual(plain, off), off, H)
+
+
+@pytest.mark.parametrize("H", [128, 144])
+def test_gather_quant_of_pairs_out_of_range_beside_a_nan_weight(lp, H):
+    """Pair 0's NaN reaches its own row's runs only, neither a row of no pair nor one past the group's end."""
+    T, k = 40, 2
+    rng = np.random.default_rng(4)
+    off = torch.tensor([30, 75], dtype=torch.int32, device="cuda")
+    order = rng.permutation(T * k).astype(np.int32)
+    bad = order.copy()
+    bad[[1, 33, 74]] = -1, T * k, -(1 << 31)
+    x, w = bf16_dev(bits(rng, (T, H))), rng.random((T, k)).astype(np.float32)
+    for value in (0.5, np.nan, np.inf):
+        w[0, 0] = value
+        rows = np.empty(T * k, np.int32)
+        rows[order] = np.arange(T * k)
+        plain = lp.lp_moe_combine_bwd(x, None, dev(rows.reshape(T, k)), dev(w), need_dw=False)[0]
+        plain[[1, 33, 74]] = 0
+        same_runs(lp, lp.lp_moe_gather_quant(x, dev(bad), off, k, weights=dev(w)), lp.lp_r128_quant_dual(plain, off), off, H)
