@@ -104,12 +104,23 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(RowArgs a) {
   }
 }
 
-// One workgroup per token: x is the token's gradient.
-template <bool kRows, bool kDots, bool kStream, int kSlots, int kThreads>
-__global__ __launch_bounds__(kThreads) void combine_bwd_kernel(RowArgs a) {
-  __shared__ float part[kThreads / 64][kSlots];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+// Sum over groups of kLanes lanes, in all of them.
+template <int kLanes>
+__device__ __forceinline__ float sum_lanes(float v) {
+#pragma unroll
+  for (int d = 1; d < kLanes; d *= 2) v += __shfl_xor(v, d);
+  return v;
+}
+
+// kOwn threads per token (of a workgroup of at least kThreads): x is the token's
+// gradient.
+template <bool kRows, bool kDots, bool kStream, int kSlots, int kOwn>
+__global__ __launch_bounds__(kOwn < kThreads ? kThreads : kOwn) void combine_bwd_kernel(RowArgs a) {
+  constexpr int kTokens = kOwn < kThreads ? kThreads / kOwn : 1, kLanes = kOwn < 64 ? kOwn : 64;
+  static_assert(kOwn <= 64 || kTokens == 1);
+  __shared__ float part[kOwn / kLanes][kSlots];
+  const int own = threadIdx.x % kOwn, lane = own % kLanes, wave = own / kLanes;
+  for (int64_t t = (int64_t)blockIdx.x * kTokens + threadIdx.x / kOwn; t < a.tokens; t += (int64_t)gridDim.x * kTokens) {
     for (int j0 = 0; j0 < a.k; j0 += kSlots) {
       uint32_t r[kSlots];
       float w[kSlots], dot[kSlots] = {};
@@ -118,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(RowArgs a) {
         r[i] = j0 + i < a.k ? (uint32_t)a.rows[t * a.k + j0 + i] : ~0u;
         w[i] = kRows && a.weights != nullptr && j0 + i < a.k ? a.weights[t * a.k + j0 + i] : 1.0f;
       }
-      for (int c = threadIdx.x; c < a.pieces; c += kThreads) {
+      for (int c = own; c < a.pieces; c += kOwn) {
         const u32x4 g = load16(a.x, t, a.pieces, c);
         float f[8];
 #pragma unroll
@@ -143,17 +154,22 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(RowArgs a) {
                                      pack_bf16x2(w[i] * f[4], w[i] * f[5]), pack_bf16x2(w[i] * f[6], w[i] * f[7])});
         }
       }
-      if constexpr (kDots) {
+      if constexpr (kDots && kOwn <= 64) {
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
+          dot[i] = sum_lanes<kLanes>(dot[i]);
+          if (lane == i && j0 + i < a.k) a.grad_w[t * a.k + j0 + i] = dot[i];
+        }
+      } else if constexpr (kDots) {
 #pragma unroll
-          for (int d = 1; d < 64; d *= 2) dot[i] += __shfl_xor(dot[i], d);
+        for (int i = 0; i < kSlots; ++i) {
+          dot[i] = sum_lanes<kLanes>(dot[i]);
           if (lane == 0) part[wave][i] = dot[i];
         }
         __syncthreads();
         if (threadIdx.x < kSlots && j0 + (int)threadIdx.x < a.k) {
           float s = 0.0f;
-          for (int v = 0; v < kThreads / 64; ++v) s += part[v][threadIdx.x];
+          for (int v = 0; v < kOwn / 64; ++v) s += part[v][threadIdx.x];
           a.grad_w[t * a.k + j0 + threadIdx.x] = s;
         }
         __syncthreads();
@@ -180,21 +196,24 @@ void by_slots(int64_t k, F&& f) {
   else f(std::integral_constant<int, 8>{});
 }
 
-// Fewer tokens than fill the GPU with workgroups of 256 threads get 1024 threads each
-// (256 tokens of 7168 with 8 rows: 13.6 us, 18.6 by 256 threads).
-constexpr int64_t kFewTokens = 1024;
+// Threads of a token in combine_bwd (us of the dots alone by 256, 64 and 16, 8 rows a
+// token unless said): short rows get 16 (2000 tokens of 128: 9.0, 5.1, 4.5; 16000 of
+// 256 with 7: 48, 19, 13), longer ones of enough tokens to fill the GPU a wave (2000 of
+// 1024: 12.7, 10.6, 28; of 2048 with 4: 9.0, 10.5), the rest 256, and 1024 where there
+// are few (256 tokens of 7168, both results: 13.6 us, 18.6 by 256).
+constexpr int64_t kFewTokens = 1024, kManyTokens = 8192;
 
-template <bool kStream, int kThreads>
+template <bool kStream, int kOwn>
 void bwd(const RowArgs& a, hipStream_t s) {
   by_slots(a.k, [&](auto slots) {
-    constexpr int kSlots = decltype(slots)::value;
-    const dim3 grid = grid_of(a.tokens), block(kThreads);
+    constexpr int kSlots = decltype(slots)::value, kBlock = kOwn < kThreads ? kThreads : kOwn;
+    const dim3 grid = grid_of((a.tokens * kOwn + kBlock - 1) / kBlock), block(kBlock);
     if (a.out != nullptr && a.grad_w != nullptr)
-      combine_bwd_kernel<true, true, kStream, kSlots, kThreads><<<grid, block, 0, s>>>(a);
+      combine_bwd_kernel<true, true, kStream, kSlots, kOwn><<<grid, block, 0, s>>>(a);
     else if (a.out != nullptr)
-      combine_bwd_kernel<true, false, kStream, kSlots, kThreads><<<grid, block, 0, s>>>(a);
+      combine_bwd_kernel<true, false, kStream, kSlots, kOwn><<<grid, block, 0, s>>>(a);
     else
-      combine_bwd_kernel<false, true, kStream, kSlots, kThreads><<<grid, block, 0, s>>>(a);
+      combine_bwd_kernel<false, true, kStream, kSlots, kOwn><<<grid, block, 0, s>>>(a);
   });
 }
 
@@ -228,8 +247,11 @@ hipError_t launch_moe_combine_bwd(const void* grad, const void* y, int64_t token
                                   const int32_t* rows, const float* weights, void* grad_y, float* grad_w,
                                   hipStream_t s) {
   const RowArgs a = args(grad, y, grad_y, grad_w, rows, weights, tokens, topk, cols);
+  const bool few = tokens < kFewTokens;
   if (streams(a)) bwd<true, kThreads>(a, s);
-  else if (tokens < kFewTokens && a.pieces > kThreads) bwd<false, 1024>(a, s);
+  else if (a.pieces <= (tokens < kManyTokens ? 16 : 32)) bwd<false, 16>(a, s);
+  else if (!few && a.pieces <= 128) bwd<false, 64>(a, s);
+  else if (few && a.pieces > kThreads) bwd<false, 1024>(a, s);
   else bwd<false, kThreads>(a, s);
   return hipGetLastError();
 }
