@@ -191,6 +191,25 @@ def test_sort(lp, T, k, E):
     check_sort(lp, few, E)
 
 
+@pytest.mark.parametrize("n", [1, 63, 1023, 1024, 1025, 2047, 2048, 2049, 3071, 65535, 65536, 65537])
+@pytest.mark.parametrize("E", [1, 3, 256, 257, 1024])
+def test_sort_at_the_borders_of_its_workgroups(lp, n, E):
+    """Evenly spread and all but one of one expert; some of nobody's."""
+    rng = np.random.default_rng(n + E)
+    for kind in range(2):
+        e = rng.integers(-1, E + 1, n).astype(np.int32) if kind == 0 else np.full(n, E - 1, np.int32)
+        if kind:
+            e[n // 2] = 0
+        off, rows, order = lp.lp_moe_sort(dev(e), E)
+        live = np.flatnonzero((e >= 0) & (e < E))
+        want = live[np.argsort(e[live], kind="stable")]
+        assert_bits_equal(off.cpu().numpy(), np.cumsum(np.bincount(e[live], minlength=E)).astype(np.int32), "offsets")
+        assert_bits_equal(order.cpu().numpy()[:live.size], want.astype(np.int32), "order")
+        at = np.full(n, -1, np.int32)
+        at[want] = np.arange(live.size)
+        assert_bits_equal(rows.cpu().numpy(), at, "rows")
+
+
 @pytest.mark.parametrize("n", [0, 1, 4096, 4097, 10000])
 def test_sort_of_nobodys_pairs(lp, n):
     experts = torch.full((n, 1), -1, dtype=torch.int32, device="cuda")
@@ -264,6 +283,12 @@ def test_rows_there_and_back(lp, T, k, E, H, drop):
         bf16_dev(gb), y, rows, dev(w))[0][:rp.size].view(torch.int16))
     none, dots = lp.lp_moe_combine_bwd(bf16_dev(gb), y, rows, dev(w), need_dy=False)
     assert none is None and torch.equal(dots, gw)
+
+
+@pytest.mark.parametrize("T,k,E,H,drop", [(1027, 3, 8, 264, 0.1), (1030, 9, 16, 136, 0.1), (1024, 1, 3, 1024, 0.0), (2049, 2, 5, 1032, 0.2),
+                                          (8195, 2, 8, 256, 0.1), (8193, 5, 7, 24, 0.2), (8191, 1, 2, 256, 0.0)])
+def test_rows_of_many_tokens(lp, T, k, E, H, drop):
+    test_rows_there_and_back(lp, T, k, E, H, drop)
 
 
 @pytest.mark.parametrize("bad", [-1, -7, 24, 1 << 20, (1 << 31) - 1, -(1 << 31)])
