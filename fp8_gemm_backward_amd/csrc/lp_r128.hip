@@ -59,27 +59,39 @@ __global__ __launch_bounds__(kThreads) void r128_cols(const uint16_t* __restrict
 // end.  Run indices between two groups' ranges have no rows.  Every wave
 // looks at 64 groups at a time, one a lane (walking them one by one cost
 // 32768 x 2048 in 64 groups 79 us along both axes, this 54 then and 45 now).
+// kAhead: so many loads at once, for kernels where these loads show.
+template <int kAhead = 1>
 __device__ __forceinline__ void run_rows(const int32_t* __restrict__ offsets, int groups, int M, int run, int& r0,
                                          int& r1) {
   const int lane = threadIdx.x & 63;
   int end0 = 0;
   r0 = r1 = 0;
-  for (int base = 0; base < groups; base += 64) {
-    int e = base + lane < groups ? offsets[base + lane] : 0;
-    e = e > M ? M : e;
-    e = e < end0 ? end0 : e;
-    e = wave_scan(e, [](int a, int b) { return a > b ? a : b; });
-    int start = __shfl_up(e, 1);
-    start = lane == 0 ? end0 : start;
-    const int k = run - (start / kRunLen + base + lane);
-    const uint64_t own = __ballot(k >= 0 && k < (e - start + kRunLen - 1) / kRunLen);
-    if (own != 0) {
-      const int j = __builtin_ctzll(own), end = __builtin_amdgcn_readlane(e, j);
-      r0 = __builtin_amdgcn_readlane(start, j) + __builtin_amdgcn_readlane(k, j) * kRunLen;
-      r1 = r0 + kRunLen < end ? r0 + kRunLen : end;
-      return;
+  for (int base0 = 0; base0 < groups; base0 += 64 * kAhead) {
+    int ends[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int g = base0 + 64 * j + lane;
+      if (base0 + 64 * j < groups) ends[j] = offsets[g < groups ? g : groups - 1];
     }
-    end0 = __builtin_amdgcn_readlane(e, 63);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int base = base0 + 64 * j;
+      if (base >= groups) return;
+      int e = ends[j] > M ? M : ends[j];
+      e = e < end0 ? end0 : e;
+      e = wave_scan(e, [](int a, int b) { return a > b ? a : b; });
+      int start = __shfl_up(e, 1);
+      start = lane == 0 ? end0 : start;
+      const int k = run - (start / kRunLen + base + lane);
+      const uint64_t own = __ballot(base + lane < groups && k >= 0 && k < (e - start + kRunLen - 1) / kRunLen);
+      if (own != 0) {
+        const int i = __builtin_ctzll(own), end = __builtin_amdgcn_readlane(e, i);
+        r0 = __builtin_amdgcn_readlane(start, i) + __builtin_amdgcn_readlane(k, i) * kRunLen;
+        r1 = r0 + kRunLen < end ? r0 + kRunLen : end;
+        return;
+      }
+      end0 = __builtin_amdgcn_readlane(e, 63);
+    }
   }
 }
 
@@ -154,11 +166,12 @@ __device__ __forceinline__ uint32_t row16_max4(const uint32_t (&m)[4], int i) {
 // thread's 32 values, which bounds tiles that come out of a cache; hence the
 // four rows' scales made side by side in four lanes, a column's
 // by one thread, and bad runs patched in a branch of their own.
-template <bool kCols, bool kRows, bool kFull, bool kStream = false>
+template <bool kCols, bool kRows, bool kFull, bool kStream = false, int kTileThreads = lp::kTileThreads>
 __device__ __forceinline__ void quant_tile(const TileArgs& a, TileLds& sh, u32x4 (&v)[kTileRows], int64_t b, int rb, int ct,
                                            int r0, int r1) {
   static_assert(kTileRows == 4, "a lane of four for each row");
-  const int tid = threadIdx.x, ci = tid & 15, ri = tid >> 4, wave = tid >> 6;
+  constexpr int kTileWaves = kTileThreads / 64, kStep = kTileThreads / 16;
+  const int tid = threadIdx.x % kTileThreads, ci = tid & 15, ri = tid >> 4, wave = tid >> 6;
   const bool col_ok = kFull || ct * kRunLen + 8 * ci < a.cols;
   const int n = kFull ? kRunLen : r1 - r0;
   const int64_t corner = (b * a.rows + r0) * a.cols + ct * kRunLen;       // (uniform)
@@ -201,7 +214,7 @@ __device__ __forceinline__ void quant_tile(const TileArgs& a, TileLds& sh, u32x4
       for (int k = 0; k < kTileRows; ++k) m[k] = amax8(v[k]);
       const RunScale q = run_scale(row16_max4(m, ci));     // row ri + kStep (ci % 4)
       const RunRecip p = run_recip(q.s, q.r);
-      if (ci < kTileRows && (kFull || ri + kStep * ci < n))
+      if (ci < kTileRows && (kFull || (ri + kStep * ci < n && ct * kRunLen < a.cols)))
         a.scales_c[((int64_t)b * a.col_tiles.d + ct) * a.rows + r0 + ri + kStep * ci] = q.s;
       const bool any = __ballot(q.bad) != 0;
       uint8_t* const to = a.codes_c + corner;
@@ -311,6 +324,38 @@ struct RowMap {
   uint32_t pairs;
 };
 
+// The values of a thread, kTileThreads of which take a tile.
+template <bool kWeighted, int kTileThreads>
+__device__ __forceinline__ void mapped_values(const TileArgs& a, const RowMap& map, int ct, int r0, int r1, u32x4 (&v)[kTileRows]) {
+  constexpr int kStep = kTileThreads / 16;
+  const int tid = threadIdx.x % kTileThreads, c = ct * kRunLen + 8 * (tid & 15), r = r0 + (tid >> 4);
+  uint32_t pair[kTileRows];
+#pragma unroll
+  for (int k = 0; k < kTileRows; ++k) {
+    pair[k] = r + kStep * k < r1 ? (uint32_t)map.order[r + kStep * k] : ~0u;
+    if (pair[k] >= map.pairs || c >= a.cols) pair[k] = ~0u;
+  }
+  // (each row into a variable of its own: into v[k] itself, one load waited for the last)
+  float w[kTileRows];
+#pragma unroll
+  for (int k = 0; k < kTileRows; ++k) {
+    u32x4 x = {0u, 0u, 0u, 0u};
+    float y = 0.0f;
+    if (pair[k] != ~0u) {
+      x = *reinterpret_cast<const u32x4*>(a.src + (int64_t)fdiv(pair[k], map.k) * a.cols + c);
+      if constexpr (kWeighted) y = map.weights[pair[k]];
+    }
+    v[k] = x;
+    w[k] = y;
+  }
+  if constexpr (kWeighted) {
+#pragma unroll
+    for (int k = 0; k < kTileRows; ++k)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) v[k][d] = pack_bf16x2(w[k] * bf16_lo(v[k][d]), w[k] * bf16_hi(v[k][d]));
+  }
+}
+
 template <bool kWeighted, bool kStream>
 __global__ __launch_bounds__(kTileThreads) void r128_mapped(TileArgs a, RowMap map) {
   __shared__ TileLds sh;
@@ -318,37 +363,41 @@ __global__ __launch_bounds__(kTileThreads) void r128_mapped(TileArgs a, RowMap m
   int r0, r1;
   run_rows(a.offsets, a.groups, a.rows, rb, r0, r1);
   if (r1 == r0) return;
-  const int c = ct * kRunLen + 8 * (threadIdx.x & 15), r = r0 + (threadIdx.x >> 4);
-  uint32_t pair[kTileRows];
-#pragma unroll
-  for (int k = 0; k < kTileRows; ++k) {
-    pair[k] = r + kStep * k < r1 ? (uint32_t)map.order[r + kStep * k] : ~0u;
-    if (pair[k] >= map.pairs || c >= a.cols) pair[k] = ~0u;
-  }
   u32x4 v[kTileRows];
-  float w[kTileRows];
-  // (weights by no branch: one between two rows' loads has the second wait for the first)
-  if constexpr (kWeighted) {
-#pragma unroll
-    for (int k = 0; k < kTileRows; ++k) w[k] = map.weights[pair[k] != ~0u ? pair[k] : 0];
-  }
-#pragma unroll
-  for (int k = 0; k < kTileRows; ++k) {
-    v[k] = u32x4{0u, 0u, 0u, 0u};
-    if (pair[k] != ~0u) v[k] = *reinterpret_cast<const u32x4*>(a.src + (int64_t)fdiv(pair[k], map.k) * a.cols + c);
-  }
-  if constexpr (kWeighted) {
-#pragma unroll
-    for (int k = 0; k < kTileRows; ++k) {
-      w[k] = pair[k] != ~0u ? w[k] : 0.0f;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) v[k][d] = pack_bf16x2(w[k] * bf16_lo(v[k][d]), w[k] * bf16_hi(v[k][d]));
-    }
-  }
+  mapped_values<kWeighted, kTileThreads>(a, map, ct, r0, r1, v);
   if (is_full(a, r1 - r0, ct))
     quant_tile<true, true, true, kStream>(a, sh, v, 0, rb, ct, r0, r1);
   else
     quant_tile<true, true, false, kStream>(a, sh, v, 0, rb, ct, r0, r1);
+}
+
+// For short runs: four column tiles to a workgroup (by_four: col_tiles / 4 of them, rounded
+// up), side by side with 128 threads each where the run has up to 32 rows, else in turn.
+// Of one tile each their number and the chain offsets, order, rows, scales bound them, whatever
+// they hold: 128 tokens of 7168 to 8 of 64 experts 17.8 us, by fours 10.9; 500 of 4096 to
+// 8 of 256 40.5 and 20.  From 20 to 40 rows a group on that is lost again (256 tokens 21.3 and
+// 23.3), and where the tiles do not fill the GPU (1034 of 176 to 2 of 131: 4.7 and 5.0).
+constexpr int kShortThreads = 128, kShortTiles = kTileThreads / kShortThreads, kShortRows = kRunLen / kShortTiles;
+
+template <bool kWeighted>
+__global__ __launch_bounds__(kTileThreads) void r128_mapped_short(TileArgs a, RowMap map, FastDiv by_four) {
+  __shared__ TileLds sh[kShortTiles];
+  const int rb = fdiv(blockIdx.x, by_four), ct0 = (blockIdx.x - rb * by_four.d) * kShortTiles;
+  int r0, r1;
+  run_rows<4>(a.offsets, a.groups, a.rows, rb, r0, r1);
+  if (r1 == r0) return;
+  u32x4 v[kTileRows];
+  if (r1 - r0 <= kShortRows) {
+    const int part = __builtin_amdgcn_readfirstlane(threadIdx.x / kShortThreads);
+    mapped_values<kWeighted, kShortThreads>(a, map, ct0 + part, r0, r1, v);
+    quant_tile<true, true, false, false, kShortThreads>(a, sh[part], v, 0, rb, ct0 + part, r0, r1);
+    return;
+  }
+#pragma unroll 1
+  for (int i = 0; i < kShortTiles && ct0 + i < (int)a.col_tiles.d; ++i) {
+    mapped_values<kWeighted, kTileThreads>(a, map, ct0 + i, r0, r1, v);
+    quant_tile<true, true, false, false>(a, sh[i], v, 0, rb, ct0 + i, r0, r1);
+  }
 }
 
 }  // namespace
@@ -390,6 +439,14 @@ hipError_t launch_moe_gather_quant(const void* x, int64_t tokens, int64_t topk, 
                    (int32_t)rows, (int32_t)cols, make_fastdiv((uint32_t)ct), make_fastdiv((uint32_t)rt)};
   const RowMap map{order, weights, make_fastdiv((uint32_t)topk), (uint32_t)rows};
   const dim3 grid((uint32_t)(rt * ct)), block(kTileThreads);
+  if (rows <= 16 * groups && rt * ct >= 1024) {
+    const int64_t fours = (ct + kShortTiles - 1) / kShortTiles;
+    const FastDiv by_four = make_fastdiv((uint32_t)fours);
+    const dim3 few((uint32_t)(rt * fours));
+    if (weights != nullptr) r128_mapped_short<true><<<few, block, 0, stream>>>(a, map, by_four);
+    else r128_mapped_short<false><<<few, block, 0, stream>>>(a, map, by_four);
+    return hipGetLastError();
+  }
   const bool past = 2 * rows * cols > kCacheBytes;
   if (weights != nullptr)
     past ? r128_mapped<true, true><<<grid, block, 0, stream>>>(a, map) : r128_mapped<true, false><<<grid, block, 0, stream>>>(a, map);

@@ -353,6 +353,28 @@ def test_gather_quant_is_gather_then_quant(lp, T, k, E, H, drop, weighted):
     same_runs(lp, lp.lp_moe_gather_quant(x, order, off, k, weights=w), lp.lp_r128_quant_dual(plain, off), off, H)
 
 
+@pytest.mark.parametrize("T,E,H", [(200, 64, 2192), (511, 64, 2048), (300, 300, 400), (16, 1000, 144)])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_gather_quant_of_many_short_runs(lp, T, E, H, weighted):
+    """Most experts with a row or none, one with every token's first slot: runs of 1 to 128 rows beside one another."""
+    rng = np.random.default_rng(T + E)
+    experts = rng.integers(0, E, (T, 2)).astype(np.int32)
+    experts[:, 0] = E // 3
+    experts[rng.random((T, 2)) < 0.1] = -1
+    off, rows, order = lp.lp_moe_sort(dev(experts), E)
+    xb = bits(rng, (T, H))
+    xb[T // 3, 5], xb[0, 7], xb[T - 1, H - 1] = 0x7F80, 0xFFC1, 0x7FC0
+    x, w = bf16_dev(xb), dev(rng.random((T, 2)).astype(np.float32)) if weighted else None
+    plain = lp.lp_moe_combine_bwd(x, None, rows, w, need_dw=False)[0]
+    out = (lp.QTensor("fp8_r128", torch.full((1, 2 * T, H), 99, dtype=torch.uint8, device="cuda"),
+                      torch.full((1, -(-H // 128), 2 * T), 5.0, device="cuda"), None, (1, 2 * T, H), -1),
+           lp.QTensor("fp8_r128", torch.full((1, 2 * T, H), 99, dtype=torch.uint8, device="cuda"),
+                      torch.full((1, 2 * T // 128 + E, H), 5.0, device="cuda"), None, (1, 2 * T, H), -2))
+    got, n = lp.lp_moe_gather_quant(x, order, off, 2, weights=w, out=out), int(off[-1])
+    same_runs(lp, got, lp.lp_r128_quant_dual(plain, off), off, H)
+    assert (got[0].codes[0, n:] == 99).all() and (got[1].codes[0, n:] == 99).all() and (got[0].scales[0, :, n:] == 5).all()
+
+
 def test_gather_quant_leaves_what_no_expert_has(lp):
     T, k, H, E = 100, 3, 160, 4
     rng = np.random.default_rng(2)
