@@ -65,6 +65,41 @@ GROUPED = [(3, 16, 32, 2), (34, 128, 160, 33), (282, 496, 160, 2), (109, 592, 32
            (1390, 1616, 32, 33), (3223, 2336, 32, 5)]
 
 
+# Those of the shapes that take middling sizes, and the large tiles.
+MIDDLING = [(2713, 288, 416), (212, 3488, 1024), (97, 9280, 2464), (393, 9392, 416), (2181, 288, 32), (1266, 6992, 32), (1348, 8832, 96)]
+MIDDLING_GROUPED = [(2099, 336, 416, 2), (205, 1632, 1056, 9), (98, 9312, 2464, 2), (398, 9360, 416, 2), (2059, 336, 32, 2), (971, 8848, 32, 2)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K", MIDDLING)
+def test_middling_shapes(lp, fmt, M, N, K):
+    test_linear(lp, fmt, M, N, K)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K,G", MIDDLING_GROUPED)
+def test_middling_shapes_grouped(lp, fmt, M, N, K, G):
+    test_grouped(lp, fmt, M, N, K, G, "uneven")
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,G", [(1, 70), (2, 33), (17, 40), (33, 9)])
+def test_fewer_rows_than_groups(lp, fmt, M, G):
+    """One row a group, the last groups' too, and all rows in the last one: as many row tiles as there can be."""
+    w, dec = weight(lp, fmt, G, 144, 96, M + G)
+    x, xv = rows_of(M, 96, M)
+    sizes = np.zeros((2, G), np.int64)
+    sizes[0, G - min(M, G):] = 1
+    sizes[0, G - 1] += M - sizes[0].sum()
+    sizes[1, G - 1] = M
+    for n in sizes:
+        ends = np.cumsum(n)
+        y = lp.lp_grouped_fwd_w4(x, w, dev(ends.astype(np.int32)))
+        for g in np.flatnonzero(n):
+            rows = slice(ends[g] - n[g], ends[g])
+            check(y[rows], xv[rows], dec[g], (fmt, M, G, g))
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 @pytest.mark.parametrize("M,N,K", DENSE)
 def test_every_shape_of_a_workgroup(lp, fmt, M, N, K):
