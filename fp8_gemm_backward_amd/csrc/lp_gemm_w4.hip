@@ -309,7 +309,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kEu)))
 // step of a wave's part of the contraction and, each further one, a fixed time too.
 // Fitted to 1500 measured problems (1 to 4096 rows, dense and up to 64 groups,
 // weights from HBM, both formats) with 7 to 18% of scatter: the shape they choose
-// is within 4% of the fastest on average, within 1.6 times in 99 of 100.  64 rows by one
+// is within 3% of the fastest on average, within 1.4 times in 99 of 100 (the grouped
+// ones' row tiles known only as a bound).  64 rows by one
 // column tile a wave ({2, 1, 4}, {1, 1, 4}) serve some hundred rows of middling
 // weights: 212 x 3488 x 4992 23 us (34.5 without them), 171 x 3616 x 1984 12.5 (18.9).
 struct Shape {
@@ -327,16 +328,14 @@ constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
 // run at a lower clock when every CU has a tile.
 constexpr int kTileFixed = 800, kTileStep = 280, kTileStepFull = 410;
 
-// Row tiles of a call: an upper bound (groups with rows: at most a tile each for its
-// first row, and one for every further row tile's worth of rows; 1 row over 48 groups launched 48
-// times the workgroups it needs without that, 19 us for 6); expected: about what grouped
-// rows make (a group with rows has one tile at least, and half of one to spare on average).
-int64_t row_tiles(const Params& p, int rows, bool expected = false) {
+// Row tiles of a call; a bound where rows are grouped: groups with rows have a tile
+// each for their first row, and one for every further row tile's worth of rows (1 row
+// over 48 groups launched 48 times the workgroups it needs by M / rows + groups, 19 us
+// for 6).
+int64_t row_tiles(const Params& p, int rows) {
   if (p.offsets == nullptr) return (p.Ptot + rows - 1) / rows;
   const int64_t used = p.Ptot < p.groups ? p.Ptot : p.groups;
-  if (!expected) return used + (p.Ptot - used) / rows;
-  const int64_t t = p.Ptot / rows + used / 2;
-  return t > used ? t : used;
+  return used + (p.Ptot - used) / rows;
 }
 
 int64_t col_tiles(const Params& p, const Shape& s) {
@@ -353,17 +352,16 @@ int choose(const Params& p) {
     const Shape& s = kShapes[i];
     // (a launch has fewer than 2^32 threads)
     if (row_tiles(p, 16 * s.rt) * col_tiles(p, s) + 8 > (int64_t)1 << 23) continue;
-    const int64_t rounds = (row_tiles(p, 16 * s.rt, true) * col_tiles(p, s) + kCUs - 1) / kCUs;
+    const int64_t rounds = (row_tiles(p, 16 * s.rt) * col_tiles(p, s) + kCUs - 1) / kCUs;
     const int64_t t = s.fixed + (rounds - 1) * s.round + (steps + s.wk - 1) / s.wk * (s.step + (rounds - 1) * s.more);
     if (t < least) {
       least = t;
       best = i;
     }
   }
-  const int64_t tiles = row_tiles(p, 256, true) * ((p.Qtot + 255) / 256);
+  const int64_t tiles = row_tiles(p, 256) * ((p.Qtot + 255) / 256);
   const int64_t t = kTileFixed + steps * (tiles <= kCUs / 2 ? kTileStep : kTileStepFull * ((tiles + kCUs - 1) / kCUs));
-  // (the fit is low where there are many rounds of many rows)
-  return best >= 0 && least + least / 8 <= t ? best : -1;
+  return best >= 0 && least <= t ? best : -1;
 }
 
 template <int F, int kIndex, int kDepth, int kXS, int kEu = 2>
