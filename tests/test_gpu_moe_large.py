@@ -62,6 +62,28 @@ def test_rows_past_2_to_32_elements(lp):
     assert torch.equal(gy[rows[t].long()], want)
 
 
+@pytest.mark.parametrize("T,k,H", [(1 << 18, 4, 64), ((1 << 18) + 1, 1, 264), (17000, 4, 1024), (900, 8, 7168), (511, 9, 8200), (5000, 3, 4096)])
+def test_gradients_of_rows_past_the_caches(lp, T, k, H):
+    """More than 64 MB of rows, by every number of threads a token can have: each result alone and both."""
+    g = gen(7)
+    x, y = randn_bf16((T, H), g), randn_bf16((T * k, H), g)
+    e = torch.randint(-1, 9, (T, k), generator=g, device="cuda").int()
+    _, rows, _ = lp.lp_moe_sort(e, 9)
+    w = torch.rand(T, k, generator=g, device="cuda")
+    gy, gw = lp.lp_moe_combine_bwd(x, y, rows, w)
+    assert torch.equal(gw, lp.lp_moe_combine_bwd(x, y, rows, w, need_dy=False)[1])
+    live = rows.reshape(-1) >= 0
+    r = rows.reshape(-1)[live].long()
+    assert torch.equal(gy[r], lp.lp_moe_combine_bwd(x, None, rows, w, need_dw=False)[0][r])
+    t = sample(T)
+    dots = x[t].double()[:, None] * y[rows[t].clamp(min=0).long()].double() * (rows[t] >= 0)[:, :, None]
+    assert ((gw[t].double() - dots.sum(2)).abs() <= H * U32 * dots.abs().sum(2)).all()
+    pair = sample(T * k)
+    pair = pair[live[pair]]
+    want = (x[pair // k].float() * w.reshape(-1)[pair][:, None]).bfloat16()
+    assert torch.equal(gy[rows.reshape(-1)[pair].long()], want)
+
+
 def test_gate_past_2_to_32_elements(lp):
     T, E, k = (1 << 22) + 3, 1024, 2
     l = randn_bf16((T, E), gen(2))
