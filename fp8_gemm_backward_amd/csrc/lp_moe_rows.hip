@@ -200,9 +200,10 @@ void by_slots(int64_t k, F&& f) {
 // token unless said): short rows get 16 (2000 tokens of 128: 9.0, 5.1, 4.5; 16000 of
 // 256 with 7: 48, 19, 13), longer ones of enough tokens to fill the GPU a wave (2000 of
 // 1024: 12.7, 10.6, 28; of 2048 with 4: 9.0, 10.5), the rest 256, and 1024 where there
-// are few (256 tokens of 7168, both results: 13.6 us, 18.6 by 256), unless their rows go
-// past the caches (900 of 7168, both results: 58.6 us by 1024, 47.3 by 256; the dots alone
-// 27.3 and 31.5).
+// are few (256 tokens of 7168, both results: 13.6 us, 18.6 by 256), past the caches only
+// where rows are longer yet (900 of 7168, both results: 58.6 us by 1024, 47.3 by 256; 512
+// of 16384 59 and 64).  Which results are asked for changes nothing: the dots have
+// the same bits with the rows or without.
 constexpr int64_t kFewTokens = 1024, kManyTokens = 8192;
 
 template <bool kStream, int kOwn>
@@ -252,7 +253,7 @@ hipError_t launch_moe_combine_bwd(const void* grad, const void* y, int64_t token
   const bool past = streams(a), few = tokens < kFewTokens;
   if (a.pieces <= (tokens < kManyTokens ? 16 : 32)) past ? bwd<true, 16>(a, s) : bwd<false, 16>(a, s);
   else if (!few && a.pieces <= 128) past ? bwd<true, 64>(a, s) : bwd<false, 64>(a, s);
-  else if (few && a.pieces > kThreads && !(past && grad_y != nullptr)) past ? bwd<true, 1024>(a, s) : bwd<false, 1024>(a, s);
+  else if (few && a.pieces > (past ? 1024 : kThreads)) past ? bwd<true, 1024>(a, s) : bwd<false, 1024>(a, s);
   else past ? bwd<true, kThreads>(a, s) : bwd<false, kThreads>(a, s);
   return hipGetLastError();
 }
