@@ -45,7 +45,7 @@ struct GateArgs {
 };
 
 template <int kCtrl>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {            // (every lane has a source: rotations of 16)
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {            // (a lane without a source gets 0)
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, true);
 }
 template <int kCtrl>
@@ -61,6 +61,19 @@ __device__ __forceinline__ float dpp(float v) {
   return __builtin_bit_cast(float, dpp<kCtrl>(__builtin_bit_cast(uint32_t, v)));
 }
 
+template <int kLane>
+__device__ __forceinline__ uint32_t of_lane(uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, kLane); }
+template <int kLane>
+__device__ __forceinline__ int32_t of_lane(int32_t v) { return __builtin_amdgcn_readlane(v, kLane); }
+template <int kLane>
+__device__ __forceinline__ uint64_t of_lane(uint64_t v) {
+  return (uint64_t)of_lane<kLane>((uint32_t)(v >> 32)) << 32 | of_lane<kLane>((uint32_t)v);
+}
+template <int kLane>
+__device__ __forceinline__ float of_lane(float v) {
+  return __builtin_bit_cast(float, of_lane<kLane>(__builtin_bit_cast(uint32_t, v)));
+}
+
 // Reduction over the token's lanes, in all of them.
 template <int kLanes, class T, class F>
 __device__ __forceinline__ T over_lanes(T v, F op) {
@@ -69,8 +82,9 @@ __device__ __forceinline__ T over_lanes(T v, F op) {
   v = op(v, dpp<0x122>(v));
   v = op(v, dpp<0x121>(v));
   if constexpr (kLanes == 64) {
-    v = op(v, __shfl_xor(v, 16));
-    v = op(v, __shfl_xor(v, 32));
+    v = op(v, dpp<0x142>(v));                                    // row_bcast:15: the last 16 lanes get the 16 before
+    v = op(v, dpp<0x143>(v));                                    // row_bcast:31: and the first 32
+    v = of_lane<63>(v);
   }
   return v;
 }
@@ -118,10 +132,12 @@ __device__ __forceinline__ uint32_t mask_of(bool c) {
   return m;
 }
 
-// The lane's logits: numbers kItems lane + i when the row is full (kFull: wide loads),
-// else kLanes i + lane.
-template <int kLanes, int kItems, bool kFull>
-__device__ __forceinline__ int logit_index(int lane, int i) { return kFull ? kItems * lane + i : kLanes * i + lane; }
+// The lane's logits: numbers kItems lane + i where the row divides into aligned pieces
+// (kWide: wide loads), else kLanes i + lane.
+template <class T, int kItems>
+constexpr int piece_of() { return kItems < 16 / (int)sizeof(T) ? kItems : 16 / (int)sizeof(T); }
+template <int kLanes, int kItems, bool kWide>
+__device__ __forceinline__ int logit_index(int lane, int i) { return kWide ? kItems * lane + i : kLanes * i + lane; }
 
 // A logit's key: above all keys of smaller logits and of equal ones (0 and -0 are) with
 // a higher index; below kNone, or at it, for -inf and past the last expert.  NaN counts
@@ -133,21 +149,21 @@ template <class T>
 constexpr Key<T> kNone = sizeof(T) == 2 ? (Key<T>)0x8080FFFF : 0;           // (-0x7F80: -inf)
 template <class T>
 constexpr Key<T> kLast = sizeof(T) == 2 ? (Key<T>)0x80000000 : 0;
-template <class T, int kLanes, int kItems, bool kFull>
+template <class T, int kLanes, int kItems, bool kWide>
 __device__ __forceinline__ Key<T> key_of(float v, int lane, int i) {
   if constexpr (sizeof(T) == 2) {
     const uint32_t b = __builtin_bit_cast(uint32_t, v);
-    return (int32_t)(pick((uint32_t)((int32_t)b >> 31), 0x80000000u - b, b) | (kFull ? kItems - 1 - i : (kItems - 1 - i) * kLanes));
+    return (int32_t)(pick((uint32_t)((int32_t)b >> 31), 0x80000000u - b, b) | (kWide ? kItems - 1 - i : (kItems - 1 - i) * kLanes));
   } else {
     v += 0.0f;                                                   // (-0 equals 0)
     const uint32_t b = __builtin_bit_cast(uint32_t, v), up = (int32_t)b < 0 ? ~b : b | 0x80000000u;
     if (v == -INFINITY) return 0;
-    return (uint64_t)up << 32 | (0xFFFFFFFFu - (uint32_t)logit_index<kLanes, kItems, kFull>(lane, i));
+    return (uint64_t)up << 32 | (0xFFFFFFFFu - (uint32_t)logit_index<kLanes, kItems, kWide>(lane, i));
   }
 }
-template <class T, int kLanes, int kItems, bool kFull>
+template <class T, int kLanes, int kItems, bool kWide>
 __device__ __forceinline__ Key<T> lane_code(int lane) {
-  if constexpr (sizeof(T) == 2) return kFull ? (kLanes - 1 - lane) * kItems : kLanes - 1 - lane;
+  if constexpr (sizeof(T) == 2) return kWide ? (kLanes - 1 - lane) * kItems : kLanes - 1 - lane;
   else return 0;
 }
 template <class T, int kLanes, int kItems>
@@ -210,16 +226,26 @@ __device__ __forceinline__ void sort_largest(K (&a)[kItems]) {
   }
 }
 
-template <class T, int kLanes, int kItems, bool kFull>
+template <class T, int kLanes, int kItems, bool kWide>
 __device__ __forceinline__ void load_logits(const T* row, int E, int lane, float (&v)[kItems]) {
-  if constexpr (kFull) {
-    constexpr int kBytes = kItems * (int)sizeof(T), kWord = kBytes < 16 ? kBytes : 16;
-    struct alignas(kWord) Words {
-      T t[kItems];
+  if constexpr (kWide) {
+    constexpr int kPiece = piece_of<T, kItems>();
+    struct alignas(kPiece * sizeof(T)) Piece {
+      T t[kPiece];
     };
-    const Words w = *reinterpret_cast<const Words*>(row + kItems * lane);
+    const Piece* const from = reinterpret_cast<const Piece*>(row + kItems * lane);
+    Piece w[kItems / kPiece] = {};
+    if (E == kLanes * kItems) {                                  // (32768 rows of 256 bf16: 9.9 us, 11.6 by the branches below)
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) v[i] = to_f32(w.t[i]);
+      for (int p = 0; p < kItems / kPiece; ++p) w[p] = from[p];
+    } else {
+#pragma unroll
+      for (int p = 0; p < kItems / kPiece; ++p)
+        if (kItems * lane + p * kPiece < E) w[p] = from[p];
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+      v[i] = kItems * lane + i / kPiece * kPiece < E ? to_f32(w[i / kPiece].t[i % kPiece]) : -INFINITY;
   } else {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
@@ -230,15 +256,15 @@ __device__ __forceinline__ void load_logits(const T* row, int E, int lane, float
 }
 
 // kKeep: of a lane's logits, at least min(k, kItems).
-template <class T, int kLanes, int kItems, bool kFull, int kKeep>
+template <class T, int kLanes, int kItems, bool kWide, int kKeep>
 __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateArgs a) {
   constexpr int kPer = 64 / kLanes, kOut = 64 / kLanes;          // tokens of a wave; slots of a lane (k <= 64)
   const int lane = threadIdx.x % kLanes, group = threadIdx.x % 64 / kLanes * kLanes;
-  const Key<T> code = lane_code<T, kLanes, kItems, kFull>(lane);
+  const Key<T> code = lane_code<T, kLanes, kItems, kWide>(lane);
   for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + threadIdx.x / 64) * kPer; t0 < a.tokens; t0 += (int64_t)gridDim.x * kWaves * kPer) {
     const int64_t t = t0 + group / kLanes, row = t < a.tokens ? t : a.tokens - 1;
     float v[kItems];
-    load_logits<T, kLanes, kItems, kFull>(static_cast<const T*>(a.logits) + row * a.E, a.E, lane, v);
+    load_logits<T, kLanes, kItems, kWide>(static_cast<const T*>(a.logits) + row * a.E, a.E, lane, v);
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < kItems; i += 2) nan |= __builtin_isunordered(v[i], v[i + 1 < kItems ? i + 1 : i]);
@@ -251,8 +277,8 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateArgs a) {
     Key<T> left[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      left[i] = key_of<T, kLanes, kItems, kFull>(v[i], lane, i);
-      if (!kFull && logit_index<kLanes, kItems, kFull>(lane, i) >= a.E) left[i] = kLast<T>;
+      left[i] = key_of<T, kLanes, kItems, kWide>(v[i], lane, i);
+      if (!kWide && logit_index<kLanes, kItems, kWide>(lane, i) >= a.E) left[i] = kLast<T>;
     }
     sort_largest<kItems, kKeep>(left);
     Key<T> mine[kOut], first = 0;
@@ -294,7 +320,7 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateArgs a) {
   }
 }
 
-template <class T, int kLanes, int kItems, bool kFull>
+template <class T, int kLanes, int kItems, bool kWide>
 __global__ __launch_bounds__(64 * kWaves) void gate_bwd_kernel(GateArgs a) {
   constexpr int kPer = 64 / kLanes, kOut = 64 / kLanes, kRow = kLanes * kItems;
   __shared__ __attribute__((aligned(16))) float s_grad[kWaves * kPer][kRow];
@@ -304,7 +330,7 @@ __global__ __launch_bounds__(64 * kWaves) void gate_bwd_kernel(GateArgs a) {
     const int64_t t = t0 + sub, row = t < a.tokens ? t : a.tokens - 1;
     int e[kOut];
     float v[kItems], w[kOut], g[kOut], inner = 0.0f;
-    if (!a.renorm) load_logits<T, kLanes, kItems, kFull>(static_cast<const T*>(a.logits) + row * a.E, a.E, lane, v);
+    if (!a.renorm) load_logits<T, kLanes, kItems, kWide>(static_cast<const T*>(a.logits) + row * a.E, a.E, lane, v);
 #pragma unroll
     for (int o = 0; o < kOut; ++o) {
       const int j = o * kLanes + lane;
@@ -349,7 +375,7 @@ __global__ __launch_bounds__(64 * kWaves) void gate_bwd_kernel(GateArgs a) {
     const bool serial = __ballot(twice) != 0;
     wave_sync();
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) d[logit_index<kLanes, kItems, kFull>(lane, i)] = v[i];
+    for (int i = 0; i < kItems; ++i) d[logit_index<kLanes, kItems, kWide>(lane, i)] = v[i];
     wave_sync();
 #pragma unroll
     for (int o = 0; o < kOut; ++o) {
@@ -367,13 +393,19 @@ __global__ __launch_bounds__(64 * kWaves) void gate_bwd_kernel(GateArgs a) {
     wave_sync();
     if (t < a.tokens) {
       T* const out = static_cast<T*>(a.grad_l) + t * a.E;
-      if constexpr (kFull && sizeof(T) == 2 && kItems >= 2) {
-        struct alignas(kItems * 2 < 16 ? kItems * 2 : 16) Words {
-          uint32_t w[kItems / 2];
-        } o;
+      if constexpr (kWide && sizeof(T) == 2 && kItems >= 2) {
+        constexpr int kPiece = piece_of<T, kItems>();
+        struct alignas(kPiece * sizeof(T)) Piece {
+          uint32_t w[kPiece / 2];
+        };
 #pragma unroll
-        for (int i = 0; i < kItems / 2; ++i) o.w[i] = pack_bf16x2(d[kItems * lane + 2 * i], d[kItems * lane + 2 * i + 1]);
-        *reinterpret_cast<Words*>(out + kItems * lane) = o;
+        for (int i = 0; i < kItems; i += kPiece) {
+          const float* const g = d + kItems * lane + i;
+          Piece o;
+#pragma unroll
+          for (int j = 0; j < kPiece / 2; ++j) o.w[j] = pack_bf16x2(g[2 * j], g[2 * j + 1]);
+          if (kItems * lane + i < a.E) *reinterpret_cast<Piece*>(out + kItems * lane + i) = o;
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
@@ -388,24 +420,24 @@ __global__ __launch_bounds__(64 * kWaves) void gate_bwd_kernel(GateArgs a) {
 
 // Up to 8 chosen, 8 of a lane's 16 logits are enough (8 of 256 for 32768 tokens: 9.9 us,
 // 11.6 with all kept).
-template <class T, int kLanes, int kItems, bool kFull>
+template <class T, int kLanes, int kItems, bool kWide>
 void launch_gate(const GateArgs& a, dim3 grid, dim3 block, hipStream_t s) {
-  if (kItems == 16 && a.k <= 8) gate_kernel<T, kLanes, kItems, kFull, kItems == 16 ? 8 : kItems><<<grid, block, 0, s>>>(a);
-  else gate_kernel<T, kLanes, kItems, kFull, kItems><<<grid, block, 0, s>>>(a);
+  if (kItems == 16 && a.k <= 8) gate_kernel<T, kLanes, kItems, kWide, kItems == 16 ? 8 : kItems><<<grid, block, 0, s>>>(a);
+  else gate_kernel<T, kLanes, kItems, kWide, kItems><<<grid, block, 0, s>>>(a);
 }
 
 template <class T, int kLanes, int kItems>
 void launch(const GateArgs& a, bool bwd, hipStream_t s) {
   const int64_t per = kWaves * (64 / kLanes), blocks = (a.tokens + per - 1) / per;
   const dim3 grid((uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), block(64 * kWaves);
-  constexpr uintptr_t kBytes = kItems * sizeof(T), kWord = kBytes < 16 ? kBytes : 16;
-  const bool full = a.E == kLanes * kItems && reinterpret_cast<uintptr_t>(a.logits) % kWord == 0 &&
+  constexpr uintptr_t kPiece = piece_of<T, kItems>(), kWord = kPiece * sizeof(T);
+  const bool wide = a.E % kPiece == 0 && reinterpret_cast<uintptr_t>(a.logits) % kWord == 0 &&
                     reinterpret_cast<uintptr_t>(a.grad_l) % kWord == 0;
   if (bwd)
-    full ? gate_bwd_kernel<T, kLanes, kItems, true><<<grid, block, 0, s>>>(a)
+    wide ? gate_bwd_kernel<T, kLanes, kItems, true><<<grid, block, 0, s>>>(a)
          : gate_bwd_kernel<T, kLanes, kItems, false><<<grid, block, 0, s>>>(a);
   else
-    full ? launch_gate<T, kLanes, kItems, true>(a, grid, block, s) : launch_gate<T, kLanes, kItems, false>(a, grid, block, s);
+    wide ? launch_gate<T, kLanes, kItems, true>(a, grid, block, s) : launch_gate<T, kLanes, kItems, false>(a, grid, block, s);
 }
 
 template <class T>
