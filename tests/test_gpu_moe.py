@@ -87,6 +87,32 @@ def test_gate(lp, T, E, k, dtype, kind):
         assert gl.dtype == dtype and (np.abs(got - ref) <= tol + k * TINY).all()
 
 
+@pytest.mark.parametrize("T,E,k", [(7, 203, 8), (6, 203, 12), (5, 144, 9), (9, 136, 8), (4, 1001, 5), (3, 1001, 20), (66, 12, 12), (5, 520, 8), (2, 509, 64)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["normal", "ties", "masked"])
+def test_gate_of_odd_rows(lp, T, E, k, dtype, kind):
+    test_gate(lp, T, E, k, dtype, kind)
+
+
+@pytest.mark.parametrize("E,k", [(64, 8), (256, 8), (256, 10), (512, 8), (1024, 9)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gate_of_logits_beside_a_16_byte_border(lp, E, k, dtype):
+    """What an aligned copy gives: the same experts, weights and gradients up to the order of the softmax's sum."""
+    rng = np.random.default_rng(E + k)
+    off = 4 // torch.empty(0, dtype=dtype).element_size()
+    l = dev(rng.standard_normal(33 * E + off).astype(np.float32)).to(dtype)[off:].view(33, E)
+    g, out = dev(rng.standard_normal((33, k)).astype(np.float32)), torch.empty(33 * E + off, dtype=dtype, device="cuda")[off:].view(33, E)
+    assert l.data_ptr() % 16 == 4 and out.data_ptr() % 16 == 4
+    for renorm in (False, True):
+        (w, e), (cw, ce) = lp.lp_moe_gate(l, k, renorm=renorm), lp.lp_moe_gate(l.clone(), k, renorm=renorm)
+        rtol = 2 * gate_rtol(None, E)
+        assert torch.equal(e, ce) and ((w - cw).abs() <= rtol * cw).all()
+        a, b = lp.lp_moe_gate_bwd(g, l, cw, ce, renorm=renorm, grad_logits=out), lp.lp_moe_gate_bwd(g, l.clone(), cw, ce, renorm=renorm)
+        # (each p of the softmax times the inner product, and a rounding to bf16)
+        size = (cw * g.abs()).sum(1, keepdim=True)
+        assert ((a - b).float().abs() <= 2 * rtol * size + 2 * (U16 if dtype == torch.bfloat16 else U32) * b.float().abs()).all()
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_gate_of_a_row_that_is_not_finite(lp, dtype, bad):
