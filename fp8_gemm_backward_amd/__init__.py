@@ -830,13 +830,15 @@ def lp_moe_sort(experts: torch.Tensor, groups: int, stream=None) -> tuple:
     outside 0 .. groups-1); order: every row's pair t * k + j (unwritten past
     the last offset)."""
     n = experts.numel()
-    new = _new(experts, stream)
-    offsets, order = new((groups,), dtype=torch.int32), new((n,), dtype=torch.int32)
-    rows = new(experts.shape, dtype=torch.int32)
     _device(experts, "experts", 4 * n, torch.int32)
+    if groups < 0:
+        raise LpError(2, "lp_moe_sort")
+    # (one allocation for the three: 1 us less of the host's 10)
+    offsets, order, rows = _new(experts, stream)((groups + 2 * n,), dtype=torch.int32).split_with_sizes((groups, n, n))
+    rows = rows.view(experts.shape)
     ws, nbytes = None, ctypes.c_size_t(0)
-    _check(lib.lp_moe_sort_workspace(n, groups, ctypes.byref(nbytes)), "lp_moe_sort_workspace")
-    if nbytes.value:
+    if n > 65536:                                            # (up to there one launch, which needs none)
+        _check(lib.lp_moe_sort_workspace(n, groups, ctypes.byref(nbytes)), "lp_moe_sort_workspace")
         ws = _new(experts, stream, result=False)((nbytes.value,), dtype=torch.uint8)
     _check(lib.lp_moe_sort(experts.data_ptr(), n, groups, offsets.data_ptr(), rows.data_ptr(), order.data_ptr(),
                            None if ws is None else ws.data_ptr(), nbytes.value, _stream(stream)), "lp_moe_sort")

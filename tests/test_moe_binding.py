@@ -21,8 +21,19 @@ def made(monkeypatch):
     return calls
 
 
+class Tensor(DeviceTensor):
+    def new_empty(self, shape, dtype=None):
+        return Tensor(shape, dtype or self.dtype)
+
+    def split_with_sizes(self, sizes):
+        return [Tensor((n,), self.dtype) for n in sizes]
+
+    def view(self, shape):
+        return Tensor(shape, self.dtype)
+
+
 def t(*shape, dtype=BF, ptr=0x10000):
-    return DeviceTensor(shape, dtype, ptr)
+    return Tensor(shape, dtype, ptr)
 
 
 def refused(made, *calls):
