@@ -308,12 +308,14 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kEu)))
 // The instantiated shapes of a workgroup, and their times in units of 10 ns:
 // fixed, and for every round of 256 workgroups (the first one, each further one) a
 // step of a wave's part of the contraction and, each further one, a fixed time too.
-// Fitted to 1500 measured problems (1 to 4096 rows, dense and up to 64 groups,
+// Fitted to 2500 measured problems (1 to 4096 rows, dense and up to 64 groups,
 // weights from HBM, both formats) with 7 to 18% of scatter: the shape they choose
 // is within 3% of the fastest on average, within 1.4 times in 99 of 100 (the grouped
 // ones' row tiles known only as a bound).  64 rows by one
 // column tile a wave ({2, 1, 4}, {1, 1, 4}) serve some hundred rows of middling
-// weights: 212 x 3488 x 4992 23 us (34.5 without them), 171 x 3616 x 1984 12.5 (18.9).
+// weights: 212 x 3488 x 4992 23 us (34.5 without them), 171 x 3616 x 1984 12.5 (18.9);
+// 80 rows ({1, 2, 5}) 1000 x 4112 x 4128, whose tiles of 112 left a third of the CUs
+// without any: 41 us (48).
 struct Shape {
   int8_t wk, nc, rt;
   int16_t fixed, step, more, round;
@@ -321,8 +323,8 @@ struct Shape {
 constexpr Shape kShapes[] = {
     {8, 1, 1, 320, 58, 76, 59},    {4, 1, 1, 412, 43, 62, 256},   {2, 1, 1, 425, 37, 48, 274},   {1, 2, 1, 347, 58, 52, 141},
     {4, 1, 2, 428, 69, 82, 260},   {2, 1, 2, 433, 51, 59, 280},   {2, 1, 4, 444, 86, 91, 316},   {4, 2, 3, 459, 120, 132, 307},
-    {2, 2, 4, 522, 110, 123, 418}, {1, 2, 4, 404, 98, 96, 213},   {1, 1, 6, 382, 91, 68, 161},   {1, 2, 7, 504, 144, 157, 511},
-    {1, 2, 8, 454, 162, 179, 494}, {1, 1, 4, 373, 67, 51, 160},
+    {2, 2, 4, 522, 110, 123, 418}, {1, 2, 4, 404, 98, 96, 213},   {1, 1, 6, 382, 91, 68, 161},   {1, 2, 5, 498, 112, 136, 364},
+    {1, 2, 8, 454, 162, 179, 494}, {1, 1, 4, 373, 67, 51, 160},   {1, 2, 3, 424, 82, 91, 189},  {2, 2, 5, 519, 128, 150, 379},
 };
 constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
 // The same of the 256 x 256 tiles that decode into LDS; their matrix cores, busier,
@@ -391,7 +393,9 @@ hipError_t launch_shape(const W4Args& a, int shape, hipStream_t s) {
     case 10: return launch<F, 10, 3, 1, 4>(a, s);
     case 11: return launch<F, 11, 2, 2>(a, s);
     case 12: return launch<F, 12, 2, 1>(a, s);
-    default: return launch<F, 13, 2, 2>(a, s);
+    case 13: return launch<F, 13, 2, 2>(a, s);
+    case 14: return launch<F, 14, 2, 2>(a, s);
+    default: return launch<F, 15, 2, 1>(a, s);
   }
 }
 

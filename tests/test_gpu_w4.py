@@ -66,9 +66,10 @@ GROUPED = [(3, 16, 32, 2), (34, 128, 160, 33), (282, 496, 160, 2), (109, 592, 32
 
 
 # Those of the shapes that take middling sizes, and the large tiles.
-MIDDLING = [(2713, 288, 416), (212, 3488, 1024), (97, 9280, 2464), (393, 9392, 416), (2181, 288, 32), (1266, 6992, 32), (1348, 8832, 96)]
+MIDDLING = [(2713, 288, 416), (212, 3488, 1024), (97, 9280, 2464), (393, 9392, 416), (2181, 288, 32), (1266, 6992, 32), (1348, 8832, 96),
+            (489, 9344, 32), (197, 8320, 672), (294, 8368, 416)]
 MIDDLING_GROUPED = [(2099, 336, 416, 2), (205, 1632, 1056, 9), (98, 9312, 2464, 2), (398, 9360, 416, 2), (2059, 336, 32, 2), (971, 8848, 32, 2),
-                    (49, 1616, 1056, 9), (157, 9520, 32, 5), (3100, 6000, 32, 2)]
+                    (49, 1616, 1056, 9), (157, 9520, 32, 5), (3100, 6000, 32, 2), (175, 9232, 32, 5), (1178, 288, 672, 70), (71, 3792, 32, 33)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
