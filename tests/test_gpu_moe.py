@@ -457,3 +457,22 @@ def test_gather_quant_of_pairs_out_of_range_beside_a_nan_weight(lp, H):
         plain = lp.lp_moe_combine_bwd(x, None, dev(rows.reshape(T, k)), dev(w), need_dw=False)[0]
         plain[[1, 33, 74]] = 0
         same_runs(lp, lp.lp_moe_gather_quant(x, dev(bad), off, k, weights=dev(w)), lp.lp_r128_quant_dual(plain, off), off, H)
+
+
+@pytest.mark.parametrize("H", [144, 4096])
+@pytest.mark.parametrize("ends", [[5, 2, 9], [-3, 4, 1 << 30], [0, 0, 0], [1 << 30, 0, -1], [30, 20, 80]])
+def test_gather_quant_of_bad_offsets(lp, ends, H):
+    """Ends that fall, below zero or past the rows: taken as the largest so far, within the rows, as the quantizer takes
+    them (64 groups and more of them empty, so that both ways of sharing out the tiles are met)."""
+    T, k = 40, 2
+    rng = np.random.default_rng(6)
+    ends = ends + [ends[-1]] * 61
+    off = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    clean = torch.from_numpy(np.maximum.accumulate(np.clip(ends, 0, T * k))).int()
+    order = rng.permutation(T * k).astype(np.int32)
+    rows = np.empty(T * k, np.int32)
+    rows[order] = np.arange(T * k)
+    x = bf16_dev(bits(rng, (T, H)))
+    plain = lp.lp_moe_gather(x, dev(rows.reshape(T, k)))
+    got = lp.lp_moe_gather_quant(x, dev(order), off, k)
+    same_runs(lp, got, lp.lp_r128_quant_dual(plain, clean.cuda()), clean, H)
