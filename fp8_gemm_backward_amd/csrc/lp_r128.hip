@@ -375,8 +375,9 @@ __global__ __launch_bounds__(kTileThreads) void r128_mapped(TileArgs a, RowMap m
 // up), side by side with 128 threads each where the run has up to 32 rows, else in turn.
 // Of one tile each their number and the chain offsets, order, rows, scales bound them, whatever
 // they hold: 128 tokens of 7168 to 8 of 64 experts 17.8 us, by fours 10.9; 500 of 4096 to
-// 8 of 256 40.5 and 20.  From 20 to 40 rows a group on that is lost again (256 tokens 21.3 and
-// 23.3), and where the tiles do not fill the GPU (1034 of 176 to 2 of 131: 4.7 and 5.0).
+// 8 of 256 40.5 and 20; 32 rows an expert on average, even or by popularity: 20 and 21, 20
+// and 16 (64 experts, 7168), 49 and 37, 49 and 29 (256, 4096).  With 96 28 and 37, 29 and 32
+// (64); also lost where the tiles do not fill the GPU (1034 of 176 to 2 of 131: 4.7 and 5.0).
 constexpr int kShortThreads = 128, kShortTiles = kTileThreads / kShortThreads, kShortRows = kRunLen / kShortTiles;
 
 template <bool kWeighted>
@@ -439,7 +440,7 @@ hipError_t launch_moe_gather_quant(const void* x, int64_t tokens, int64_t topk, 
                    (int32_t)rows, (int32_t)cols, make_fastdiv((uint32_t)ct), make_fastdiv((uint32_t)rt)};
   const RowMap map{order, weights, make_fastdiv((uint32_t)topk), (uint32_t)rows};
   const dim3 grid((uint32_t)(rt * ct)), block(kTileThreads);
-  if (rows <= 16 * groups && rt * ct >= 1024) {
+  if (rows <= 32 * groups && rt * ct >= 1024) {
     const int64_t fours = (ct + kShortTiles - 1) / kShortTiles;
     const FastDiv by_four = make_fastdiv((uint32_t)fours);
     const dim3 few((uint32_t)(rt * fours));
