@@ -294,6 +294,26 @@ def test_captured_sorts_have_workspaces_of_their_own(lp):
             assert torch.equal(off, eoff) and torch.equal(rows, erows) and torch.equal(order[:n], eorder[:n])
 
 
+@pytest.mark.parametrize("n", [7, 2000, 5000, 65536, 70000])
+def test_captured_sort_over_the_most_experts(lp, n):
+    """1024 experts: the counters take more LDS than 64 KB."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    e_in = [torch.randint(-1, 1024, (n, 1), generator=gen, device="cuda").int() for _ in range(3)]
+    e = e_in[0].clone()
+    lp.lp_moe_sort(e, 1024)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        off, rows, order = lp.lp_moe_sort(e, 1024)
+    for v in e_in + e_in[:1]:
+        e.copy_(v)
+        graph.replay()
+        want = lp.lp_moe_sort(v, 1024)
+        torch.cuda.synchronize()
+        live = int(want[0][-1])
+        assert torch.equal(off, want[0]) and torch.equal(rows, want[1]) and torch.equal(order[:live], want[2][:live])
+
+
 # ---------------------------------------------------------------- other streams
 
 NAMES = ["lp_moe_gate", "lp_moe_gate_bwd", "lp_moe_sort", "lp_moe_gather", "lp_moe_gather_quant", "lp_moe_combine",
