@@ -134,7 +134,22 @@ struct TileLds {
   alignas(16) uint16_t max[kTileWaves][kRunLen];
   alignas(16) float r[kRunLen], l[kRunLen];                // of the runs along the rows (RunRecip)
   uint32_t bad[kRunLen / 64];                              // whether one of 64 columns has a bad run
+  int rows[2];                                             // run_rows_once
 };
+
+// run_rows by the first wave, for all of a workgroup.
+__device__ __forceinline__ void run_rows_once(const TileArgs& a, TileLds& sh, int run, int& r0, int& r1) {
+  if (threadIdx.x < 64) {
+    run_rows(a.offsets, a.groups, a.rows, run, r0, r1);
+    if (threadIdx.x == 0) {
+      sh.rows[0] = r0;
+      sh.rows[1] = r1;
+    }
+  }
+  __syncthreads();
+  r0 = __builtin_amdgcn_readfirstlane(sh.rows[0]);
+  r1 = __builtin_amdgcn_readfirstlane(sh.rows[1]);
+}
 
 __device__ __forceinline__ float bf16_at(u32x4 v, int e) { return e % 2 ? bf16_hi(v[e / 2]) : bf16_lo(v[e / 2]); }
 
@@ -361,7 +376,7 @@ __global__ __launch_bounds__(kTileThreads) void r128_mapped(TileArgs a, RowMap m
   __shared__ TileLds sh;
   const int rb = fdiv(blockIdx.x, a.col_tiles), ct = blockIdx.x - rb * a.col_tiles.d;
   int r0, r1;
-  run_rows(a.offsets, a.groups, a.rows, rb, r0, r1);
+  run_rows_once(a, sh, rb, r0, r1);
   if (r1 == r0) return;
   u32x4 v[kTileRows];
   mapped_values<kWeighted, kTileThreads>(a, map, ct, r0, r1, v);
