@@ -327,7 +327,7 @@ __global__ __launch_bounds__(kTileThreads) void r128_tile(TileArgs a) {
 
 // Results larger than a quarter of the 256 MB cache are stored past the caches: 4096
 // tokens to 8 experts each, 7168 wide, read x (59 MB, each row k times) faster from a
-// cache that 470 MB of codes do not wash through, 118 us in all (150).
+// cache that 470 MB of codes do not wash through, 117 us in all (150).
 constexpr int64_t kCacheBytes = (int64_t)64 << 20;
 
 // Rows that come from elsewhere: row r is row order[r] / k of src, times
