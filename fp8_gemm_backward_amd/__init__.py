@@ -853,10 +853,10 @@ def _tokens(rows: torch.Tensor) -> tuple:
     return T, k
 
 
-def _matrix(t: torch.Tensor, name: str, rows: int) -> int:
-    """Columns of a bf16 matrix [rows, columns]."""
-    if t.dim() != 2 or t.shape[0] != rows:
-        raise ValueError(f"{name} must be [{rows}, columns], not {tuple(t.shape)}")
+def _matrix(t: torch.Tensor, name: str, rows: int, cols: Optional[int] = None) -> int:
+    """Columns of a bf16 matrix [rows, columns] (cols: that many)."""
+    if t.dim() != 2 or t.shape[0] != rows or cols not in (None, t.shape[1]):
+        raise ValueError(f"{name} must be [{rows}, {'columns' if cols is None else cols}], not {tuple(t.shape)}")
     _device(t, name, 2 * rows * t.shape[1], torch.bfloat16)
     return t.shape[1]
 
@@ -869,8 +869,7 @@ def lp_moe_gather(x: torch.Tensor, rows: torch.Tensor, out: Optional[torch.Tenso
     if out is None:
         out = _new(x, stream)((T * k, H), dtype=torch.bfloat16)
     else:
-        _matrix(out, "out", T * k)
-        _device(out, "out", 2 * T * k * H)
+        _matrix(out, "out", T * k, H)
     _check(lib.lp_moe_gather(x.data_ptr(), T, k, H, rows.data_ptr(), out.data_ptr(), _stream(stream)), "lp_moe_gather")
     return out
 
@@ -923,8 +922,7 @@ def lp_moe_combine(y: torch.Tensor, rows: torch.Tensor, weights: Optional[torch.
     if out is None:
         out = _new(y, stream)((T, H), dtype=torch.bfloat16)
     else:
-        _matrix(out, "out", T)
-        _device(out, "out", 2 * T * H)
+        _matrix(out, "out", T, H)
     _check(lib.lp_moe_combine(y.data_ptr(), T, k, H, rows.data_ptr(), None if weights is None else weights.data_ptr(),
                               out.data_ptr(), _stream(stream)), "lp_moe_combine")
     return out
