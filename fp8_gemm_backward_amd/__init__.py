@@ -861,6 +861,12 @@ def _matrix(t: torch.Tensor, name: str, rows: int, cols: Optional[int] = None) -
     return t.shape[1]
 
 
+def _width(t: torch.Tensor, name: str, cols: int) -> None:
+    """Refuses a tensor of several dimensions whose rows are not `cols` long."""
+    if t.dim() > 1 and t.shape[-1] != cols:
+        raise ValueError(f"{name} must have rows of {cols}, not {tuple(t.shape)}")
+
+
 def lp_moe_gather(x: torch.Tensor, rows: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """bf16 rows [T * k, H]: out[rows[t, j]] = x[t] (rows as lp_moe_sort makes
     them).  Rows of no pair are left as they were in `out`."""
@@ -944,8 +950,10 @@ def lp_moe_combine_bwd(grad: torch.Tensor, y: Optional[torch.Tensor], rows: torc
             grad_y = _new(grad, stream)((T * k, H), dtype=torch.bfloat16)
         else:
             _device(grad_y, "grad_y", 2 * T * k * H, torch.bfloat16)
+            _width(grad_y, "grad_y", H)
     if need_dw:
         _device(y, "y", 2 * T * k * H, torch.bfloat16)
+        _width(y, "y", H)
         if grad_weights is None:
             grad_weights = _new(grad, stream)((T, k), dtype=torch.float32)
         else:
