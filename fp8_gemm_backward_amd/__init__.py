@@ -973,6 +973,7 @@ def _fwd_w4(x: torch.Tensor, w: QTensor, offsets: Optional[torch.Tensor], y: Opt
         y = _new(x, stream)((M, w.rows), dtype=torch.bfloat16)
     else:
         _device(y, "y", 2 * M * w.rows, torch.bfloat16)
+        _width(y, "y", w.rows)
     wc = w.c()
     if offsets is None:
         _check(lib.lp_linear_fwd_w4(x.data_ptr(), M, ctypes.byref(wc), y.data_ptr(), _stream(stream)), "lp_linear_fwd_w4")

@@ -25,3 +25,13 @@ def test_the_rows_of_combines_gradient_have_its_width(made):  # noqa: F811
     refused(made, lambda: lp.lp_moe_combine_bwd(t(7, 32), t(14, 48), rows, w), lambda: lp.lp_moe_combine_bwd(t(7, 32), t(7, 64), rows, w),
             lambda: lp.lp_moe_combine_bwd(t(7, 32), t(14, 32), rows, w, grad_y=t(14, 48)),
             lambda: lp.lp_moe_combine_bwd(t(7, 32), t(14, 32), rows, w, grad_y=t(28, 16)))
+
+
+def test_results_of_the_4_bit_forward_have_its_width(made):  # noqa: F811
+    def weight(batch):
+        return lp.QTensor("mxfp4", t(batch, 48, 32, dtype=torch.uint8), t(batch, 48, 2, dtype=torch.uint8), None, (batch, 48, 64))
+    lp.lp_linear_fwd_w4(t(3, 64), weight(1), y=t(5, 48))
+    lp.lp_grouped_fwd_w4(t(3, 64), weight(2), t(2, dtype=I), y=t(3 * 48))
+    made.clear()
+    refused(made, lambda: lp.lp_linear_fwd_w4(t(3, 64), weight(1), y=t(3, 64)), lambda: lp.lp_linear_fwd_w4(t(3, 64), weight(1), y=t(48, 3)),
+            lambda: lp.lp_grouped_fwd_w4(t(3, 64), weight(2), t(2, dtype=I), y=t(3, 64)))
