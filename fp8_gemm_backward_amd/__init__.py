@@ -783,6 +783,19 @@ def _gate_dtype(logits: torch.Tensor) -> int:
     return _GATE_DTYPE[logits.dtype]
 
 
+def _width(t: torch.Tensor, name: str, cols: int) -> None:
+    """Refuses a tensor of several dimensions whose rows are not `cols` long."""
+    if t.dim() > 1 and t.shape[-1] != cols:
+        raise ValueError(f"{name} must have rows of {cols}, not {tuple(t.shape)}")
+
+
+def _pairs(t: torch.Tensor, name: str, tokens: int, topk: int, dtype) -> None:
+    """A number for each (token, slot) pair: [tokens, topk], or as many in another shape."""
+    _device(t, name, 4 * tokens * topk, dtype)
+    if t.numel() != tokens * topk:
+        _width(t, name, topk)
+
+
 def lp_moe_gate(logits: torch.Tensor, topk: int, renorm: bool = True, weights: Optional[torch.Tensor] = None,
                 chosen: Optional[torch.Tensor] = None, stream=None) -> tuple:
     """(weights float32 [T, topk], chosen int32 [T, topk]) of logits [T, E]
@@ -791,13 +804,15 @@ def lp_moe_gate(logits: torch.Tensor, topk: int, renorm: bool = True, weights: O
     their softmax probabilities, divided by their sum with renorm."""
     T, E = logits.shape
     dtype = _gate_dtype(logits)
+    _device(logits, "logits", T * E * logits.element_size())
+    if weights is not None:
+        _pairs(weights, "weights", T, topk, torch.float32)
+    if chosen is not None:
+        _pairs(chosen, "chosen", T, topk, torch.int32)
     if weights is None or chosen is None:
         new = _new(logits, stream)
         weights = new((T, topk), dtype=torch.float32) if weights is None else weights
         chosen = new((T, topk), dtype=torch.int32) if chosen is None else chosen
-    _device(logits, "logits", T * E * logits.element_size())
-    _device(weights, "weights", 4 * T * topk, torch.float32)
-    _device(chosen, "chosen", 4 * T * topk, torch.int32)
     _check(lib.lp_moe_gate(logits.data_ptr(), dtype, T, E, topk, int(renorm), weights.data_ptr(), chosen.data_ptr(),
                            _stream(stream)), "lp_moe_gate")
     return weights, chosen
@@ -810,12 +825,14 @@ def lp_moe_gate_bwd(grad_weights: torch.Tensor, logits: torch.Tensor, weights: t
     T, E = logits.shape
     k = chosen.shape[-1]
     dtype = _gate_dtype(logits)
+    _device(logits, "logits", T * E * logits.element_size())
     if grad_logits is None:
         grad_logits = _new(logits, stream)((T, E), dtype=logits.dtype)
-    _device(logits, "logits", T * E * logits.element_size())
-    _device(grad_logits, "grad_logits", T * E * logits.element_size(), logits.dtype)
-    _device(grad_weights, "grad_weights", 4 * T * k, torch.float32)
-    _device(weights, "weights", 4 * T * k, torch.float32)
+    else:
+        _device(grad_logits, "grad_logits", T * E * logits.element_size(), logits.dtype)
+        _width(grad_logits, "grad_logits", E)
+    _pairs(grad_weights, "grad_weights", T, k, torch.float32)
+    _pairs(weights, "weights", T, k, torch.float32)
     _device(chosen, "chosen", 4 * T * k, torch.int32)
     _check(lib.lp_moe_gate_bwd(grad_weights.data_ptr(), logits.data_ptr(), dtype, T, E, k, int(renorm),
                                weights.data_ptr(), chosen.data_ptr(), grad_logits.data_ptr(), _stream(stream)),
@@ -861,12 +878,6 @@ def _matrix(t: torch.Tensor, name: str, rows: int, cols: Optional[int] = None) -
     return t.shape[1]
 
 
-def _width(t: torch.Tensor, name: str, cols: int) -> None:
-    """Refuses a tensor of several dimensions whose rows are not `cols` long."""
-    if t.dim() > 1 and t.shape[-1] != cols:
-        raise ValueError(f"{name} must have rows of {cols}, not {tuple(t.shape)}")
-
-
 def lp_moe_gather(x: torch.Tensor, rows: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """bf16 rows [T * k, H]: out[rows[t, j]] = x[t] (rows as lp_moe_sort makes
     them).  Rows of no pair are left as they were in `out`."""
@@ -894,7 +905,7 @@ def lp_moe_gather_quant(x: torch.Tensor, order: torch.Tensor, offsets: torch.Ten
     _device(order, "order", 4 * M, torch.int32)
     _device(offsets, "offsets", 4 * G, torch.int32)
     if weights is not None:
-        _device(weights, "weights", 4 * M, torch.float32)
+        _pairs(weights, "weights", T, topk, torch.float32)
     runs, nb = M // 128 + G, -(-H // 128)
     if out is None:
         new = _new(x, stream)
@@ -924,7 +935,7 @@ def lp_moe_combine(y: torch.Tensor, rows: torch.Tensor, weights: Optional[torch.
     T, k = _tokens(rows)
     H = _matrix(y, "y", T * k)
     if weights is not None:
-        _device(weights, "weights", 4 * T * k, torch.float32)
+        _pairs(weights, "weights", T, k, torch.float32)
     if out is None:
         out = _new(y, stream)((T, H), dtype=torch.bfloat16)
     else:
@@ -944,7 +955,7 @@ def lp_moe_combine_bwd(grad: torch.Tensor, y: Optional[torch.Tensor], rows: torc
     T, k = _tokens(rows)
     H = _matrix(grad, "grad", T)
     if weights is not None:
-        _device(weights, "weights", 4 * T * k, torch.float32)
+        _pairs(weights, "weights", T, k, torch.float32)
     if need_dy:
         if grad_y is None:
             grad_y = _new(grad, stream)((T * k, H), dtype=torch.bfloat16)
@@ -957,7 +968,7 @@ def lp_moe_combine_bwd(grad: torch.Tensor, y: Optional[torch.Tensor], rows: torc
         if grad_weights is None:
             grad_weights = _new(grad, stream)((T, k), dtype=torch.float32)
         else:
-            _device(grad_weights, "grad_weights", 4 * T * k, torch.float32)
+            _pairs(grad_weights, "grad_weights", T, k, torch.float32)
     _check(lib.lp_moe_combine_bwd(grad.data_ptr(), y.data_ptr() if need_dw else None, T, k, H, rows.data_ptr(),
                                   None if weights is None else weights.data_ptr(), grad_y.data_ptr() if need_dy else None,
                                   grad_weights.data_ptr() if need_dw else None, _stream(stream)), "lp_moe_combine_bwd")

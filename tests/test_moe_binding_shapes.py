@@ -35,3 +35,23 @@ def test_results_of_the_4_bit_forward_have_its_width(made):  # noqa: F811
     made.clear()
     refused(made, lambda: lp.lp_linear_fwd_w4(t(3, 64), weight(1), y=t(3, 64)), lambda: lp.lp_linear_fwd_w4(t(3, 64), weight(1), y=t(48, 3)),
             lambda: lp.lp_grouped_fwd_w4(t(3, 64), weight(2), t(2, dtype=I), y=t(3, 64)))
+
+
+def test_numbers_by_pair_and_gradients_of_logits_have_their_width(made):  # noqa: F811
+    """A slot more a token than the call has: refused; the same numbers in another shape: taken."""
+    rows, w, e, wide = t(7, 2, dtype=I), t(7, 2, dtype=F), t(7, 2, dtype=I), t(7, 3, dtype=F)
+    order, off = t(14, dtype=I), t(3, dtype=I)
+    for same in (w, t(14, dtype=F), t(14, 1, dtype=F), t(1, 7, 2, dtype=F), t(9, 2, dtype=F)):
+        lp.lp_moe_combine(t(14, 32), rows, same)
+        lp.lp_moe_combine_bwd(t(7, 32), t(14, 32), rows, same)
+        lp.lp_moe_gather_quant(t(7, 144), order, off, 2, weights=same)
+        lp.lp_moe_gate_bwd(same, t(7, 12), same, e)
+        lp.lp_moe_gate(t(7, 12), 2, weights=same, chosen=e)
+    lp.lp_moe_gate_bwd(w, t(7, 12), w, e, grad_logits=t(8, 12))
+    made.clear()
+    refused(made, lambda: lp.lp_moe_combine(t(14, 32), rows, wide), lambda: lp.lp_moe_combine_bwd(t(7, 32), t(14, 32), rows, wide),
+            lambda: lp.lp_moe_combine_bwd(t(7, 32), t(14, 32), rows, w, grad_weights=wide),
+            lambda: lp.lp_moe_gather_quant(t(7, 144), order, off, 2, weights=wide),
+            lambda: lp.lp_moe_gate(t(7, 12), 2, weights=wide, chosen=e), lambda: lp.lp_moe_gate(t(7, 12), 2, weights=w, chosen=t(7, 3, dtype=I)),
+            lambda: lp.lp_moe_gate_bwd(wide, t(7, 12), w, e), lambda: lp.lp_moe_gate_bwd(w, t(7, 12), wide, e),
+            lambda: lp.lp_moe_gate_bwd(w, t(7, 12), w, e, grad_logits=t(7, 16)))
