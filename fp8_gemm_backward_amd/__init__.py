@@ -914,8 +914,8 @@ def lp_moe_gather_quant(x: torch.Tensor, order: torch.Tensor, offsets: torch.Ten
                QTensor("fp8_r128", new((1, M, H), dtype=torch.uint8), new((1, runs, H), dtype=torch.float32), None,
                        (1, M, H), -2, G))
     else:
-        for q, n, name in zip(out, (nb * M, runs * H), ("out[0]", "out[1]")):
-            if q.fmt != "fp8_r128" or tuple(q.shape) != (1, M, H) or q.axis != (-1 if q is out[0] else -2):
+        for q, n, axis, name in zip(out, (nb * M, runs * H), (-1, -2), ("out[0]", "out[1]")):
+            if q.fmt != "fp8_r128" or tuple(q.shape) != (1, M, H) or q.axis != axis:
                 raise ValueError(f"{name}: not the tensor this call writes")
             _device(q.codes, f"{name} codes", M * H, torch.uint8)
             _device(q.scales, f"{name} scales", 4 * n, torch.float32)

@@ -55,3 +55,14 @@ def test_numbers_by_pair_and_gradients_of_logits_have_their_width(made):  # noqa
             lambda: lp.lp_moe_gate(t(7, 12), 2, weights=wide, chosen=e), lambda: lp.lp_moe_gate(t(7, 12), 2, weights=w, chosen=t(7, 3, dtype=I)),
             lambda: lp.lp_moe_gate_bwd(wide, t(7, 12), w, e), lambda: lp.lp_moe_gate_bwd(w, t(7, 12), wide, e),
             lambda: lp.lp_moe_gate_bwd(w, t(7, 12), w, e, grad_logits=t(7, 16)))
+
+
+def test_the_two_fp8_copies_are_told_apart_by_place(made):  # noqa: F811
+    """One tensor given for both would be written twice: its scales are large enough for both where rows are short."""
+    order, off = t(2000, dtype=I), t(3, dtype=I)
+    cols, toks = lp.lp_moe_gather_quant(t(1000, 16), order, off, 2)
+    assert cols.scales.nbytes >= toks.scales.nbytes
+    made.clear()
+    refused(made, lambda: lp.lp_moe_gather_quant(t(1000, 16), order, off, 2, out=(cols, cols)),
+            lambda: lp.lp_moe_gather_quant(t(1000, 16), order, off, 2, out=(toks, toks)),
+            lambda: lp.lp_moe_gather_quant(t(1000, 16), order, off, 2, out=(toks, cols)))
