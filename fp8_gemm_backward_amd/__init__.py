@@ -964,14 +964,16 @@ def lp_moe_combine_bwd(grad: torch.Tensor, y: Optional[torch.Tensor], rows: torc
             _width(grad_y, "grad_y", H)
     if need_dw:
         _device(y, "y", 2 * T * k * H, torch.bfloat16)
-        _width(y, "y", H)
+        if y is not None:
+            _width(y, "y", H)
         if grad_weights is None:
             grad_weights = _new(grad, stream)((T, k), dtype=torch.float32)
         else:
             _pairs(grad_weights, "grad_weights", T, k, torch.float32)
-    _check(lib.lp_moe_combine_bwd(grad.data_ptr(), y.data_ptr() if need_dw else None, T, k, H, rows.data_ptr(),
-                                  None if weights is None else weights.data_ptr(), grad_y.data_ptr() if need_dy else None,
-                                  grad_weights.data_ptr() if need_dw else None, _stream(stream)), "lp_moe_combine_bwd")
+    _check(lib.lp_moe_combine_bwd(grad.data_ptr(), y.data_ptr() if need_dw and y is not None else None, T, k, H,
+                                  rows.data_ptr(), None if weights is None else weights.data_ptr(),
+                                  grad_y.data_ptr() if need_dy else None, grad_weights.data_ptr() if need_dw else None,
+                                  _stream(stream)), "lp_moe_combine_bwd")
     return (grad_y if need_dy else None), (grad_weights if need_dw else None)
 
 

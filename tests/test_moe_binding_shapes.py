@@ -66,3 +66,10 @@ def test_the_two_fp8_copies_are_told_apart_by_place(made):  # noqa: F811
     refused(made, lambda: lp.lp_moe_gather_quant(t(1000, 16), order, off, 2, out=(cols, cols)),
             lambda: lp.lp_moe_gather_quant(t(1000, 16), order, off, 2, out=(toks, toks)),
             lambda: lp.lp_moe_gather_quant(t(1000, 16), order, off, 2, out=(toks, cols)))
+
+
+def test_combines_gradient_of_nothing_needs_no_rows(made):  # noqa: F811
+    """No token, or rows of no column: the C call reads no y, and none has to be given."""
+    for T, H in ((0, 32), (7, 0)):
+        gy, gw = lp.lp_moe_combine_bwd(t(T, H), None, t(T, 2, dtype=I))
+        assert gy.shape == (2 * T, H) and gw.shape == (T, 2) and made.pop()[1][1] is None
