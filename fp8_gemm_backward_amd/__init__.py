@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 import re
 from typing import Optional
@@ -840,6 +841,14 @@ def lp_moe_gate_bwd(grad_weights: torch.Tensor, logits: torch.Tensor, weights: t
     return grad_logits
 
 
+@functools.lru_cache(maxsize=256)
+def _sort_workspace(pairs: int, groups: int) -> int:
+    """Bytes of workspace that a sort needs (asked of the library once for a size: 0.2 us a call, 1.8 asked anew)."""
+    nbytes = ctypes.c_size_t(0)
+    _check(lib.lp_moe_sort_workspace(pairs, groups, ctypes.byref(nbytes)), "lp_moe_sort")
+    return nbytes.value
+
+
 def lp_moe_sort(experts: torch.Tensor, groups: int, stream=None) -> tuple:
     """(offsets int32 [groups], rows int32 like experts, order int32 [pairs]) of
     int32 experts [T, k]: the pairs stably sorted by expert.  offsets: the
@@ -848,17 +857,13 @@ def lp_moe_sort(experts: torch.Tensor, groups: int, stream=None) -> tuple:
     the last offset)."""
     n = experts.numel()
     _device(experts, "experts", 4 * n, torch.int32)
-    if groups < 0:
-        raise LpError(2, "lp_moe_sort")
+    nbytes = _sort_workspace(n, groups)
     # (one allocation for the three: 1 us less of the host's 10)
     offsets, order, rows = _new(experts, stream)((groups + 2 * n,), dtype=torch.int32).split_with_sizes((groups, n, n))
     rows = rows.view(experts.shape)
-    ws, nbytes = None, ctypes.c_size_t(0)
-    if n > 65536:                                            # (up to there one launch, which needs none)
-        _check(lib.lp_moe_sort_workspace(n, groups, ctypes.byref(nbytes)), "lp_moe_sort_workspace")
-        ws = _new(experts, stream, result=False)((nbytes.value,), dtype=torch.uint8)
+    ws = _new(experts, stream, result=False)((nbytes,), dtype=torch.uint8) if nbytes else None
     _check(lib.lp_moe_sort(experts.data_ptr(), n, groups, offsets.data_ptr(), rows.data_ptr(), order.data_ptr(),
-                           None if ws is None else ws.data_ptr(), nbytes.value, _stream(stream)), "lp_moe_sort")
+                           None if ws is None else ws.data_ptr(), nbytes, _stream(stream)), "lp_moe_sort")
     return offsets, rows, order
 
 

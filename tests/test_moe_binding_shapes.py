@@ -73,3 +73,31 @@ def test_combines_gradient_of_nothing_needs_no_rows(made):  # noqa: F811
     for T, H in ((0, 32), (7, 0)):
         gy, gw = lp.lp_moe_combine_bwd(t(T, H), None, t(T, 2, dtype=I))
         assert gy.shape == (2 * T, H) and gw.shape == (T, 2) and made.pop()[1][1] is None
+
+
+def test_the_sorts_workspace_is_what_the_library_asks_for(made, monkeypatch):  # noqa: F811
+    """Up to any number of pairs: the binding has no limit of its own."""
+    asked = []
+
+    def workspace(pairs, groups, nbytes):
+        asked.append((pairs, groups))
+        nbytes._obj.value = 0 if pairs <= 100 else 16 * pairs
+        return 0
+    monkeypatch.setattr(lp.lib, "lp_moe_sort_workspace", workspace)
+    lp._sort_workspace.cache_clear()
+    try:
+        for pairs in (0, 8, 100, 101, 65536, 65537):
+            lp.lp_moe_sort(t(pairs, dtype=I), 4)
+            name, args = made.pop()
+            assert name == "lp_moe_sort" and args[1:3] == (pairs, 4)
+            assert (args[6] is None, args[7]) == ((True, 0) if pairs <= 100 else (False, 16 * pairs))
+        assert asked == [(n, 4) for n in (0, 8, 100, 101, 65536, 65537)]
+    finally:
+        lp._sort_workspace.cache_clear()
+
+
+def test_the_sorts_workspace_is_refused_as_the_sort_is():
+    for pairs, groups in ((8, 0), (8, 1025), (1 << 30, 4)):
+        with pytest.raises(lp.LpError) as e:
+            lp._sort_workspace(pairs, groups)
+        assert "lp_moe_sort" in str(e.value)
