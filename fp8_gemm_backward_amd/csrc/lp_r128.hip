@@ -327,7 +327,8 @@ __global__ __launch_bounds__(kTileThreads) void r128_tile(TileArgs a) {
 
 // Results larger than a quarter of the 256 MB cache are stored past the caches: 4096
 // tokens to 8 experts each, 7168 wide, read x (59 MB, each row k times) faster from a
-// cache that 470 MB of codes do not wash through, 117 us in all (150).
+// cache that 470 MB of codes do not wash through, 117 us in all (150); to 8 of 1024 experts,
+// whose short runs go by fours (below), 267 (292), and 2048 of them to 4 of 256 57 (66).
 constexpr int64_t kCacheBytes = (int64_t)64 << 20;
 
 // Rows that come from elsewhere: row r is row order[r] / k of src, times
@@ -395,7 +396,7 @@ __global__ __launch_bounds__(kTileThreads) void r128_mapped(TileArgs a, RowMap m
 // (64); also lost where the tiles do not fill the GPU (1034 of 176 to 2 of 131: 4.7 and 5.0).
 constexpr int kShortThreads = 128, kShortTiles = kTileThreads / kShortThreads, kShortRows = kRunLen / kShortTiles;
 
-template <bool kWeighted>
+template <bool kWeighted, bool kStream>
 __global__ __launch_bounds__(kTileThreads) void r128_mapped_short(TileArgs a, RowMap map, FastDiv by_four) {
   __shared__ TileLds sh[kShortTiles];
   const int rb = fdiv(blockIdx.x, by_four), ct0 = (blockIdx.x - rb * by_four.d) * kShortTiles;
@@ -406,13 +407,13 @@ __global__ __launch_bounds__(kTileThreads) void r128_mapped_short(TileArgs a, Ro
   if (r1 - r0 <= kShortRows) {
     const int part = __builtin_amdgcn_readfirstlane(threadIdx.x / kShortThreads);
     mapped_values<kWeighted, kShortThreads>(a, map, ct0 + part, r0, r1, v);
-    quant_tile<true, true, false, false, kShortThreads>(a, sh[part], v, 0, rb, ct0 + part, r0, r1);
+    quant_tile<true, true, false, kStream, kShortThreads>(a, sh[part], v, 0, rb, ct0 + part, r0, r1);
     return;
   }
 #pragma unroll 1
   for (int i = 0; i < kShortTiles && ct0 + i < (int)a.col_tiles.d; ++i) {
     mapped_values<kWeighted, kTileThreads>(a, map, ct0 + i, r0, r1, v);
-    quant_tile<true, true, false, false>(a, sh[i], v, 0, rb, ct0 + i, r0, r1);
+    quant_tile<true, true, false, kStream>(a, sh[i], v, 0, rb, ct0 + i, r0, r1);
   }
 }
 
@@ -455,15 +456,17 @@ hipError_t launch_moe_gather_quant(const void* x, int64_t tokens, int64_t topk, 
                    (int32_t)rows, (int32_t)cols, make_fastdiv((uint32_t)ct), make_fastdiv((uint32_t)rt)};
   const RowMap map{order, weights, make_fastdiv((uint32_t)topk), (uint32_t)rows};
   const dim3 grid((uint32_t)(rt * ct)), block(kTileThreads);
+  const bool past = 2 * rows * cols > kCacheBytes;
   if (rows <= 32 * groups && rt * ct >= 1024) {
     const int64_t fours = (ct + kShortTiles - 1) / kShortTiles;
     const FastDiv by_four = make_fastdiv((uint32_t)fours);
     const dim3 few((uint32_t)(rt * fours));
-    if (weights != nullptr) r128_mapped_short<true><<<few, block, 0, stream>>>(a, map, by_four);
-    else r128_mapped_short<false><<<few, block, 0, stream>>>(a, map, by_four);
+    if (weights != nullptr)
+      past ? r128_mapped_short<true, true><<<few, block, 0, stream>>>(a, map, by_four) : r128_mapped_short<true, false><<<few, block, 0, stream>>>(a, map, by_four);
+    else
+      past ? r128_mapped_short<false, true><<<few, block, 0, stream>>>(a, map, by_four) : r128_mapped_short<false, false><<<few, block, 0, stream>>>(a, map, by_four);
     return hipGetLastError();
   }
-  const bool past = 2 * rows * cols > kCacheBytes;
   if (weights != nullptr)
     past ? r128_mapped<true, true><<<grid, block, 0, stream>>>(a, map) : r128_mapped<true, false><<<grid, block, 0, stream>>>(a, map);
   else
