@@ -26,3 +26,86 @@ def test_gather_quant_of_short_runs_past_the_caches(lp, T, k, E, H, weighted):
         q.codes.fill_(99)
     same_runs(lp, lp.lp_moe_gather_quant(x, order, off, k, weights=w, out=out), lp.lp_r128_quant_dual(plain, off), off, H)
     assert all((q.codes[0, n:] == 99).all() for q in out)
+
+
+# ---------------------------------------------------------------- gate
+
+U32, U16 = 2.0 ** -24, 2.0 ** -8                         # half a step of fp32 and bf16
+GATES = [(40, 12, 12), (33, 16, 5), (50, 64, 64), (21, 100, 33), (17, 203, 64), (30, 256, 64), (20, 256, 8), (9, 300, 64), (9, 1001, 64), (8, 1024, 64)]
+
+
+def far_logits(T, E, k, dtype, seed):
+    """fp32 [T, E] from a peak down to 70 below it, most of the k largest far below; differences of two are exact in fp32
+    (multiples of 2^-10, of 1/4 in bf16's range)."""
+    rng = np.random.default_rng(seed)
+    unit = 4 if dtype == torch.bfloat16 else 1024
+    v = -40 * unit + rng.integers(0, 8 * unit, (T, E))
+    v[:, rng.permutation(E)[:k]] = rng.integers(-40 * unit, 30 * unit, (T, k))
+    v[np.arange(T), rng.integers(0, E, T)] = 30 * unit
+    return (v / unit).astype(np.float32)
+
+
+def adds(E):
+    """Roundings on the way of a term into the sum over a row: those of a lane, then those over the lanes."""
+    return (max(1, -(-E // 16)) - 1 + 4) if E <= 256 else -(-E // 64) - 1 + 6
+
+
+def weights_bound(l, k, E, renorm):
+    """Relative error of a weight e^d / sum, in fp32.
+
+    The exponential: the instruction's 2^t is within a step (2 U32); t = d log2 e is split into a rounded part and its
+    residual, whose own rounding is 2^-24 of half a step of t < 128 and whose square term is below 2^-36: nothing; one
+    rounding puts the residual in.  3 U32, and below 0.01 of them for the rest.
+    The sum: of the chosen, the same exponentials, at most 4 a lane, then 6 times over the lanes.  Of all, exponentials
+    without the residual: half a step of t times ln 2, |d| U32, and |d| 2^-26 0.9 for what log2 e has beyond fp32; in the
+    sum the mean of |d| by weight counts.  The quotient is correctly rounded."""
+    if renorm:
+        return (3.01 + 3.01 + 9 + 1) * U32
+    d = np.abs(l - l.max(1, keepdims=True))
+    p = np.exp(-d)
+    mean = (p * d).sum(1, keepdims=True) / p.sum(1, keepdims=True)
+    return (3.01 + 2 + 1.23 * mean + adds(E) + 1) * U32
+
+
+def exact_weights(l, e, renorm):
+    """fp64 [T, k] of the chosen e, and the softmax [T, E]."""
+    p = np.exp(l.astype(np.float64) - l.max(1, keepdims=True))
+    top = np.take_along_axis(p, e, 1)
+    return top / (top if renorm else p).sum(1, keepdims=True), p / p.sum(1, keepdims=True)
+
+
+@pytest.mark.parametrize("T,E,k", GATES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_gate_far_below_the_peak(lp, T, E, k, dtype, renorm):
+    lv = far_logits(T, E, k, dtype, E + k)
+    l = torch.from_numpy(lv).cuda().to(dtype)
+    assert np.array_equal(l.float().cpu().numpy(), lv)
+    w, e = lp.lp_moe_gate(l, k, renorm=renorm)
+    eh = e.cpu().numpy().astype(np.int64)
+    assert np.array_equal(eh, np.argsort(-lv, 1, kind="stable")[:, :k])
+    want, p = exact_weights(lv, eh, renorm)
+    wh = w.cpu().numpy().astype(np.float64)
+    assert (np.abs(wh - want) <= weights_bound(lv, k, E, renorm) * want).all(), (np.abs(wh / want - 1) / U32).max()
+
+    # The gradient, from the weights as they are: sum w g in fp32 (a product's rounding, at most 3 sums a lane and 6 over
+    # the lanes: 10 U32), then w (g - that) by two roundings; or p times it, p = e^d / sum by its own exponentials (those
+    # of bf16 logits without the residual), a quotient and a product, and w g added to it.
+    g = np.random.default_rng(k).standard_normal((T, k)).astype(np.float32)
+    got = lp.lp_moe_gate_bwd(torch.from_numpy(g).cuda(), l, w, e, renorm=renorm).float().cpu().numpy().astype(np.float64)
+    g = g.astype(np.float64)
+    inner, size = (wh * g).sum(1, keepdims=True), (wh * np.abs(g)).sum(1, keepdims=True)
+    ref, tol = np.zeros((T, E)), np.zeros((T, E))
+    if renorm:
+        np.put_along_axis(ref, eh, wh * (g - inner), 1)
+        np.put_along_axis(tol, eh, wh * (10 * size + 2.01 * (np.abs(g) + size)) * U32, 1)
+    else:
+        own = np.zeros((T, E))
+        np.put_along_axis(own, eh, wh * g, 1)
+        d = np.abs(lv.astype(np.float64) - lv.max(1, keepdims=True))
+        one = 3.01 if dtype == torch.float32 else 2 + 1.23 * d
+        mean = (p * one).sum(1, keepdims=True) if dtype == torch.bfloat16 else 3.01
+        ref = own - p * inner
+        tol = (p * size * (one + mean + adds(E) + 10 + 2) + np.abs(own) + np.abs(ref)) * U32 * 1.01
+    tol += np.abs(ref) * (U16 if dtype == torch.bfloat16 else 0)
+    assert (np.abs(got - ref) <= tol).all(), (np.abs(got - ref) / np.maximum(tol, 1e-300)).max()
