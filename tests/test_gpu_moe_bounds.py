@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from test_gpu_moe import same_runs
+from test_gpu_train_streams import busy, segment_stream  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +110,89 @@ def test_gate_far_below_the_peak(lp, T, E, k, dtype, renorm):
         tol = (p * size * (one + mean + adds(E) + 10 + 2) + np.abs(own) + np.abs(ref)) * U32 * 1.01
     tol += np.abs(ref) * (U16 if dtype == torch.bfloat16 else 0)
     assert (np.abs(got - ref) <= tol).all(), (np.abs(got - ref) / np.maximum(tol, 1e-300)).max()
+
+
+# ---------------------------------------------------------------- 4-bit forward
+
+# (M, N, K, groups; 0: dense) that go to the 256 x 256 tiles.
+LARGE_TILES = [(1348, 8832, 96, 0), (3100, 6000, 32, 2)]
+
+
+def rows_and_weight(lp, fmt, M, N, K, G, seed):
+    """x, a weight over `G` groups (0: one, dense) and its bf16 values in fp64."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    run, n = 32 if fmt == "mxfp4" else 16, max(G, 1)
+    codes = torch.randint(0, 256, (n, N, K // 2), generator=g, dtype=torch.uint8, device="cuda")
+    scales = torch.randint(*((118, 126) if fmt == "mxfp4" else (0x20, 0x40)), (n, N, K // run), generator=g, dtype=torch.uint8, device="cuda")
+    w = lp.QTensor(fmt, codes, scales, torch.tensor([0.03], device="cuda") if fmt == "nvfp4" else None, shape=(n, N, K))
+    return torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_(generator=g), w
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K,G", LARGE_TILES)
+@pytest.mark.parametrize("raw", [False, True])
+def test_large_tiles_on_another_stream(lp, busy, fmt, M, N, K, G, raw):  # noqa: F811
+    """The bits of the current stream, whose late writes to freed memory miss the result; the result is that stream's."""
+    x, w = rows_and_weight(lp, fmt, M, N, K, G, M)
+    off = torch.tensor([M // 3, M - 7], dtype=torch.int32, device="cuda")
+
+    def call(stream):
+        return lp.lp_grouped_fwd_w4(x, w, off, stream=stream) if G else lp.lp_linear_fwd_w4(x, w, stream=stream)
+    n = M - 7 if G else M
+    want = call(None)[:n].clone()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    mine = [torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    busy()
+    for t in mine:
+        t.fill_(7)
+    del mine, t
+    got = call(s.cuda_stream if raw else s)
+    s.synchronize()
+    assert segment_stream(got.data_ptr()) == s.cuda_stream
+    torch.cuda.synchronize()
+    assert torch.equal(got[:n], want)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K,G", LARGE_TILES)
+def test_captured_large_tiles(lp, fmt, M, N, K, G):
+    x, w = rows_and_weight(lp, fmt, M, N, K, G, M)
+    off = torch.tensor([M // 3, M - 7], dtype=torch.int32, device="cuda")
+    y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+
+    def call(y):
+        return lp.lp_grouped_fwd_w4(x, w, off, y=y) if G else lp.lp_linear_fwd_w4(x, w, y=y)
+    call(torch.empty_like(y))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(y)
+    for k in range(3):
+        x.copy_(torch.roll(x, 1, 0))
+        off.copy_(torch.tensor([M // (2 + k), M - 7], dtype=torch.int32))
+        graph.replay()
+        want = call(torch.full_like(y, 7.0))
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), k
+
+
+def close(y, x, w):
+    """y against x w^T in fp64, w the bf16 values that the kernel multiplies: exact products, K sums in fp32 in any order (a
+    step each, should the matrix core cut off rather than round) and one rounding to bf16."""
+    want, size = x.double() @ w.double().T, x.double().abs() @ w.double().abs().T
+    off = (y.double() - want).abs()
+    assert (off <= U16 * want.abs() + x.shape[1] * 2 * U32 * size).all()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K,G", LARGE_TILES)
+def test_large_tiles_against_the_decoded_weight(lp, fmt, M, N, K, G):
+    x, w = rows_and_weight(lp, fmt, M, N, K, G, N)
+    if not G:
+        close(lp.lp_linear_fwd_w4(x, w), x, lp.lp_dequant(w)[0])
+        return
+    off = torch.tensor([M // 3, M], dtype=torch.int32, device="cuda")
+    y, dec = lp.lp_grouped_fwd_w4(x, w, off), lp.lp_dequant(w)
+    close(y[:M // 3], x[:M // 3], dec[0])
+    close(y[M // 3:], x[M // 3:], dec[1])
