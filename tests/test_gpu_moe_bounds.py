@@ -186,6 +186,20 @@ def close(y, x, w):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_w4_weights_past_2_to_32_bytes(lp, fmt):
+    """Every group's rows, those of the last groups past 2^32 bytes of codes."""
+    G, N, K, M = 40, 16400, 14336, 57
+    x, q = rows_and_weight(lp, fmt, M, N, K, G, 5)
+    off = torch.zeros(G, dtype=torch.int32, device="cuda")
+    off[1:20], off[20:G - 1], off[G - 1] = 3, 20, M
+    y = lp.lp_grouped_fwd_w4(x, q, off)
+    for e, r in ((1, slice(0, 3)), (20, slice(3, 20)), (G - 1, slice(20, M))):
+        one = lp.QTensor(fmt, q.codes[e:e + 1], q.scales[e:e + 1], q.tensor_scale, shape=(1, N, K))
+        close(y[r], x[r], lp.lp_dequant(one)[0])
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 @pytest.mark.parametrize("M,N,K,G", LARGE_TILES)
 def test_large_tiles_against_the_decoded_weight(lp, fmt, M, N, K, G):
     x, w = rows_and_weight(lp, fmt, M, N, K, G, N)
