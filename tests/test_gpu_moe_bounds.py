@@ -4,7 +4,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import moe as O
 from test_gpu_moe import same_runs
+from test_gpu_moe_layer import Weights, f64
 from test_gpu_train_streams import busy, segment_stream  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -210,3 +212,33 @@ def test_large_tiles_against_the_decoded_weight(lp, fmt, M, N, K, G):
     y, dec = lp.lp_grouped_fwd_w4(x, w, off), lp.lp_dequant(w)
     close(y[:M // 3], x[:M // 3], dec[0])
     close(y[M // 3:], x[M // 3:], dec[1])
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("T,E,k,width,hidden", [(1, 8, 2, 256, 512), (9, 16, 4, 288, 160), (200, 8, 3, 256, 544)])
+def test_served_layer_within_its_roundings(lp, fmt, T, E, k, width, hidden):
+    """fp64 with the bf16 values that both formats' weights stand for.  h, y and the result are rounded to bf16, half a step
+    each, times |W| for h; the sums in fp32 are off by a step for each of their terms at the most.  The gate's weights: 17
+    half steps (weights_bound), and 12 more in the exponential and in the sum for rounded differences of logits within 12 of
+    one another."""
+    gen = torch.Generator(device="cuda").manual_seed(300 + T)
+    layer = Weights(lp, fmt, E, k, width, hidden, gen)
+    x = torch.randn(T, width, generator=gen, device="cuda").bfloat16()
+    out = f64(layer.forward(x))
+    logits = f64(x.float() @ layer.router.T)
+    assert np.ptp(logits, axis=1).max() < 12
+    w, chosen = O.gate(logits, k, True)
+    xv, (W1, W2) = f64(x), layer.values
+    for t in range(T):
+        want, bound = np.zeros(width), np.zeros(width)
+        for j, e in enumerate(chosen[t]):
+            h = W1[e] @ xv[t]
+            bh = width * 2 * U32 * np.abs(W1[e]) @ np.abs(xv[t])
+            bh += U16 * (np.abs(h) + bh)
+            y = W2[e] @ np.maximum(h, 0)
+            b = np.abs(W2[e]) @ bh + hidden * 2 * U32 * np.abs(W2[e]) @ (np.abs(h) + bh)
+            b += U16 * (np.abs(y) + b)
+            want += w[t, j] * y
+            bound += w[t, j] * b + (41 + 2 * k) * U32 * np.abs(w[t, j] * y)
+        bound += U16 * (np.abs(want) + bound)
+        assert (np.abs(out[t] - want) <= bound).all(), (t, (np.abs(out[t] - want) / bound).max())
