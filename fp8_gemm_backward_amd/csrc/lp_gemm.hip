@@ -443,7 +443,9 @@ hipError_t launch_fwd(const lp_qtensor& x, const lp_qtensor& w, const int32_t* o
   const int64_t ptiles = offsets ? (x.rows / BP + groups) : (x.rows + BP - 1) / BP;
   prm.ntiles = (int32_t)(ptiles * prm.nq);
   if (mx) return fwd_mx(prm, x.fmt == LP_MXFP4, stream);
-  const bool split = BQ == Big::BQ && tile_split(prm);
+  // (An MXFP4 weight comes here for contractions too short for a split: with longer
+  // ones 128 x 256 rows and columns a workgroup, lp_gemm_w4.hip, always take less.)
+  const bool split = BQ == Big::BQ && w.fmt != LP_MXFP4 && tile_split(prm);
   const hipError_t e = fwd_dec(prm, x.fmt, w.fmt, false, stream);
   if (e != hipSuccess || !split) return e;
   return fwd_dec(tail_params(prm), x.fmt, w.fmt, true, stream);

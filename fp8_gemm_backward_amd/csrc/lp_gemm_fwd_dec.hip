@@ -25,9 +25,8 @@ hipError_t fwd_dec(const Params& prm, int fmt_x, int fmt_w, bool narrow, hipStre
   if (fmt_x == LP_BF16 && fmt_w == LP_FP8_B128)
     return narrow ? run<Narrow, BF16, -1, FP8_B128, -1, false, true>(prm, s)
                   : run<Big, BF16, -1, FP8_B128, -1, false, true>(prm, s);
-  if (fmt_x == LP_BF16 && fmt_w == LP_MXFP4)
-    return narrow ? run<Narrow, BF16, -1, MXFP4, -1, false, true>(prm, s)
-                  : run<Big, BF16, -1, MXFP4, -1, false, true>(prm, s);
+  if (fmt_x == LP_BF16 && fmt_w == LP_MXFP4)       // (never narrow)
+    return run<Big, BF16, -1, MXFP4, -1, false, true>(prm, s);
   if (fmt_x == LP_BF16 && fmt_w == LP_NVFP4)
     return narrow ? run<Narrow, BF16, -1, NVFP4, -1, false, true>(prm, s)
                   : run<Big, BF16, -1, NVFP4, -1, false, true>(prm, s);

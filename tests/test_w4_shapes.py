@@ -52,3 +52,14 @@ def test_the_listed_sizes_take_every_shape_and_the_large_tiles(rule):
 def test_the_large_tiles_of_another_stream_are_the_large_tiles(rule):
     shape, _ = rule
     assert all(shape(*s) == -1 for s in B.LARGE_TILES)
+
+
+def test_the_large_tiles_take_no_contraction_that_a_grouped_call_splits(rule):
+    """An MXFP4 weight's tiles have no second launch: contractions of 64 slabs of 64 and more never go to them."""
+    shape, _ = rule
+    sizes = [1, 100, 255, 256, 257, 1000, 4096, 9001, 32768, 100000]
+    for M in sizes:
+        for N in [16, 256, 272, 1040, 4096, 8208, 65536]:
+            for K in (4096, 4128, 14336, 1 << 17):
+                for G in (0, 1, 2, 5, 64, 1024):
+                    assert shape(M, N, K, G) >= 0, (M, N, K, G)
