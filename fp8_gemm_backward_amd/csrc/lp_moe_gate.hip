@@ -13,10 +13,12 @@
 // logit.  No logit is read twice; sums are fp32.  The gradient adds the chosen
 // slots' parts to the softmax's in LDS.
 //
-// 32768 tokens of 256 bf16 logits, 8 chosen: 9.9 us, the gradient 9.4 (17 and 36 MB,
-// 3.3 and 7.0 us of copying; with a wave to a token and the lane's best logit sought
-// anew for each choice 32.4 and 22.0).  Bound by instructions, 600 a wave of four
-// tokens, and by the launch.
+// 32768 tokens of 256 bf16 logits, 8 chosen: 10.2 us, the gradient 9.4 after it, 11.3 of
+// logits out of the caches (17 and 36 MB, 3.3 and 7.0 us of copying; with a wave to a
+// token and the lane's best logit sought anew for each choice 32.4 and 22.0).  fp32:
+// 17.0 and 16.4 (34 and 69 MB, 6.7 and 13.5 us).  The choice is bound by instructions,
+// 554 a wave of four bf16 tokens: 7.6 us of every SIMD, 73% of the kernel's time with its
+// launch and its last waves; the gradient by its bytes.
 #include <math.h>
 
 #include <type_traits>

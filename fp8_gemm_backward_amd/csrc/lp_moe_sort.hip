@@ -11,7 +11,7 @@
 // integers, whose order changes nothing), or, where the pairs are many, takes
 // from two launches that count every chunk's experts and add them up.
 //
-// 96 pairs 3.4 us, 32768 of 64 experts 7.1, 2^20 15: a launch and a chain of
+// 96 pairs 3.3 us, 32768 of 64 experts 7.5, 2^20 15: a launch and a chain of
 // dependent steps, then the counting of all pairs by every workgroup.
 #include "lp_device.hpp"
 #include "lp_internal.hpp"

@@ -327,7 +327,7 @@ __global__ __launch_bounds__(kTileThreads) void r128_tile(TileArgs a) {
 
 // Results larger than a quarter of the 256 MB cache are stored past the caches: 4096
 // tokens to 8 experts each, 7168 wide, read x (59 MB, each row k times) faster from a
-// cache that 470 MB of codes do not wash through, 117 us in all (150); to 8 of 1024 experts,
+// cache that 470 MB of codes do not wash through, 120 us in all (150); to 8 of 1024 experts,
 // whose short runs go by fours (below), 267 (292), and 2048 of them to 4 of 256 57 (66).
 constexpr int64_t kCacheBytes = (int64_t)64 << 20;
 

@@ -492,7 +492,8 @@ lp_status lp_grouped_dx_deferred(const lp_qtensor* grad_out, const void* w, int6
  *      scale); K % 32 == 0;
  *    - x LP_BF16 and w LP_BF16 or LP_FP8_B128 (K % 16 == 0) or LP_NVFP4
  *      (scale_axis -1, K % 32 == 0): an NVFP4 x decoded first with
- *      lp_dequant, which saves the per-tile decode of x;
+ *      lp_dequant, which saves the per-tile decode of x (a call of few
+ *      rows by a 4-bit weight, MXFP4 too: lp_linear_fwd_w4, lp_moe.h);
  *    - x LP_FP8_R128 (scale_axis -1) and w LP_FP8_B128 (K % 16 == 0), on the
  *      FP8 MFMA: sums of each 128 of K, times the two scales' fp32 product,
  *      added in fp32, as lp_linear_bwd says of these operands.
