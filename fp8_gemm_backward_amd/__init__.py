@@ -922,11 +922,16 @@ def lp_moe_gather_quant(x: torch.Tensor, order: torch.Tensor, offsets: torch.Ten
                QTensor("fp8_r128", new((1, M, H), dtype=torch.uint8), new((1, runs, H), dtype=torch.float32), None,
                        (1, M, H), -2, G))
     else:
-        for q, n, axis, name in zip(out, (nb * M, runs * H), (-1, -2), ("out[0]", "out[1]")):
+        for q, axis, n, length, codes, scales in ((out[0], -1, nb * M, M, "out[0] codes", "out[0] scales"),
+                                                  (out[1], -2, runs * H, H, "out[1] codes", "out[1] scales")):
             if q.fmt != "fp8_r128" or tuple(q.shape) != (1, M, H) or q.axis != axis:
-                raise ValueError(f"{name}: not the tensor this call writes")
-            _device(q.codes, f"{name} codes", M * H, torch.uint8)
-            _device(q.scales, f"{name} scales", 4 * n, torch.float32)
+                raise ValueError(f"{codes}: not of the tensor this call writes")
+            _device(q.codes, codes, M * H, torch.uint8)
+            _device(q.scales, scales, 4 * n, torch.float32)
+            if M * H and q.codes.numel() != M * H:
+                _width(q.codes, codes, H)
+            if M * H and q.scales.numel() != n:
+                _width(q.scales, scales, length)
         out[1].run_groups = G
     cols, toks = out
     _check(lib.lp_moe_gather_quant(x.data_ptr(), T, topk, H, order.data_ptr(), None if weights is None else weights.data_ptr(),

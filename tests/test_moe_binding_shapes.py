@@ -101,3 +101,17 @@ def test_the_sorts_workspace_is_refused_as_the_sort_is():
         with pytest.raises(lp.LpError) as e:
             lp._sort_workspace(pairs, groups)
         assert "lp_moe_sort" in str(e.value)
+
+
+def test_the_fp8_copies_have_their_width(made):  # noqa: F811
+    """Codes and scales whose rows are longer: refused; as many in another shape, or more rows: taken."""
+    order, off, x = t(2000, dtype=I), t(3, dtype=I), t(1000, 144)
+
+    def copies(codes=(1, 2000, 144), cols=(1, 2, 2000), rows=(1, 18, 144), codes_rows=(1, 2000, 144)):
+        return (lp.QTensor("fp8_r128", t(*codes, dtype=torch.uint8), t(*cols, dtype=F), None, (1, 2000, 144), -1),
+                lp.QTensor("fp8_r128", t(*codes_rows, dtype=torch.uint8), t(*rows, dtype=F), None, (1, 2000, 144), -2))
+    for kw in ({}, dict(codes=(2000 * 144,)), dict(cols=(1, 4000)), dict(rows=(1, 19, 144)), dict(cols=(3, 2000))):
+        lp.lp_moe_gather_quant(x, order, off, 2, out=copies(**kw))
+    made.clear()
+    refused(made, *(lambda kw=kw: lp.lp_moe_gather_quant(x, order, off, 2, out=copies(**kw))
+                    for kw in (dict(codes=(1, 2000, 160)), dict(codes_rows=(1, 2000, 160)), dict(cols=(1, 2, 2048)), dict(rows=(1, 18, 160)))))
