@@ -784,6 +784,19 @@ def _gate_dtype(logits: torch.Tensor) -> int:
     return _GATE_DTYPE[logits.dtype]
 
 
+@functools.lru_cache(maxsize=1)
+def _several_gpus() -> bool:
+    return torch.cuda.device_count() > 1
+
+
+def _here(t: torch.Tensor, name: str, stream) -> None:
+    """Refuses a tensor of another GPU than the current one, on whose stream a call without a stream runs."""
+    if stream is None and _several_gpus():
+        at = t.device.index
+        if at is not None and at != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, not on the current device")
+
+
 def _width(t: torch.Tensor, name: str, cols: int) -> None:
     """Refuses a tensor of several dimensions whose rows are not `cols` long."""
     if t.dim() > 1 and t.shape[-1] != cols:
@@ -809,6 +822,7 @@ def lp_moe_gate(logits: torch.Tensor, topk: int, renorm: bool = True, weights: O
     T, E = logits.shape
     dtype = _gate_dtype(logits)
     _device(logits, "logits", T * E * logits.element_size())
+    _here(logits, "logits", stream)
     if weights is not None:
         _pairs(weights, "weights", T, topk, torch.float32)
     if chosen is not None:
@@ -830,6 +844,7 @@ def lp_moe_gate_bwd(grad_weights: torch.Tensor, logits: torch.Tensor, weights: t
     k = chosen.shape[-1]
     dtype = _gate_dtype(logits)
     _device(logits, "logits", T * E * logits.element_size())
+    _here(logits, "logits", stream)
     if grad_logits is None:
         grad_logits = _new(logits, stream)((T, E), dtype=logits.dtype)
     else:
@@ -860,6 +875,7 @@ def lp_moe_sort(experts: torch.Tensor, groups: int, stream=None) -> tuple:
     the last offset)."""
     n = experts.numel()
     _device(experts, "experts", 4 * n, torch.int32)
+    _here(experts, "experts", stream)
     nbytes = _sort_workspace(n, groups)
     # (one allocation for the three: 1 us less of the host's 10)
     offsets, order, rows = _new(experts, stream)((groups + 2 * n,), dtype=torch.int32).split_with_sizes((groups, n, n))
@@ -880,10 +896,11 @@ def _tokens(rows: torch.Tensor) -> tuple:
 
 def _matrix(t: torch.Tensor, name: str, rows: int, cols: Optional[int] = None) -> int:
     """Columns of a bf16 matrix [rows, columns] (cols: that many)."""
-    if t.dim() != 2 or t.shape[0] != rows or cols not in (None, t.shape[1]):
-        raise ValueError(f"{name} must be [{rows}, {'columns' if cols is None else cols}], not {tuple(t.shape)}")
-    _device(t, name, 2 * rows * t.shape[1], torch.bfloat16)
-    return t.shape[1]
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or cols not in (None, shape[1]):
+        raise ValueError(f"{name} must be [{rows}, {'columns' if cols is None else cols}], not {tuple(shape)}")
+    _device(t, name, 2 * rows * shape[1], torch.bfloat16)
+    return shape[1]
 
 
 def lp_moe_gather(x: torch.Tensor, rows: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -891,6 +908,7 @@ def lp_moe_gather(x: torch.Tensor, rows: torch.Tensor, out: Optional[torch.Tenso
     them).  Rows of no pair are left as they were in `out`."""
     T, k = _tokens(rows)
     H = _matrix(x, "x", T)
+    _here(x, "x", stream)
     if out is None:
         out = _new(x, stream)((T * k, H), dtype=torch.bfloat16)
     else:
@@ -908,6 +926,7 @@ def lp_moe_gather_quant(x: torch.Tensor, order: torch.Tensor, offsets: torch.Ten
     T = x.shape[0]
     M, G = T * topk, offsets.numel()
     H = _matrix(x, "x", T)
+    _here(x, "x", stream)
     if G == 0:
         raise LpError(2, "offsets of no group")
     _device(order, "order", 4 * M, torch.int32)
@@ -947,6 +966,7 @@ def lp_moe_combine(y: torch.Tensor, rows: torch.Tensor, weights: Optional[torch.
     token without a row."""
     T, k = _tokens(rows)
     H = _matrix(y, "y", T * k)
+    _here(y, "y", stream)
     if weights is not None:
         _pairs(weights, "weights", T, k, torch.float32)
     if out is None:
@@ -967,6 +987,7 @@ def lp_moe_combine_bwd(grad: torch.Tensor, y: Optional[torch.Tensor], rows: torc
     `grad_y`; y is read for grad_weights only."""
     T, k = _tokens(rows)
     H = _matrix(grad, "grad", T)
+    _here(grad, "grad", stream)
     if weights is not None:
         _pairs(weights, "weights", T, k, torch.float32)
     if need_dy:
@@ -992,14 +1013,16 @@ def lp_moe_combine_bwd(grad: torch.Tensor, y: Optional[torch.Tensor], rows: torc
 
 def _fwd_w4(x: torch.Tensor, w: QTensor, offsets: Optional[torch.Tensor], y: Optional[torch.Tensor], stream):
     M, K = x.shape
-    if K != w.cols:
-        raise ValueError(f"x has {K} columns, the weight {w.cols}")
+    _, N, cols = w.shape
+    if K != cols:
+        raise ValueError(f"x has {K} columns, the weight {cols}")
     _device(x, "x", 2 * M * K, torch.bfloat16)
+    _here(x, "x", stream)
     if y is None:
-        y = _new(x, stream)((M, w.rows), dtype=torch.bfloat16)
+        y = _new(x, stream)((M, N), dtype=torch.bfloat16)
     else:
-        _device(y, "y", 2 * M * w.rows, torch.bfloat16)
-        _width(y, "y", w.rows)
+        _device(y, "y", 2 * M * N, torch.bfloat16)
+        _width(y, "y", N)
     wc = w.c()
     if offsets is None:
         _check(lib.lp_linear_fwd_w4(x.data_ptr(), M, ctypes.byref(wc), y.data_ptr(), _stream(stream)), "lp_linear_fwd_w4")

@@ -115,3 +115,27 @@ def test_the_fp8_copies_have_their_width(made):  # noqa: F811
     made.clear()
     refused(made, *(lambda kw=kw: lp.lp_moe_gather_quant(x, order, off, 2, out=copies(**kw))
                     for kw in (dict(codes=(1, 2000, 160)), dict(codes_rows=(1, 2000, 160)), dict(cols=(1, 2, 2048)), dict(rows=(1, 18, 160)))))
+
+
+def test_tensors_of_another_gpu_than_the_current_one_are_refused(made, monkeypatch):  # noqa: F811
+    """Without a stream a call runs on the current GPU, which cannot reach the other one's memory.  (A given stream says
+    where it runs.)"""
+    monkeypatch.setattr(lp, "_several_gpus", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+    def on(at, x):
+        x.device = torch.device("cuda", at)
+        return x
+    q = lp.QTensor("mxfp4", t(2, 48, 32, dtype=torch.uint8), t(2, 48, 2, dtype=torch.uint8), None, (2, 48, 64))
+    one = lp.QTensor("mxfp4", t(1, 48, 32, dtype=torch.uint8), t(1, 48, 2, dtype=torch.uint8), None, (1, 48, 64))
+    rows, w, e, order, off = t(7, 2, dtype=I), t(7, 2, dtype=F), t(7, 2, dtype=I), t(14, dtype=I), t(2, dtype=I)
+    calls = [lambda at, s: lp.lp_moe_gate(on(at, t(7, 12)), 2, stream=s), lambda at, s: lp.lp_moe_gate_bwd(w, on(at, t(7, 12)), w, e, stream=s),
+             lambda at, s: lp.lp_moe_sort(on(at, t(7, 2, dtype=I)), 4, stream=s), lambda at, s: lp.lp_moe_gather(on(at, t(7, 32)), rows, stream=s),
+             lambda at, s: lp.lp_moe_gather_quant(on(at, t(7, 144)), order, off, 2, stream=s),
+             lambda at, s: lp.lp_moe_combine(on(at, t(14, 32)), rows, w, stream=s),
+             lambda at, s: lp.lp_moe_combine_bwd(on(at, t(7, 32)), t(14, 32), rows, w, stream=s),
+             lambda at, s: lp.lp_linear_fwd_w4(on(at, t(3, 64)), one, stream=s), lambda at, s: lp.lp_grouped_fwd_w4(on(at, t(3, 64)), q, off, stream=s)]
+    for call in calls:
+        call(0, None), call(1, 0x500)
+    made.clear()
+    refused(made, *(lambda c=c: c(1, None) for c in calls))
