@@ -12,7 +12,8 @@
 // backward decodes it, and contracted on the bf16 MFMA with fp32 sums.  A
 // bf16 x with an NVFP4 weight is the same product with x decoded
 // beforehand (lp_dequant), once rather than in every tile that reads it; an
-// MXFP4 weight takes the same way in the 4-bit forward of many rows.
+// MXFP4 weight takes the same way in the 4-bit forward of many rows and a short
+// contraction.
 #include "lp_gemm_kernel.hpp"
 
 namespace lp {
